@@ -16,6 +16,12 @@ launch, and `allreduce_rmsnorm_add_quant` folds a tensor-parallel all-reduce
 module holds its two-shot row partition and gather. The norms and the quant
 also take fp16 activations.
 
+The products that read these rows, over ragged groups: `group_rows` (a
+router's or the adapters' ids -> rows in group order), `grouped_gemm` (the
+experts' matrix products, on rows of the three FP8 formats or 16-bit ones),
+`combine_rows` (each token's weighted sum) and `lora_add` (the low-rank
+adapters of many requests beside a shared projection).
+
 Formats: MXFP8 (E4M3 + one E8M0 scale per 1x32 block), 1x128 block FP8 with
 fp32 scales, and per-token FP8 with an [M,1] fp32 scale.
 
@@ -28,4 +34,7 @@ from .binding import (  # noqa: F401
     SgqError, library, library_path, rmsnorm_add_quant, swiglu_quant, status_string,
     rmsnorm_add, swiglu, quantize_fp8, rmsnorm_dual_quant, NormSeg, F_FP16, set_sm_budget,
     allreduce_rmsnorm_add_quant, MAX_RANKS,
+)
+from .grouped import (  # noqa: F401
+    GEMM_FORMATS, MAX_GROUPS, MAX_RANK, combine_rows, gemm_scale_shapes, group_rows, grouped_gemm, lora_add,
 )

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "sgq.h"
+#include "sgq_host.h"
 #include "sgq_launch.h"
 
 namespace sgq {
@@ -118,22 +119,43 @@ cudaError_t ensure_dynamic_smem(const void* kernel, int device, int bytes) {
     return e;
 }
 
+namespace {
+// The current device and its multiprocessor count. The count is queried
+// once per device and cached; on the call path the one runtime call left is
+// cudaGetDevice, which reads the calling thread's current device.
+// sgq_set_sm_budget() replaces the count used for planning.
+constexpr int kMaxDevices = 64;
+std::atomic<int> sm_cache[kMaxDevices];
+std::atomic<int> sm_budget{0};
+}  // namespace
+
+Device current_device() {
+    Device d = {-1, 0};
+    if (cudaGetDevice(&d.id) != cudaSuccess) return {-1, 0};
+    const int budget = sm_budget.load(std::memory_order_relaxed);
+    if (budget > 0) {
+        d.sms = budget;
+        return d;
+    }
+    if (d.id < 0 || d.id >= kMaxDevices) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d.id) == cudaSuccess) d.sms = n;
+        return d;
+    }
+    int n = sm_cache[d.id].load(std::memory_order_relaxed);
+    if (n <= 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d.id) != cudaSuccess) n = 0;
+        if (n > 0) sm_cache[d.id].store(n, std::memory_order_relaxed);
+    }
+    d.sms = n;
+    return d;
+}
+
 }  // namespace sgq
 
+using namespace sgq;
+
 namespace {
-
-// Largest element count of one tensor: its byte sizes (at most 4 bytes an
-// element) stay far inside size_t and the kernels' 64-bit offsets.
-constexpr int64_t kMaxElements = int64_t(1) << 56;
-
-bool aligned(const void* p, uintptr_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Half-open byte ranges [a, a+na) and [b, b+nb) intersect (null or empty never does).
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 
 int group_of(int fmt) { return fmt == SGQ_FMT_MXFP8 ? 32 : fmt == SGQ_FMT_FP8_BLOCK128 ? 128 : 8; }
 
@@ -154,8 +176,6 @@ float bf16_value(uint32_t b) {
 }
 
 constexpr uint32_t kLayoutFlags = SGQ_F_SCALE_SWIZZLED | SGQ_F_SCALE_COL_MAJOR;
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // The scale layout the flags select for format fmt at [M, W], and its size
 // in bytes. False when a layout flag does not belong to the format.
@@ -183,41 +203,6 @@ bool scale_geometry(int fmt, uint32_t flags, int64_t M, int64_t W, sgq::ScaleOut
     return true;
 }
 
-// The current device and its multiprocessor count. The count is queried
-// once per device and cached; on the call path the one runtime call left is
-// cudaGetDevice, which reads the calling thread's current device.
-// sgq_set_sm_budget() replaces the count used for planning.
-constexpr int kMaxDevices = 64;
-std::atomic<int> sm_cache[kMaxDevices];
-std::atomic<int> sm_budget{0};
-
-struct Device {
-    int id;
-    int sms;
-};
-
-Device current_device() {
-    Device d = {-1, 0};
-    if (cudaGetDevice(&d.id) != cudaSuccess) return {-1, 0};
-    const int budget = sm_budget.load(std::memory_order_relaxed);
-    if (budget > 0) {
-        d.sms = budget;
-        return d;
-    }
-    if (d.id < 0 || d.id >= kMaxDevices) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d.id) == cudaSuccess) d.sms = n;
-        return d;
-    }
-    int n = sm_cache[d.id].load(std::memory_order_relaxed);
-    if (n <= 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d.id) != cudaSuccess) n = 0;
-        if (n > 0) sm_cache[d.id].store(n, std::memory_order_relaxed);
-    }
-    d.sms = n;
-    return d;
-}
-
 // Plan the rows of a launch whose scale layout covers so.Ms >= M rows: the
 // grid covers the layout's padding rows too, and the exact-fit kernels only
 // run when there are none.
@@ -241,9 +226,6 @@ bool plan_norm(int64_t M, int64_t Ms, int H, int sms, sgq::Plan* p) {
     }
     return p->grid <= 0x7FFFFFFF;
 }
-
-// Dynamic shared memory one CTA may use (227 KB on sm_100-class parts).
-constexpr int kMaxDynamicSmem = 227 * 1024;
 
 // Chunks (8 columns) one CTA of the row engine covers: kMaxTPR threads with
 // kMaxNV chunks each, 16384 columns.
@@ -282,26 +264,6 @@ int wide_segments(int nch, int gch, int min_seg, int* segc) {
     const int sc = (int)round_up((nch + s - 1) / s, gch);
     *segc = sc;
     return (nch + sc - 1) / sc;
-}
-
-struct Span {
-    const void* p;
-    size_t n;
-};
-
-// True when any two of the spans intersect.
-bool any_overlap(const Span* s, int k) {
-    for (int i = 0; i < k; ++i)
-        for (int j = i + 1; j < k; ++j)
-            if (overlap(s[i].p, s[i].n, s[j].p, s[j].n)) return true;
-    return false;
-}
-
-
-int launched(cudaError_t e) {
-    if (e == cudaSuccess) return SGQ_OK;
-    sgq::note_launch_error(e);
-    return SGQ_ERR_LAUNCH;
 }
 
 // Column segments a row for a norm launch over `rows` rows (the grid's second

@@ -1,0 +1,101 @@
+// sgq_group.cuh -- arguments and host-side launchers of the ragged-group
+// kernels (group_rows, grouped_gemm, combine_rows, lora_add), one translation
+// unit per operation.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sgq_host.h"
+
+namespace sgq {
+
+constexpr int FMT_16BIT = 3;         // beside Fmt: 16-bit rows and weights
+constexpr int kMaxGroups = 1024;
+constexpr int kMaxRank = 128;
+
+struct GroupRowsArgs {
+    const void* ids;
+    int32_t* offsets;
+    int32_t* rows;
+    int32_t* slots;      // or null
+    uint32_t n;          // T * k ids
+    uint32_t k;
+    int groups;
+    int wide;            // 64-bit ids
+};
+
+struct GroupGemmArgs {
+    const void* x;
+    const void* xs;
+    const void* w;
+    const void* ws;
+    const int32_t* offsets;
+    const int32_t* rows;  // or null
+    uint16_t* out;
+    int64_t x_rows;
+    int S, groups, N, K;
+};
+
+struct CombineArgs {
+    const uint16_t* y;
+    const int32_t* slots;
+    const float* weights;  // or null
+    uint16_t* out;
+    int64_t T;
+    int64_t S;
+    int k;
+    int N;
+    int nblk;              // column blocks a token
+};
+
+struct LoraArgs {
+    const uint16_t* x;
+    const uint16_t* a;
+    const uint16_t* b;
+    const float* scaling;  // or null
+    const int32_t* offsets;
+    const int32_t* rows;   // or null
+    const int32_t* slots;  // null exactly when rows is
+    uint16_t* y;
+    float* v;              // workspace [S, R]
+    int64_t T;
+    int S, groups, R, K, N;
+};
+
+cudaError_t launch_group_rows(const Device& dev, const GroupRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream);
+cudaError_t launch_combine(int dt, const Device& dev, const CombineArgs& a, cudaStream_t stream);
+cudaError_t launch_lora(int dt, const Device& dev, const LoraArgs& a, cudaStream_t stream);
+
+// Launch k on `stream` with programmatic stream serialisation (as launch_pdl,
+// for any grid), in clusters of `cluster` CTAs along x.
+template <typename Args>
+cudaError_t launch_grid(void (*k)(const Args), dim3 grid, int threads, int smem, int cluster, int device,
+                        const Args& a, cudaStream_t stream) {
+    if (smem > 40 * 1024) {
+        const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(k), device, smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+// The range of slots of group g, held inside [0, S] and ascending: what the
+// kernels take for offsets[g], offsets[g + 1] whatever they hold.
+__device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+}  // namespace sgq

@@ -1,0 +1,255 @@
+"""Products over ragged groups of rows (include/sgq_group.h), with the same
+entry-point names: the routing of an expert layer, its grouped matrix products
+on FP8 or 16-bit rows, its weighted sum, and the low-rank adapters of many
+requests beside a shared projection.
+
+Argument marshalling only, as in `binding`: checks, output allocation, the
+call. Every tensor of a call has to be on one CUDA device; the call runs on
+that device and on `stream` (default: its current stream), and what it
+allocates belongs to that stream.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from .binding import F_FP16, FORMATS, GROUP, SgqError, _act_dtype, _check, _ptr, _want, library
+
+MAX_GROUPS = 1024
+MAX_RANK = 128
+#: grouped_gemm's formats: the FP8 formats, and "none" for 16-bit rows and weights.
+GEMM_FORMATS = {**FORMATS, "none": 3}
+_bound = None
+
+
+def _lib() -> C.CDLL:
+    global _bound
+    L = library()
+    if _bound is not L:
+        vp, i64, u32 = C.c_void_p, C.c_int64, C.c_uint32
+        L.group_rows.restype = C.c_int
+        L.group_rows.argtypes = [C.c_int, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.grouped_gemm.restype = C.c_int
+        L.grouped_gemm.argtypes = [C.c_int, u32, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.combine_rows.restype = C.c_int
+        L.combine_rows.argtypes = [u32, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.lora_add.restype = C.c_int
+        L.lora_add.argtypes = [u32, i64, i64, i64, i64, i64, i64] + [vp] * 10
+        L.sgq_lora_workspace_bytes.restype = i64
+        L.sgq_lora_workspace_bytes.argtypes = [i64, i64]
+        _bound = L
+    return L
+
+
+def _dims(t: torch.Tensor, n: int, name: str):
+    if t.dim() != n:
+        raise SgqError(f"{name}: expected {n} dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+class _On:
+    """The device and stream of a call: every tensor on one CUDA device, made
+    the current one for the call, with `stream` its current stream."""
+
+    def __init__(self, stream, **tensors):
+        there = {n: t for n, t in tensors.items() if t is not None}
+        first = next(iter(there.values())).device
+        for n, t in there.items():
+            if t.device != first:
+                raise SgqError(f"{n}: on {t.device}, the other tensors on {first}")
+        if first.type != "cuda":
+            raise SgqError(f"expected CUDA tensors, got {first}")
+        if stream is not None and stream.device != first:
+            raise SgqError(f"stream: of {stream.device}, the tensors on {first}")
+        self.device = first
+        self.stream = torch.cuda.current_stream(first) if stream is None else stream
+        self._same = stream is None and torch.cuda.current_device() == first.index
+        self.handle = C.c_void_p(self.stream.cuda_stream)
+
+    def __enter__(self):
+        if not self._same:
+            self._ctx = torch.cuda.stream(self.stream)     # makes the stream's device current, too
+            self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        if not self._same:
+            self._ctx.__exit__(*e)
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def group_rows(ids: torch.Tensor, groups: int, *, offsets_out: torch.Tensor | None = None,
+               rows_out: torch.Tensor | None = None, slots_out: torch.Tensor | None = None, stream=None):
+    """Rows in group order (one kernel launch): the routing of an expert layer,
+    or the adapters of a batch's requests.
+
+    ids [T, k] (or [T], k = 1) int32 or int64: the group of each of a token's
+    k rows; an id outside [0, groups) takes no slot. Returns (offsets
+    [groups+1], rows [T*k], slots like ids), all int32: group g has the slots
+    offsets[g] to offsets[g+1]; slot s holds token rows[s] (-1 behind the last
+    group); ids[t, j] has slot slots[t, j] (-1 where it has none). Ids of one
+    group keep their order.
+    """
+    if ids.dim() not in (1, 2):
+        raise SgqError(f"ids: expected [T, k] or [T], got {tuple(ids.shape)}")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise SgqError(f"ids: expected int32 or int64, got {ids.dtype}")
+    _want(ids, ids.shape, ids.dtype, "ids")
+    T, k = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    groups = int(groups)
+    if not 1 <= groups <= MAX_GROUPS or k < 1:
+        raise SgqError(f"groups: 1 to {MAX_GROUPS}, got {groups}; ids a token: at least 1, got {k}")
+    for t, shape, name in ((offsets_out, (groups + 1,), "offsets_out"), (rows_out, (T * k,), "rows_out"),
+                           (slots_out, tuple(ids.shape), "slots_out")):
+        if t is not None:
+            _want(t, shape, torch.int32, name)
+    with _On(stream, ids=ids, offsets_out=offsets_out, rows_out=rows_out, slots_out=slots_out) as on:
+        if offsets_out is None:
+            offsets_out = on.empty((groups + 1,), torch.int32)
+        if rows_out is None:
+            rows_out = on.empty((T * k,), torch.int32)
+        if slots_out is None:
+            slots_out = on.empty(tuple(ids.shape), torch.int32)
+        st = _lib().group_rows(ids.element_size(), T, k, groups, _ptr(ids), _ptr(offsets_out), _ptr(rows_out),
+                               _ptr(slots_out), on.handle)
+        _check(st, "group_rows")
+    return offsets_out, rows_out, slots_out
+
+
+def gemm_scale_shapes(fmt: str, x_rows: int, groups: int, N: int, K: int):
+    """(shape of x_scale, shape of w_scale, their dtype) of grouped_gemm; None for "none"."""
+    if fmt == "none":
+        return None, None, None
+    if fmt == "mxfp8":
+        return (x_rows, K // 32), (groups, -(-N // 128) * 128, -(-(K // 32) // 4) * 4), torch.uint8
+    if fmt == "block128":
+        return (x_rows, K // 128), (groups, -(-N // 128), K // 128), torch.float32
+    return (x_rows, 1), (groups, N), torch.float32
+
+
+def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt: str = "mxfp8",
+                 x_scale: torch.Tensor | None = None, w_scale: torch.Tensor | None = None,
+                 rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, stream=None):
+    """Matrix products grouped by ragged sets of rows (one kernel launch):
+    out[s] = x[rows[s]] @ w[g].T for the slots s of group g, summed in fp32.
+
+    x [X, K] and w [groups, N, K]: uint8 E4M3 with the scales of an FP8 format,
+    or bfloat16 / float16 with fmt="none". x_scale is what the library's
+    quantisation writes row-major; w_scale: "mxfp8" uint8 [groups, N up to 128,
+    K/32 up to 4] (each group's scales in the swizzled layout), "block128"
+    float32 [groups, ceil(N/128), K/128], "per_token" float32 [groups, N].
+    offsets [groups+1] int32; rows [S] int32 or None (slot s reads x[s], S = X).
+    A row index outside x reads zeros. Returns out [S, N] (bfloat16, float16 by
+    out_dtype or `out`, x's type with "none"); slots of no group keep what out
+    held.
+    """
+    if fmt not in GEMM_FORMATS:
+        raise SgqError(f"unknown format {fmt!r}")
+    X, K = _dims(x, 2, "x")
+    groups, N, _ = _dims(w, 3, "w")
+    dt = _act_dtype(x, "x") if fmt == "none" else torch.uint8
+    _want(x, (X, K), dt, "x")
+    _want(w, (groups, N, K), dt, "w")
+    unit = {"per_token": 16, "none": 8, **GROUP}[fmt]
+    if K < 1 or K % unit or N < 1 or N % 8:
+        raise SgqError(f"{fmt}: K has to be a multiple of {unit} and N of 8, got K = {K}, N = {N}", 2)
+    xshape, wshape, sdt = gemm_scale_shapes(fmt, X, groups, N, K)
+    for t, shape, name in ((x_scale, xshape, "x_scale"), (w_scale, wshape, "w_scale")):
+        if (t is None) != (shape is None):
+            raise SgqError(f"{name}: {'missing' if t is None else 'of no use'} with format {fmt!r}")
+        if t is not None:
+            _want(t, shape, sdt, name)
+    _want(offsets, (groups + 1,), torch.int32, "offsets")
+    S = X
+    if rows is not None:
+        S, = _dims(rows, 1, "rows")
+        _want(rows, (S,), torch.int32, "rows")
+    odt = out_dtype or (out.dtype if out is not None else dt if fmt == "none" else torch.bfloat16)
+    if odt not in (torch.bfloat16, torch.float16) or (fmt == "none" and odt != dt):
+        raise SgqError(f"out: {odt} does not go with x of {x.dtype}")
+    if out is not None:
+        _want(out, (S, N), odt, "out")
+    with _On(stream, x=x, w=w, offsets=offsets, x_scale=x_scale, w_scale=w_scale, rows=rows, out=out) as on:
+        if out is None:
+            out = on.empty((S, N), odt)
+        st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, _ptr(x),
+                                 _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(offsets), _ptr(rows), _ptr(out), on.handle)
+        _check(st, "grouped_gemm")
+    return out
+
+
+def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, *,
+                 out: torch.Tensor | None = None, stream=None):
+    """The weighted sum of each token's rows (one kernel launch):
+    out[t] = sum_j weights[t, j] * y[slots[t, j]], in fp32 in order of j.
+
+    y [S, N] bfloat16 or float16; slots [T, k] int32 (a slot outside [0, S)
+    adds nothing); weights [T, k] float32 or None (ones). Returns out [T, N] of
+    y's type.
+    """
+    S, N = _dims(y, 2, "y")
+    T, k = _dims(slots, 2, "slots")
+    dt = _act_dtype(y, "y")
+    _want(y, (S, N), dt, "y")
+    _want(slots, (T, k), torch.int32, "slots")
+    if weights is not None:
+        _want(weights, (T, k), torch.float32, "weights")
+    if out is not None:
+        _want(out, (T, N), dt, "out")
+    with _On(stream, y=y, slots=slots, weights=weights, out=out) as on:
+        if out is None:
+            out = on.empty((T, N), dt)
+        st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, _ptr(y), _ptr(slots), _ptr(weights),
+                                 _ptr(out), on.handle)
+        _check(st, "combine_rows")
+    return out
+
+
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, offsets: torch.Tensor, *,
+             rows: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+             scaling: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The low-rank adapters of many requests, added in place to a shared
+    projection's output (two kernel launches): for slot s of adapter g with
+    t = rows[s], y[t] += scaling[g] * (x[t] @ a[g].T) @ b[g].T, in fp32.
+
+    x [T, K], a [groups, R, K], b [groups, N, R] and y [T, N]: all bfloat16 or
+    all float16. offsets, rows, slots: group_rows of the requests' adapters
+    ([T] ids, -1 for none); rows and slots both None where the rows of x
+    already are in adapter order (slot s is row s). scaling [groups] float32 or
+    None (ones). workspace: float32 [S, R] or None (allocated). Rows without an
+    adapter stay as they are. Returns y.
+    """
+    T, K = _dims(x, 2, "x")
+    groups, R, _ = _dims(a, 3, "a")
+    _, N = _dims(y, 2, "y")
+    dt = _act_dtype(x, "x")
+    _want(x, (T, K), dt, "x")
+    _want(a, (groups, R, K), dt, "a")
+    _want(b, (groups, N, R), dt, "b")
+    _want(y, (T, N), dt, "y")
+    _want(offsets, (groups + 1,), torch.int32, "offsets")
+    if (rows is None) != (slots is None):
+        raise SgqError("rows and slots go together")
+    S = T
+    if rows is not None:
+        S, = _dims(rows, 1, "rows")
+        _want(rows, (S,), torch.int32, "rows")
+        if slots.dim() == 2 and slots.shape[1] == 1:
+            slots = slots.view(-1) if slots.is_contiguous() else slots
+        _want(slots, (T,), torch.int32, "slots")
+    if scaling is not None:
+        _want(scaling, (groups,), torch.float32, "scaling")
+    if workspace is not None:
+        _want(workspace, (S, R), torch.float32, "workspace")
+    with _On(stream, x=x, a=a, b=b, y=y, offsets=offsets, rows=rows, slots=slots, scaling=scaling,
+             workspace=workspace) as on:
+        if workspace is None:
+            workspace = on.empty((S, R), torch.float32)
+        st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, _ptr(x), _ptr(a), _ptr(b),
+                             _ptr(scaling), _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(y), _ptr(workspace), on.handle)
+        _check(st, "lora_add")
+    return y
