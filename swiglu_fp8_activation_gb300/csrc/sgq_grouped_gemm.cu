@@ -1,121 +1,575 @@
 // sgq_grouped_gemm.cu -- matrix products grouped by ragged sets of rows
-// (include/sgq_group.h, grouped_gemm).
+// (include/sgq_group.h, grouped_gemm), on the fifth-generation tensor cores.
 //
-// A first form, right for every case: 64 x 64 output tiles, operands widened
-// to fp32 in shared memory, fp32 multiply-adds, each 32 products scaled.
+// One tile is 128 channels (rows of w[g]) by up to BN slots of group g; the
+// weights are the M side of the product and the slots its N side, so that a
+// group of one row costs an N of 16 and not an M of 128, and the weights,
+// which bound a decode step, stream through the same 16 KB tiles at every
+// size. out^T = w . x^T: a lane of the accumulator is a channel, a column a
+// slot. Both operands are K-major rows of 128 bytes (128 FP8 or 64 16-bit
+// values, one "chunk" of K) in 128-byte swizzle.
+//
+// A CTA keeps its tensor memory and walks over tiles (persistent, one CTA a
+// multiprocessor). The tiles follow from the offsets on the device: every CTA
+// scans them once (running maximum, which holds them in order, then the sum
+// of tiles). Warps:
+//   0     copies: the weights' tile by TMA, their scales as 512-byte tiles
+//         (MXFP8), the slots' rows by TMA, as a box or, where rows gives
+//         them, four at a time by row index
+//   1     the products (one thread), four instructions of 32 bytes of K a chunk
+//   2, 3  the slots' scales (MXFP8 and 1x128): row-major in memory, written
+//         into the operand's layout in shared memory
+//   4-7   the epilogue, one quarter of the channels each
+// Two accumulators in tensor memory let the epilogue of one tile run under
+// the products of the next. With 1x128 scales, which fp32 holds and no block
+// scale of the tensor core can, every chunk is its own accumulator and the
+// epilogue warps sum the chunks in registers, scaled.
+#include <stddef.h>
+
 #include "sgq_group.cuh"
+#include "sgq_tc.cuh"
 
 namespace sgq {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 32;
+constexpr int kThreads = 256;
+constexpr int kM = 128;            // channels a tile
+constexpr int kChunk = 128;        // bytes of K a chunk
+constexpr int kScaleThreads = 64;
+constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
 
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(h) : "r"(c));
-    return f16x2_to_f32x2(h).x;
-}
+struct alignas(128) GemmParams {
+    CUtensorMap mw;                // w as bytes [groups][N][K], box 128 x 128 rows
+    CUtensorMap mx;                // x as bytes [x_rows][K], box 128 x BN rows, or x 1 for row indices
+    GroupGemmArgs a;
+    int n_tiles;                   // tiles of 128 channels
+    int chunks;                    // chunks of K
+    int kbytes;                    // bytes of a row
+    int f16;                       // out (and 16-bit operands) are fp16
+    int xs_align;                  // 16, 4 or 1: alignment of every 4-byte (4 chunks: 16-byte) piece of x_scale
+};
 
-template <int DT>
-__device__ __forceinline__ float value16(uint16_t v) {
-    return DT == DT_BF16 ? __uint_as_float((uint32_t)v << 16) : f16x2_to_f32x2(v).x;
-}
+template <int FMT, int BN>
+struct Cfg {
+    static constexpr bool kMx = FMT == FMT_MX, kB128 = FMT == FMT_B128;
+    static constexpr int kW = kM * kChunk, kX = BN * kChunk;
+    static constexpr int kHalves = (BN + 127) / 128;              // 128-slot pieces of the slots' scales
+    static constexpr int kSw = kMx ? 512 : 0;                     // weights' scales of a chunk
+    static constexpr int kSx = kMx ? 512 * kHalves : kB128 ? 4 * BN : 0;
+    static constexpr int kStage = kW + kX + kSw + kSx;
+    static constexpr int kFixed = 1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + 4 * 4 * BN + 1024;
+    static constexpr int kFit = (kMaxDynamicSmem - kFixed) / kStage;
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
+    static constexpr int kAccCols = 2 * BN;
+    static constexpr int kScaleCols = kMx ? kScaleBufs * 4 * (1 + kHalves) : 0;
+    static constexpr int kNeed = kAccCols + kScaleCols;
+    static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr int kSmem = kFixed + kStages * kStage;
+    static_assert(kNeed <= 512 && kStages >= 3, "tile too large");
+};
 
-// Stored value k of row r of x, and of channel n of group g; 0 outside.
-template <int FMT, int DT>
-__device__ __forceinline__ float x_value(const GroupGemmArgs& a, int64_t r, int k) {
-    if (r < 0 || r >= a.x_rows || k >= a.K) return 0.0f;
-    const int64_t i = r * a.K + k;
-    return FMT == FMT_16BIT ? value16<DT>(static_cast<const uint16_t*>(a.x)[i]) : e4m3_value(static_cast<const uint8_t*>(a.x)[i]);
-}
-
-template <int FMT, int DT>
-__device__ __forceinline__ float w_value(const GroupGemmArgs& a, int g, int n, int k) {
-    if (n >= a.N || k >= a.K) return 0.0f;
-    const int64_t i = ((int64_t)g * a.N + n) * a.K + k;
-    return FMT == FMT_16BIT ? value16<DT>(static_cast<const uint16_t*>(a.w)[i]) : e4m3_value(static_cast<const uint8_t*>(a.w)[i]);
-}
-
-// The scale of the 32 products from k on (one MX block, part of a 128-block).
-template <int FMT>
-__device__ __forceinline__ float scale_of(const GroupGemmArgs& a, int64_t r, int g, int n, int k) {
-    if (FMT == FMT_16BIT || r < 0 || r >= a.x_rows || n >= a.N) return 1.0f;
-    if (FMT == FMT_MX) {
-        const int64_t Np = (a.N + 127) / 128 * 128, Kp = (a.K / 32 + 3) / 4;
-        const int b = k / 32;
-        const int64_t tile = ((int64_t)g * Np + n / 128 * 128) * Kp * 4 + (int64_t)(b / 4) * 512;
-        const int cw = static_cast<const uint8_t*>(a.ws)[tile + (n % 32) * 16 + (n / 32 % 4) * 4 + b % 4];
-        const int cx = static_cast<const uint8_t*>(a.xs)[r * (a.K / 32) + b];
-        return ldexpf(1.0f, cw + cx - 254);
+// Warp-wide and block-wide inclusive scan (maximum or sum) of one value a thread.
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int v, int* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = MAX ? max(v, o) : v + o;
     }
-    if (FMT == FMT_B128)
-        return static_cast<const float*>(a.xs)[r * (a.K / 128) + k / 128] *
-               static_cast<const float*>(a.ws)[((int64_t)g * ((a.N + 127) / 128) + n / 128) * (a.K / 128) + k / 128];
-    return static_cast<const float*>(a.xs)[r] * static_cast<const float*>(a.ws)[(int64_t)g * a.N + n];
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before = MAX ? max(before, part[w]) : before + part[w];
+    __syncthreads();
+    return MAX ? max(v, before) : v + before;
 }
 
-template <int FMT, int DT>
-__global__ void __launch_bounds__(256) grouped_gemm_kernel(const GroupGemmArgs a) {
-    __shared__ float xs[kStep][kTile + 1], ws[kStep][kTile + 1];
+// lo[g] = the held offset of group g (g = 0 .. G), first[g] = tiles of bn
+// slots in the groups before g. All threads of the block.
+__device__ void scan_groups(const int32_t* offsets, int G, int S, int bn, int* lo, int* first, int* part) {
+    const int per = (G + kThreads) / kThreads;                    // of G + 1 offsets, per a thread
+    const int b = threadIdx.x * per, e = min(b + per, G + 1);
+    int run = 0;
+    for (int g = b; g < e; ++g) {
+        run = max(run, held(offsets[g], 0, S));
+        lo[g] = run;
+    }
+    const int upto = block_scan<true>(run, part);                 // includes this thread's own
+    // earlier threads' maximum: the scan without this thread's values
+    if (threadIdx.x < kThreads) first[threadIdx.x] = upto;
+    __syncthreads();
+    const int before = threadIdx.x ? first[threadIdx.x - 1] : 0;
+    __syncthreads();
+    for (int g = b; g < e; ++g) lo[g] = max(lo[g], before);
+    __syncthreads();
+    int sum = 0;
+    for (int g = b; g < e && g < G; ++g) sum += (lo[g + 1] - lo[g] + bn - 1) / bn;
+    int at = block_scan<false>(sum, part) - sum;
+    for (int g = b; g < e; ++g) {
+        first[g] = at;
+        if (g < G) at += (lo[g + 1] - lo[g] + bn - 1) / bn;
+    }
+    __syncthreads();
+}
+
+// The tiles of one CTA in order: slots [s0, s0 + m) of group g, channels from n0 on.
+struct Walk {
+    const int* lo;
+    const int* first;
+    int G, n_tiles, bn;
+    int64_t tile, end;
+    int g, s0, m, n0;
+
+    __device__ Walk(const int* lo_, const int* first_, int G_, int n_tiles_, int bn_)
+        : lo(lo_), first(first_), G(G_), n_tiles(n_tiles_), bn(bn_), tile(blockIdx.x), end((int64_t)first_[G_] * n_tiles_), g(0) {}
+    __device__ bool next() {
+        if (tile >= end) return false;
+        const int q = (int)(tile / n_tiles);
+        while (first[g + 1] <= q) ++g;
+        s0 = lo[g] + (q - first[g]) * bn;
+        m = min(bn, lo[g + 1] - s0);
+        n0 = (int)(tile % n_tiles) * kM;
+        tile += gridDim.x;
+        return true;
+    }
+};
+
+__device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using C = Cfg<FMT, BN>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
+    uint8_t* tiles = smem;
+    uint8_t* scales = smem + kStages * (C::kW + C::kX);
+    int* lo = reinterpret_cast<int*>(scales + kStages * (C::kSw + C::kSx));
+    int* first = lo + kMaxGroups + 8;
+    float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4 warps][BN]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(xbuf + 4 * BN);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    int* part = reinterpret_cast<int*>(misc + 4);                        // 8 ints
+    volatile uint32_t* stop = misc + 1;
+    const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
+    const uint32_t tiles_at = tc::smem_addr(tiles), scales_at = tc::smem_addr(scales);
+
+    const GroupGemmArgs& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunks = p.chunks;
+    const bool gather = a.rows != nullptr;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::bar_init(full + 8 * i, 1 + (C::kMx || C::kB128 ? kScaleThreads : 0));
+            tc::bar_init(empty + 8 * i, C::kB128 ? 5 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(acc_full + 8 * i, 1);
+            tc::bar_init(acc_empty + 8 * i, 4);
+        }
+        tc::bar_init(done, 1);
+        tc::fence_barrier_init();
+        *stop = 0;
+        tc::prefetch_map(&p.mw);
+        tc::prefetch_map(&p.mx);
+    }
+    if (warp == 2) tc::tmem_alloc(tc::smem_addr(misc), C::kCols);
     pdl_wait();
     pdl_trigger();
-    // the group and first slot of this CTA's tile
-    int tile = blockIdx.x, g = 0, lo = 0, hi = 0, prev = 0;
-    for (;; ++g) {
-        if (g == a.groups) return;
-        lo = held(a.offsets[g], prev, a.S);
-        hi = held(a.offsets[g + 1], lo, a.S);
-        prev = lo;
-        const int tiles = (hi - lo + kTile - 1) / kTile;
-        if (tile < tiles) break;
-        tile -= tiles;
+    scan_groups(a.offsets, a.groups, a.S, BN, lo, first, part);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = misc[0];
+    Walk walk(lo, first, a.groups, p.n_tiles, BN);
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- copies
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        int64_t issued = 0;
+        const int scale_tiles = C::kMx ? (p.kbytes / 32 + 3) / 4 : 0;
+        while (ok && walk.next()) {
+            constexpr int kQ = (BN / 4 + 31) / 32;                       // groups of four rows a lane
+            const int quads = (walk.m + 3) / 4;
+            int r[kQ][4];
+            if (gather) {
+#pragma unroll
+                for (int i = 0; i < kQ; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = (i * 32 + lane) * 4 + j;
+                        const int v = c < walk.m ? a.rows[walk.s0 + c] : 0;
+                        r[i][j] = v >= 0 && v < a.x_rows ? v : 0;
+                    }
+            }
+            const uint8_t* ws = static_cast<const uint8_t*>(a.ws) +
+                                ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * scale_tiles * 512;
+            const uint32_t bytes = C::kW + C::kSw + (gather ? quads * 512 : C::kX);
+            for (int kc = 0; kc < chunks; ++kc) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
+                if (!ok) break;
+                const uint32_t w_at = tiles_at + st * (C::kW + C::kX), x_at = w_at + C::kW;
+                const uint32_t bar = full + 8 * st;
+                if (lane == 0) {
+                    tc::bar_arrive_expect(bar, bytes);
+                    tc::load_3d(w_at, &p.mw, bar, kc * kChunk, walk.n0, walk.g);
+                    if (C::kMx) tc::load_bulk(scales_at + st * (C::kSw + C::kSx), ws + (int64_t)kc * 512, 512, bar);
+                    if (!gather) tc::load_2d(x_at, &p.mx, bar, kc * kChunk, walk.s0);
+                }
+                if (gather) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kQ; ++i)
+                        if (i * 32 + lane < quads)
+                            tc::load_gather4(x_at + (i * 32 + lane) * 512, &p.mx, bar, kc * kChunk, r[i][0], r[i][1], r[i][2],
+                                             r[i][3]);
+                }
+                ++issued;
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            // gave up: wait (a while) for the copies in flight before the block's memory goes
+            uint32_t never = 0;
+            for (int i = 0; i < kStages && i < issued; ++i) {
+                if (--st < 0) {
+                    st = kStages - 1;
+                    ph ^= 1;
+                }
+                tc::bar_wait(full + 8 * st, ph, &never, 1 << 27);
+                never = 0;
+            }
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------- products
+        if (lane == 0) {
+            int st = 0, use = 0;
+            uint32_t ph = 0, chunk_no = 0;
+            bool ok = true;
+            while (ok && walk.next()) {
+                const uint32_t n = (uint32_t)(walk.m + 15) & ~15u;
+                uint32_t idesc;
+                if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kM >> 7) << 27);
+                else idesc = (1u << 4) | ((n >> 3) << 17) | ((kM >> 4) << 24);
+                if (FMT == FMT_16BIT && !p.f16) idesc |= (1u << 7) | (1u << 10);
+                const int left = p.kbytes - (chunks - 1) * kChunk;
+                const int last_steps = (left + 31) / 32;
+                for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
+                    const int buf = use & 1;
+                    if (C::kB128 || kc == 0) {
+                        ok = tc::bar_wait(acc_empty + 8 * buf, ((use >> 1) & 1) ^ 1, stop);
+                        if (!ok) break;
+                    }
+                    ok = tc::bar_wait(full + 8 * st, ph, stop);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t w_at = tiles_at + st * (C::kW + C::kX);
+                    const uint64_t dw = tc::desc_sw128(w_at), dx = tc::desc_sw128(w_at + C::kW);
+                    const uint32_t d = tmem + buf * BN;
+                    const uint32_t sw = tmem + C::kAccCols + (chunk_no % kScaleBufs) * 4 * (1 + C::kHalves), sx = sw + 4;
+                    if (C::kMx) {
+                        const uint32_t s_at = scales_at + st * (C::kSw + C::kSx);
+                        tc::copy_scales(sw, tc::desc_rows16(s_at));
+#pragma unroll
+                        for (int h = 0; h < C::kHalves; ++h) tc::copy_scales(sx + 4 * h, tc::desc_rows16(s_at + 512 + 512 * h));
+                    }
+                    const int steps = kc == chunks - 1 ? last_steps : 4;
+                    for (int k = 0; k < steps; ++k) {
+                        const uint32_t add = k > 0 || (!C::kB128 && kc > 0);
+                        if (C::kMx) tc::mma_mx8(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
+                        else if (FMT == FMT_16BIT) tc::mma_f16(d, dw + 2 * k, dx + 2 * k, idesc, add);
+                        else tc::mma_f8(d, dw + 2 * k, dx + 2 * k, idesc, add);
+                    }
+                    tc::commit(empty + 8 * st);
+                    if (C::kB128 || kc == chunks - 1) {
+                        tc::commit(acc_full + 8 * buf);
+                        ++use;
+                    }
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                uint32_t never = 0;
+                tc::commit(done);
+                tc::bar_wait(done, 0, &never, 1 << 27);
+            }
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------- scales of the slots
+        if (C::kMx || C::kB128) {
+            constexpr int kRows = (BN + kScaleThreads - 1) / kScaleThreads;
+            const int u = tid - 64;
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const int64_t row_bytes = C::kMx ? p.kbytes / 32 : (int64_t)chunks * 4;
+            while (ok && walk.next()) {
+                const uint8_t* src[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const int c = u + i * kScaleThreads;
+                    int64_t r = c < walk.m ? (gather ? a.rows[walk.s0 + c] : walk.s0 + c) : -1;
+                    src[i] = r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.xs) + r * row_bytes : nullptr;
+                }
+                const float* ws = C::kB128 ? static_cast<const float*>(a.ws) +
+                                                 ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * chunks
+                                           : nullptr;
+                // four chunks' scales a row at a time, the next four in flight
+                uint32_t cur[kRows][4], nxt[kRows][4];
+                auto fetch = [&](uint32_t (&v)[kRows][4], int kc) {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[i][q] = 0;
+                        if (!src[i]) continue;
+                        const uint8_t* s = src[i] + (int64_t)kc * 4;
+                        if (p.xs_align == 16) {
+                            const uint4 t = *reinterpret_cast<const uint4*>(s);
+                            v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+                        } else if (p.xs_align == 4) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (kc + q < chunks) v[i][q] = reinterpret_cast<const uint32_t*>(s)[q];
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                if (kc * 4 + q < row_bytes) v[i][q / 4] |= (uint32_t)s[q] << (8 * (q % 4));
+                        }
+                    }
+                };
+                fetch(cur, 0);
+                for (int kc0 = 0; ok && kc0 < chunks; kc0 += 4) {
+                    if (kc0 + 4 < chunks) fetch(nxt, kc0 + 4);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (kc0 + q >= chunks) break;
+                        const float w = C::kB128 ? ws[kc0 + q] : 0.0f;
+                        ok = tc::bar_wait(empty + 8 * st, ph ^ 1, stop);
+                        if (!ok) break;
+                        uint8_t* dst = scales + st * (C::kSw + C::kSx) + C::kSw;
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i) {
+                            const int c = u + i * kScaleThreads;
+                            if (c < BN) {
+                                if (C::kMx)
+                                    *reinterpret_cast<uint32_t*>(dst + (c >> 7) * 512 + (c & 31) * 16 + ((c >> 5) & 3) * 4) = cur[i][q];
+                                else
+                                    *reinterpret_cast<float*>(dst + 4 * c) = __uint_as_float(cur[i][q]) * w;
+                            }
+                        }
+                        tc::fence_async_smem();
+                        tc::bar_arrive(full + 8 * st);
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) cur[i][q] = nxt[i][q];
+                }
+            }
+        }
+    } else {
+        // -------------------------------------------------------- epilogue
+        const int quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)quarter << 21;                  // first lane of the quarter, in the address
+        float* xrow = xbuf + quarter * BN;
+        int use = 0, st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            const int n = walk.n0 + quarter * 32 + lane;
+            const int m = walk.m;
+            uint32_t there[BN / 32];
+            float wn = 1.0f;
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) {
+                const int c = i * 32 + lane;
+                int64_t r = c < m ? walk.s0 + c : -1;
+                if (gather && c < m) r = a.rows[r];
+                const bool valid = r >= 0 && r < a.x_rows;
+                there[i] = __ballot_sync(0xFFFFFFFFu, valid);
+                if (FMT == FMT_PT) xrow[c] = valid ? static_cast<const float*>(a.xs)[r] : 0.0f;
+            }
+            if (FMT == FMT_PT && n < a.N) wn = static_cast<const float*>(a.ws)[(int64_t)walk.g * a.N + n];
+            __syncwarp();
+            uint16_t* out = a.out + (int64_t)walk.s0 * a.N + n;
+            // columns c0 .. c0 + 31 of the tile: rounded once and stored, channel by channel
+            auto store = [&](int c0, uint32_t valid, const float (&v)[32]) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float r = (valid >> c) & 1 ? v[c] : 0.0f;
+                    const uint32_t b = p.f16 ? f32x2_to_f16x2(r, 0.0f) : f32x2_to_bf16x2(r, 0.0f);
+                    if (c0 + c < m && n < a.N) out[(int64_t)(c0 + c) * a.N] = (uint16_t)b;
+                }
+            };
+            if (C::kB128) {
+                float acc[BN];
+#pragma unroll
+                for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+                for (int kc = 0; kc < chunks; ++kc, ++use) {
+                    const int buf = use & 1;
+                    ok = tc::bar_wait(full + 8 * st, ph, stop) && tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc::fence_after();
+                    const float4* s = reinterpret_cast<const float4*>(scales + st * (C::kSw + C::kSx));
+#pragma unroll
+                    for (int c0 = 0; c0 < BN; c0 += 32) {
+                        if (c0 < m) {
+                            uint32_t v[32];
+                            tc::tmem_load32(tmem + lanes + buf * BN + c0, v);
+                            tc::tmem_load_wait(v);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 f = s[(c0 + c) / 4];
+                                acc[c0 + c] = fmaf(__uint_as_float(v[c]), f.x, acc[c0 + c]);
+                                acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y, acc[c0 + c + 1]);
+                                acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z, acc[c0 + c + 2]);
+                                acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w, acc[c0 + c + 3]);
+                            }
+                        }
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::bar_arrive(acc_empty + 8 * buf);
+                        tc::bar_arrive(empty + 8 * st);
+                    }
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c0 = 0; c0 < BN; c0 += 32) {
+                    float v[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] = acc[c0 + c];
+                    if (c0 < m) store(c0, there[c0 / 32], v);
+                }
+            } else {
+                const int buf = use & 1;
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
+                if (!ok) break;
+                ++use;
+                tc::fence_after();
+#pragma unroll
+                for (int c0 = 0; c0 < BN; c0 += 32) {
+                    if (c0 < m) {
+                        uint32_t v[32];
+                        float f[32];
+                        tc::tmem_load32(tmem + lanes + buf * BN + c0, v);
+                        tc::tmem_load_wait(v);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            f[c] = __uint_as_float(v[c]);
+                            if (FMT == FMT_PT) f[c] = f[c] * xrow[c0 + c] * wn;
+                        }
+                        store(c0, there[c0 / 32], f);
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+            }
+        }
     }
-    const int s0 = lo + tile * kTile, n0 = blockIdx.y * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-            const int r = i / kStep, k = i % kStep, s = s0 + r;
-            const int64_t row = s < hi ? (a.rows ? a.rows[s] : s) : -1;
-            xs[k][r] = x_value<FMT, DT>(a, row, k0 + k);
-            ws[k][r] = w_value<FMT, DT>(a, g, n0 + r, k0 + k);
-        }
-        __syncthreads();
-        float part[4][4] = {};
-        for (int k = 0; k < kStep; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xs[k][ty * 4 + i], ws[k][tx + 16 * j], part[i][j]);
-        for (int i = 0; i < 4; ++i) {
-            const int s = s0 + ty * 4 + i;
-            const int64_t row = s < hi ? (a.rows ? a.rows[s] : s) : -1;
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = fmaf(part[i][j], scale_of<FMT>(a, row, g, n0 + tx + 16 * j, k0), acc[i][j]);
-        }
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int s = s0 + ty * 4 + i, n = n0 + tx + 16 * j;
-            if (s < hi && n < a.N)
-                a.out[(int64_t)s * a.N + n] =
-                    (uint16_t)(DT == DT_F16 ? f32x2_to_f16x2(acc[i][j], 0.0f) : f32x2_to_bf16x2(acc[i][j], 0.0f));
-        }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 2) tc::tmem_free(tmem, C::kCols);
+    if (tid == 0 && *stop) atomicAdd(&g_gave_up, 1);
 }
 
-template <int DT>
-cudaError_t run(int fmt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream) {
-    const dim3 grid((unsigned)((a.S + kTile - 1) / kTile + a.groups), (unsigned)((a.N + kTile - 1) / kTile));
-    auto k = fmt == FMT_MX ? grouped_gemm_kernel<FMT_MX, DT>
-             : fmt == FMT_B128 ? grouped_gemm_kernel<FMT_B128, DT>
-             : fmt == FMT_PT ? grouped_gemm_kernel<FMT_PT, DT> : grouped_gemm_kernel<FMT_16BIT, DT>;
-    return launch_grid(k, grid, 256, 0, 1, dev.id, a, stream);
+// --------------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder, looked up once (no link to the driver library).
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// A byte tensor of `dims` (innermost first, rows of dims[0] bytes), box of
+// 128 bytes by `box_rows` rows, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows) {
+    const EncodeTiled f = encoder();
+    if (!f) return false;
+    cuuint64_t strides[2] = {dims[0], rank == 3 ? dims[0] * dims[1] : 0};
+    const cuuint32_t box[3] = {kChunk, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int BN>
+cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
+    using C = Cfg<FMT, BN>;
+    const GroupGemmArgs& a = p.a;
+    const cuuint64_t wd[3] = {(cuuint64_t)p.kbytes, (cuuint64_t)a.N, (cuuint64_t)a.groups};
+    // with no row of x at all nothing of it is used: any memory serves as its map
+    const cuuint64_t xd[2] = {(cuuint64_t)p.kbytes, (cuuint64_t)(a.x_rows ? a.x_rows : 1)};
+    if (!encode(&p.mw, a.w, 3, wd, kM) || !encode(&p.mx, a.x_rows ? a.x : a.w, 2, xd, a.rows ? 1 : BN))
+        return cudaErrorInvalidValue;
+    const int64_t most = ((int64_t)a.S / BN + (a.S < a.groups ? a.S : a.groups)) * p.n_tiles;   // tiles at most
+    const int64_t grid = most < dev.sms ? most : dev.sms > 0 ? dev.sms : 1;
+    return launch_grid(grouped_gemm_kernel<FMT, BN>, dim3((unsigned)(grid > 0 ? grid : 1)), kThreads, C::kSmem, 1, dev.id, p,
+                       stream);
+}
+
+template <int FMT>
+cudaError_t pick(const Device& dev, GemmParams& p, cudaStream_t stream) {
+    const int64_t mean = ((int64_t)p.a.S + p.a.groups - 1) / p.a.groups;
+    if (mean <= 24) return run<FMT, 32>(dev, p, stream);
+    if (mean <= 64) return run<FMT, 64>(dev, p, stream);
+    if (FMT == FMT_B128 || mean <= 128) return run<FMT, 128>(dev, p, stream);
+    return run<FMT, FMT == FMT_B128 ? 128 : 192>(dev, p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream) {
-    return dt == DT_F16 ? run<DT_F16>(fmt, dev, a, stream) : run<DT_BF16>(fmt, dev, a, stream);
+    GemmParams p;
+    p.a = a;
+    p.kbytes = fmt == FMT_16BIT ? 2 * a.K : a.K;
+    p.chunks = (p.kbytes + kChunk - 1) / kChunk;
+    p.n_tiles = (a.N + kM - 1) / kM;
+    p.f16 = dt == DT_F16;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.xs);
+    const int64_t row = fmt == FMT_MX ? a.K / 32 : (int64_t)p.chunks * 4;      // bytes of a row of x_scale
+    p.xs_align = at % 16 == 0 && row % 16 == 0 ? 16 : at % 4 == 0 && row % 4 == 0 ? 4 : 1;
+    switch (fmt) {
+        case FMT_MX: return pick<FMT_MX>(dev, p, stream);
+        case FMT_B128: return pick<FMT_B128>(dev, p, stream);
+        case FMT_PT: return pick<FMT_PT>(dev, p, stream);
+        default: return pick<FMT_16BIT>(dev, p, stream);
+    }
 }
 
 }  // namespace sgq
