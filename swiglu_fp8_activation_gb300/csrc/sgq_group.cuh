@@ -3,6 +3,7 @@
 // unit per operation.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -58,10 +59,19 @@ struct LoraArgs {
     const int32_t* rows;   // or null
     const int32_t* slots;  // null exactly when rows is
     uint16_t* y;
-    float* v;              // workspace [S, R]
+    void* v;               // workspace, S rows of lora_row_bytes(R)
     int64_t T;
     int S, groups, R, K, N;
 };
+
+// A byte tensor of `dims` (innermost first, rows of dims[0] bytes, a multiple
+// of 16), box of 128 bytes by `box_rows` rows, 128-byte
+// swizzle, zeros outside. False when the driver refuses it.
+bool encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows);
+
+// Bytes of a row of lora_add's workspace: two parts of R 16-bit values, then
+// the row's factor (fp32) and 12 bytes of zeros.
+__host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }
 
 cudaError_t launch_group_rows(const Device& dev, const GroupRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream);

@@ -119,7 +119,7 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
 
 int64_t sgq_lora_workspace_bytes(int64_t S, int64_t R) {
     if (S < 0 || S > kMaxRows || R < 1 || R > SGQ_MAX_RANK) return 0;
-    return S * R * 4;
+    return S * lora_row_bytes((int)R);
 }
 
 int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, int64_t K, int64_t N, const void* x,
@@ -153,7 +153,7 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
     l.rows = rows;
     l.slots = slots;
     l.y = static_cast<uint16_t*>(y);
-    l.v = static_cast<float*>(workspace);
+    l.v = workspace;
     l.T = T;
     l.S = (int)S;
     l.groups = (int)groups;

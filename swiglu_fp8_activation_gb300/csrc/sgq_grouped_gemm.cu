@@ -14,12 +14,16 @@
 // scans them once (running maximum, which holds them in order, then the sum
 // of tiles). Warps:
 //   0     copies: the weights' tile by TMA, their scales as 512-byte tiles
-//         (MXFP8), the slots' rows by TMA, as a box or, where rows gives
-//         them, four at a time by row index
+//         (MXFP8), the slots' rows as a box where they follow one another
 //   1     the products (one thread), four instructions of 32 bytes of K a chunk
 //   2, 3  the slots' scales (MXFP8 and 1x128): row-major in memory, written
 //         into the operand's layout in shared memory
-//   4-7   the epilogue, one quarter of the channels each
+//   4-7   the epilogue, one quarter of the channels each; with 1x128 scales
+//         4-11, half of the slots each
+//   last 4  with row indices: the slots' rows, gathered in 16-byte
+//         asynchronous copies into the swizzled layout. (TMA's four-row gather
+//         took 76 cycles an instruction of 512 bytes: 32768 MXFP8 rows of N =
+//         4096, K = 6144 ran in 3687 us with it.)
 // Two accumulators in tensor memory let the epilogue of one tile run under
 // the products of the next. With 1x128 scales, which fp32 holds and no block
 // scale of the tensor core can, every chunk is its own accumulator and the
@@ -27,21 +31,21 @@
 #include <stddef.h>
 
 #include "sgq_group.cuh"
+#include "sgq_ragged.cuh"
 #include "sgq_tc.cuh"
 
 namespace sgq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kGatherThreads = 128;
 constexpr int kM = 128;            // channels a tile
-constexpr int kChunk = 128;        // bytes of K a chunk
 constexpr int kScaleThreads = 64;
 constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
 
 struct alignas(128) GemmParams {
     CUtensorMap mw;                // w as bytes [groups][N][K], box 128 x 128 rows
-    CUtensorMap mx;                // x as bytes [x_rows][K], box 128 x BN rows, or x 1 for row indices
+    CUtensorMap mx;                // x as bytes [x_rows][K], box 128 x BN rows (not used with row indices)
     GroupGemmArgs a;
     int n_tiles;                   // tiles of 128 channels
     int chunks;                    // chunks of K
@@ -65,54 +69,14 @@ struct Cfg {
     static constexpr int kScaleCols = kMx ? kScaleBufs * 4 * (1 + kHalves) : 0;
     static constexpr int kNeed = kAccCols + kScaleCols;
     static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+    static constexpr int kEpiWarps = kB128 ? 8 : 4;
+    static constexpr int kGatherWarp = 4 + kEpiWarps;             // first of the four
+    static constexpr int kThreads = 32 * kGatherWarp;             // without the gather's
+    static constexpr int kEpiCols = kB128 && BN >= 64 ? BN / 2 : BN;   // slots of an epilogue warp
+    static constexpr int kBehind = kStages / 2;                   // chunks of a gather's copies in flight
     static constexpr int kSmem = kFixed + kStages * kStage;
     static_assert(kNeed <= 512 && kStages >= 3, "tile too large");
 };
-
-// Warp-wide and block-wide inclusive scan (maximum or sum) of one value a thread.
-template <bool MAX>
-__device__ __forceinline__ int block_scan(int v, int* part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (lane >= d) v = MAX ? max(v, o) : v + o;
-    }
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before = MAX ? max(before, part[w]) : before + part[w];
-    __syncthreads();
-    return MAX ? max(v, before) : v + before;
-}
-
-// lo[g] = the held offset of group g (g = 0 .. G), first[g] = tiles of bn
-// slots in the groups before g. All threads of the block.
-__device__ void scan_groups(const int32_t* offsets, int G, int S, int bn, int* lo, int* first, int* part) {
-    const int per = (G + kThreads) / kThreads;                    // of G + 1 offsets, per a thread
-    const int b = threadIdx.x * per, e = min(b + per, G + 1);
-    int run = 0;
-    for (int g = b; g < e; ++g) {
-        run = max(run, held(offsets[g], 0, S));
-        lo[g] = run;
-    }
-    const int upto = block_scan<true>(run, part);                 // includes this thread's own
-    // earlier threads' maximum: the scan without this thread's values
-    if (threadIdx.x < kThreads) first[threadIdx.x] = upto;
-    __syncthreads();
-    const int before = threadIdx.x ? first[threadIdx.x - 1] : 0;
-    __syncthreads();
-    for (int g = b; g < e; ++g) lo[g] = max(lo[g], before);
-    __syncthreads();
-    int sum = 0;
-    for (int g = b; g < e && g < G; ++g) sum += (lo[g + 1] - lo[g] + bn - 1) / bn;
-    int at = block_scan<false>(sum, part) - sum;
-    for (int g = b; g < e; ++g) {
-        first[g] = at;
-        if (g < G) at += (lo[g + 1] - lo[g] + bn - 1) / bn;
-    }
-    __syncthreads();
-}
 
 // The tiles of one CTA in order: slots [s0, s0 + m) of group g, channels from n0 on.
 struct Walk {
@@ -139,7 +103,7 @@ struct Walk {
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
 template <int FMT, int BN>
-__global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
     using C = Cfg<FMT, BN>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -151,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
     float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4 warps][BN]
     uint64_t* bars = reinterpret_cast<uint64_t*>(xbuf + 4 * BN);
     uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
-    int* part = reinterpret_cast<int*>(misc + 4);                        // 8 ints
+    int* part = reinterpret_cast<int*>(misc + 4);                        // 16 ints
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
@@ -164,12 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::bar_init(full + 8 * i, 1 + (C::kMx || C::kB128 ? kScaleThreads : 0));
-            tc::bar_init(empty + 8 * i, C::kB128 ? 5 : 1);
+            tc::bar_init(full + 8 * i, 1 + (C::kMx || C::kB128 ? kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0));
+            tc::bar_init(empty + 8 * i, C::kB128 ? 1 + C::kEpiWarps : 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(acc_full + 8 * i, 1);
-            tc::bar_init(acc_empty + 8 * i, 4);
+            tc::bar_init(acc_empty + 8 * i, C::kEpiWarps);
         }
         tc::bar_init(done, 1);
         tc::fence_barrier_init();
@@ -179,11 +143,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
     }
     if (warp == 2) tc::tmem_alloc(tc::smem_addr(misc), C::kCols);
     pdl_wait();
-    pdl_trigger();
     scan_groups(a.offsets, a.groups, a.S, BN, lo, first, part);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    // a next launch that holds tensor memory while it waits for this one may
+    // start only now that this CTA has its own
+    pdl_trigger();
     const uint32_t tmem = misc[0];
     Walk walk(lo, first, a.groups, p.n_tiles, BN);
 
@@ -195,22 +161,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
         int64_t issued = 0;
         const int scale_tiles = C::kMx ? (p.kbytes / 32 + 3) / 4 : 0;
         while (ok && walk.next()) {
-            constexpr int kQ = (BN / 4 + 31) / 32;                       // groups of four rows a lane
-            const int quads = (walk.m + 3) / 4;
-            int r[kQ][4];
-            if (gather) {
-#pragma unroll
-                for (int i = 0; i < kQ; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = (i * 32 + lane) * 4 + j;
-                        const int v = c < walk.m ? a.rows[walk.s0 + c] : 0;
-                        r[i][j] = v >= 0 && v < a.x_rows ? v : 0;
-                    }
-            }
             const uint8_t* ws = static_cast<const uint8_t*>(a.ws) +
                                 ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * scale_tiles * 512;
-            const uint32_t bytes = C::kW + C::kSw + (gather ? quads * 512 : C::kX);
+            const uint32_t bytes = C::kW + C::kSw + (gather ? 0 : C::kX);
             for (int kc = 0; kc < chunks; ++kc) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                 if (!ok) break;
@@ -221,14 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                     tc::load_3d(w_at, &p.mw, bar, kc * kChunk, walk.n0, walk.g);
                     if (C::kMx) tc::load_bulk(scales_at + st * (C::kSw + C::kSx), ws + (int64_t)kc * 512, 512, bar);
                     if (!gather) tc::load_2d(x_at, &p.mx, bar, kc * kChunk, walk.s0);
-                }
-                if (gather) {
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < kQ; ++i)
-                        if (i * 32 + lane < quads)
-                            tc::load_gather4(x_at + (i * 32 + lane) * 512, &p.mx, bar, kc * kChunk, r[i][0], r[i][1], r[i][2],
-                                             r[i][3]);
                 }
                 ++issued;
                 if (++st == kStages) {
@@ -356,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                     for (int q = 0; q < 4; ++q) {
                         if (kc0 + q >= chunks) break;
                         const float w = C::kB128 ? ws[kc0 + q] : 0.0f;
-                        ok = tc::bar_wait(empty + 8 * st, ph ^ 1, stop);
+                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                         if (!ok) break;
                         uint8_t* dst = scales + st * (C::kSw + C::kSx) + C::kSw;
 #pragma unroll
@@ -370,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                             }
                         }
                         tc::fence_async_smem();
-                        tc::bar_arrive(full + 8 * st);
+                        __syncwarp();
+                        if (lane == 0) tc::bar_arrive(full + 8 * st);
                         if (++st == kStages) {
                             st = 0;
                             ph ^= 1;
@@ -383,10 +329,58 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                 }
             }
         }
+    } else if (warp >= C::kGatherWarp) {
+        // ------------------------------------------- gathered rows of the slots
+        // thread u copies 16-byte piece u % 8 of rows u / 8 + 16 i of the chunk
+        constexpr int kRows = BN / 16;
+        const int u = tid - 32 * C::kGatherWarp, piece = u & 7;
+        int st = 0, lag_st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        int behind = 0;                                                  // chunks issued and not yet handed over
+        auto hand_over = [&]() {
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(full + 8 * lag_st);
+            if (++lag_st == kStages) lag_st = 0;
+            --behind;
+        };
+        while (ok && walk.next()) {
+            const uint8_t* src[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int c = (u >> 3) + 16 * i;
+                const int64_t r = c < walk.m ? a.rows[walk.s0 + c] : -1;
+                src[i] = r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.x) + r * p.kbytes + piece * 16 : nullptr;
+            }
+            for (int kc = 0; kc < chunks; ++kc) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
+                if (!ok) break;
+                uint8_t* dst = tiles + st * (C::kW + C::kX) + C::kW + (u >> 3) * kChunk + ((piece ^ ((u >> 3) & 7)) << 4);
+                const int k = kc * kChunk;
+                const bool in = k + piece * 16 < p.kbytes;               // zeros behind the row's end
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (src[i]) cp_async16(dst + i * 16 * kChunk, in ? src[i] + k : src[i], in ? 16 : 0);
+                cp_async_commit();
+                if (++behind > C::kBehind) {
+                    cp_async_wait<C::kBehind>();
+                    hand_over();
+                }
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        cp_async_wait<0>();
+        while (ok && behind > 0) hand_over();
     } else {
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const uint32_t lanes = (uint32_t)quarter << 21;                  // first lane of the quarter, in the address
+        const int first_c = C::kB128 && BN >= 64 ? ((warp - 4) >> 2) * C::kEpiCols : 0;   // this warp's slots of a tile
+        const bool idle = C::kB128 && BN < 64 && warp >= 8;
         float* xrow = xbuf + quarter * BN;
         int use = 0, st = 0;
         uint32_t ph = 0;
@@ -418,21 +412,21 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                 }
             };
             if (C::kB128) {
-                float acc[BN];
+                float acc[C::kEpiCols];
 #pragma unroll
-                for (int c = 0; c < BN; ++c) acc[c] = 0.0f;
+                for (int c = 0; c < C::kEpiCols; ++c) acc[c] = 0.0f;
                 for (int kc = 0; kc < chunks; ++kc, ++use) {
                     const int buf = use & 1;
                     ok = tc::bar_wait(full + 8 * st, ph, stop) && tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc::fence_after();
-                    const float4* s = reinterpret_cast<const float4*>(scales + st * (C::kSw + C::kSx));
+                    const float4* s = reinterpret_cast<const float4*>(scales + st * (C::kSw + C::kSx)) + first_c / 4;
 #pragma unroll
-                    for (int c0 = 0; c0 < BN; c0 += 32) {
-                        if (c0 < m) {
+                    for (int c0 = 0; c0 < C::kEpiCols; c0 += 32) {
+                        if (first_c + c0 < m && !idle) {
                             uint32_t v[32];
-                            tc::tmem_load32(tmem + lanes + buf * BN + c0, v);
+                            tc::tmem_load32(tmem + lanes + buf * BN + first_c + c0, v);
                             tc::tmem_load_wait(v);
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
@@ -457,11 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c0 = 0; c0 < BN; c0 += 32) {
+                for (int c0 = 0; c0 < C::kEpiCols; c0 += 32) {
                     float v[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) v[c] = acc[c0 + c];
-                    if (c0 < m) store(c0, there[c0 / 32], v);
+                    if (first_c + c0 < m && !idle) store(first_c + c0, there[(first_c + c0) / 32], v);
                 }
             } else {
                 const int buf = use & 1;
@@ -499,35 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
 
 // --------------------------------------------------------------------- host
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder, looked up once (no link to the driver library).
-EncodeTiled encoder() {
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
-// A byte tensor of `dims` (innermost first, rows of dims[0] bytes), box of
-// 128 bytes by `box_rows` rows, 128-byte swizzle, zeros outside.
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows) {
-    const EncodeTiled f = encoder();
-    if (!f) return false;
-    cuuint64_t strides[2] = {dims[0], rank == 3 ? dims[0] * dims[1] : 0};
-    const cuuint32_t box[3] = {kChunk, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
-    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int FMT, int BN>
 cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
     using C = Cfg<FMT, BN>;
@@ -535,11 +500,12 @@ cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
     const cuuint64_t wd[3] = {(cuuint64_t)p.kbytes, (cuuint64_t)a.N, (cuuint64_t)a.groups};
     // with no row of x at all nothing of it is used: any memory serves as its map
     const cuuint64_t xd[2] = {(cuuint64_t)p.kbytes, (cuuint64_t)(a.x_rows ? a.x_rows : 1)};
-    if (!encode(&p.mw, a.w, 3, wd, kM) || !encode(&p.mx, a.x_rows ? a.x : a.w, 2, xd, a.rows ? 1 : BN))
+    if (!encode_rows(&p.mw, a.w, 3, wd, kM) || !encode_rows(&p.mx, a.x_rows ? a.x : a.w, 2, xd, BN))
         return cudaErrorInvalidValue;
     const int64_t most = ((int64_t)a.S / BN + (a.S < a.groups ? a.S : a.groups)) * p.n_tiles;   // tiles at most
     const int64_t grid = most < dev.sms ? most : dev.sms > 0 ? dev.sms : 1;
-    return launch_grid(grouped_gemm_kernel<FMT, BN>, dim3((unsigned)(grid > 0 ? grid : 1)), kThreads, C::kSmem, 1, dev.id, p,
+    return launch_grid(grouped_gemm_kernel<FMT, BN>, dim3((unsigned)(grid > 0 ? grid : 1)), C::kThreads + (a.rows ? kGatherThreads : 0),
+                       C::kSmem, 1, dev.id, p,
                        stream);
 }
 

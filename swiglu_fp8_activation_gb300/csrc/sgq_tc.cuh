@@ -79,15 +79,6 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint
                  : "memory");
 }
 
-// Rows r0 .. r3 of a 2-D tensor (box: one row), one below the other.
-__device__ __forceinline__ void load_gather4(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int r0, int r1, int r2,
-                                             int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
-        "%6, %7}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
-}
-
 // `bytes` (a multiple of 16) from 16-byte aligned global memory.
 __device__ __forceinline__ void load_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),

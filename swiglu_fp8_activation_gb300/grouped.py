@@ -10,11 +10,12 @@ allocates belongs to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 
 import torch
 
-from .binding import F_FP16, FORMATS, GROUP, SgqError, _act_dtype, _check, _ptr, _want, library
+from .binding import F_FP16, FORMATS, GROUP, SgqError, _act_dtype, _check, _want, library
 
 MAX_GROUPS = 1024
 MAX_RANK = 128
@@ -48,37 +49,31 @@ def _dims(t: torch.Tensor, n: int, name: str):
     return t.shape
 
 
-class _On:
-    """The device and stream of a call: every tensor on one CUDA device, made
-    the current one for the call, with `stream` its current stream."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+_here = contextlib.nullcontext()
 
-    def __init__(self, stream, **tensors):
-        there = {n: t for n, t in tensors.items() if t is not None}
-        first = next(iter(there.values())).device
-        for n, t in there.items():
-            if t.device != first:
-                raise SgqError(f"{n}: on {t.device}, the other tensors on {first}")
-        if first.type != "cuda":
-            raise SgqError(f"expected CUDA tensors, got {first}")
-        if stream is not None and stream.device != first:
-            raise SgqError(f"stream: of {stream.device}, the tensors on {first}")
-        self.device = first
-        self.stream = torch.cuda.current_stream(first) if stream is None else stream
-        self._same = stream is None and torch.cuda.current_device() == first.index
-        self.handle = C.c_void_p(self.stream.cuda_stream)
 
-    def __enter__(self):
-        if not self._same:
-            self._ctx = torch.cuda.stream(self.stream)     # makes the stream's device current, too
-            self._ctx.__enter__()
-        return self
+def _on(stream, what: str, *tensors):
+    """(device, stream handle, context) of a call: every tensor (or None) on
+    one CUDA device; the context makes it the current one, with `stream` its
+    current stream, so that what the call allocates belongs to that stream."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise SgqError(f"{what}: a tensor on {t.device}, another on {tensors[0].device}")
+    if d < 0:
+        raise SgqError(f"{what}: expected CUDA tensors, got {tensors[0].device}")
+    if stream is None:
+        if d == torch.cuda.current_device():
+            return tensors[0].device, _raw_stream(d), _here
+        stream = torch.cuda.current_stream(d)
+    elif stream.device != tensors[0].device:
+        raise SgqError(f"{what}: a stream of {stream.device}, tensors on {tensors[0].device}")
+    return tensors[0].device, stream.cuda_stream, torch.cuda.stream(stream)
 
-    def __exit__(self, *e):
-        if not self._same:
-            self._ctx.__exit__(*e)
 
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+def _at(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 def group_rows(ids: torch.Tensor, groups: int, *, offsets_out: torch.Tensor | None = None,
@@ -106,16 +101,18 @@ def group_rows(ids: torch.Tensor, groups: int, *, offsets_out: torch.Tensor | No
                            (slots_out, tuple(ids.shape), "slots_out")):
         if t is not None:
             _want(t, shape, torch.int32, name)
-    with _On(stream, ids=ids, offsets_out=offsets_out, rows_out=rows_out, slots_out=slots_out) as on:
+    dev, at, ctx = _on(stream, "group_rows", ids, offsets_out, rows_out, slots_out)
+    with ctx:
         if offsets_out is None:
-            offsets_out = on.empty((groups + 1,), torch.int32)
+            offsets_out = torch.empty((groups + 1,), dtype=torch.int32, device=dev)
         if rows_out is None:
-            rows_out = on.empty((T * k,), torch.int32)
+            rows_out = torch.empty((T * k,), dtype=torch.int32, device=dev)
         if slots_out is None:
-            slots_out = on.empty(tuple(ids.shape), torch.int32)
-        st = _lib().group_rows(ids.element_size(), T, k, groups, _ptr(ids), _ptr(offsets_out), _ptr(rows_out),
-                               _ptr(slots_out), on.handle)
-        _check(st, "group_rows")
+            slots_out = torch.empty(tuple(ids.shape), dtype=torch.int32, device=dev)
+        st = _lib().group_rows(ids.element_size(), T, k, groups, _at(ids), _at(offsets_out), _at(rows_out),
+                               _at(slots_out), at)
+        if st:
+            _check(st, "group_rows")
     return offsets_out, rows_out, slots_out
 
 
@@ -173,12 +170,14 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt
         raise SgqError(f"out: {odt} does not go with x of {x.dtype}")
     if out is not None:
         _want(out, (S, N), odt, "out")
-    with _On(stream, x=x, w=w, offsets=offsets, x_scale=x_scale, w_scale=w_scale, rows=rows, out=out) as on:
+    dev, at, ctx = _on(stream, "grouped_gemm", x, w, offsets, x_scale, w_scale, rows, out)
+    with ctx:
         if out is None:
-            out = on.empty((S, N), odt)
-        st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, _ptr(x),
-                                 _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(offsets), _ptr(rows), _ptr(out), on.handle)
-        _check(st, "grouped_gemm")
+            out = torch.empty((S, N), dtype=odt, device=dev)
+        st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, _at(x),
+                                 _at(x_scale), _at(w), _at(w_scale), _at(offsets), _at(rows), _at(out), at)
+        if st:
+            _check(st, "grouped_gemm")
     return out
 
 
@@ -200,13 +199,20 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
         _want(weights, (T, k), torch.float32, "weights")
     if out is not None:
         _want(out, (T, N), dt, "out")
-    with _On(stream, y=y, slots=slots, weights=weights, out=out) as on:
+    dev, at, ctx = _on(stream, "combine_rows", y, slots, weights, out)
+    with ctx:
         if out is None:
-            out = on.empty((T, N), dt)
-        st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, _ptr(y), _ptr(slots), _ptr(weights),
-                                 _ptr(out), on.handle)
-        _check(st, "combine_rows")
+            out = torch.empty((T, N), dtype=dt, device=dev)
+        st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, _at(y), _at(slots), _at(weights),
+                                 _at(out), at)
+        if st:
+            _check(st, "combine_rows")
     return out
+
+
+def lora_workspace_bytes(S: int, R: int) -> int:
+    """Bytes of lora_add's workspace for S slots and rank R (0 out of range)."""
+    return _lib().sgq_lora_workspace_bytes(int(S), int(R))
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, offsets: torch.Tensor, *,
@@ -220,7 +226,8 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
     all float16. offsets, rows, slots: group_rows of the requests' adapters
     ([T] ids, -1 for none); rows and slots both None where the rows of x
     already are in adapter order (slot s is row s). scaling [groups] float32 or
-    None (ones). workspace: float32 [S, R] or None (allocated). Rows without an
+    None (ones). workspace: uint8 [lora_workspace_bytes(S, R)] or None
+    (allocated). Rows without an
     adapter stay as they are. Returns y.
     """
     T, K = _dims(x, 2, "x")
@@ -244,12 +251,13 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
     if scaling is not None:
         _want(scaling, (groups,), torch.float32, "scaling")
     if workspace is not None:
-        _want(workspace, (S, R), torch.float32, "workspace")
-    with _On(stream, x=x, a=a, b=b, y=y, offsets=offsets, rows=rows, slots=slots, scaling=scaling,
-             workspace=workspace) as on:
+        _want(workspace, (lora_workspace_bytes(S, R),), torch.uint8, "workspace")
+    dev, at, ctx = _on(stream, "lora_add", x, a, b, y, offsets, rows, slots, scaling, workspace)
+    with ctx:
         if workspace is None:
-            workspace = on.empty((S, R), torch.float32)
-        st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, _ptr(x), _ptr(a), _ptr(b),
-                             _ptr(scaling), _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(y), _ptr(workspace), on.handle)
-        _check(st, "lora_add")
+            workspace = torch.empty((lora_workspace_bytes(S, R),), dtype=torch.uint8, device=dev)
+        st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, _at(x), _at(a), _at(b),
+                             _at(scaling), _at(offsets), _at(rows), _at(slots), _at(y), _at(workspace), at)
+        if st:
+            _check(st, "lora_add")
     return y

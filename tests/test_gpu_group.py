@@ -265,7 +265,7 @@ def run_lora(ids, G, R, K, N, dtype=torch.bfloat16, scaled=True, seed=0, sorted_
     res, tol = ref.lora(x, a, b, y, offsets, rows, slots, scaling, T)
     out, untouched = guarded((T, N), dtype)
     out.copy_(y)
-    ws, ws_untouched = guarded((T, R), torch.float32)
+    ws, ws_untouched = guarded((sgq.lora_workspace_bytes(T, R),), torch.uint8)
     dx, da, db, doff, drows, dslots, dc = cuda(x, a, b, offsets, rows, slots, scaling)
     got = sgq.lora_add(dx, da, db, out, doff, rows=drows, slots=dslots, scaling=dc, workspace=ws)
     assert got is out

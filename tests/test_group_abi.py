@@ -158,7 +158,7 @@ def test_lora_refusals(L):
         assert lora(L, y=P(i)) == INVALID, i
         assert lora(L, ws=P(i)) == INVALID, i
     assert lora(L, ws=P(7)) == INVALID
-    assert L.sgq_lora_workspace_bytes(8, 16) == 8 * 16 * 4
+    assert L.sgq_lora_workspace_bytes(8, 16) == 8 * (16 * 4 + 16)
     assert L.sgq_lora_workspace_bytes(8, 200) == 0
     assert L.sgq_lora_workspace_bytes(-1, 8) == 0
 
@@ -211,7 +211,7 @@ def test_python_refusals():
     no(sgq.lora_add, *args, rows=i32(4))                                        # rows without slots
     no(sgq.lora_add, *args, rows=i32(4), slots=i32(3))
     no(sgq.lora_add, *args, scaling=torch.zeros(3))
-    no(sgq.lora_add, *args, workspace=torch.zeros(4, 16))
+    no(sgq.lora_add, *args, workspace=u8(4 * 8 * 4))
     no(sgq.lora_add, args[0], args[1], bf(2, 8, 32), args[3], off)              # b transposed
     no(sgq.lora_add, args[0], args[1].half(), args[2], args[3], off)
     no(sgq.lora_add, *args)                                                     # on the CPU
