@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
     const uint32_t tiles_at = tc::smem_addr(tiles), scales_at = tc::smem_addr(scales);
 
     const GroupGemmArgs& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int chunks = p.chunks;
     const bool gather = a.rows != nullptr;
 
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
     // a next launch that holds tensor memory while it waits for this one may
     // start only now that this CTA has its own
     pdl_trigger();
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     Walk walk(lo, first, a.groups, p.n_tiles, BN);
 
     if (warp == 0) {
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                 if (!ok) break;
                 const uint32_t w_at = tiles_at + st * (C::kW + C::kX), x_at = w_at + C::kW;
                 const uint32_t bar = full + 8 * st;
-                if (lane == 0) {
+                if (tc::elect()) {
                     tc::bar_arrive_expect(bar, bytes);
                     tc::load_3d(w_at, &p.mw, bar, kc * kChunk, walk.n0, walk.g);
                     if (C::kMx) tc::load_bulk(scales_at + st * (C::kSw + C::kSx), ws + (int64_t)kc * 512, 512, bar);
@@ -196,27 +196,28 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         }
     } else if (warp == 1) {
         // -------------------------------------------------------- products
-        if (lane == 0) {
-            int st = 0, use = 0;
-            uint32_t ph = 0, chunk_no = 0;
-            bool ok = true;
-            while (ok && walk.next()) {
-                const uint32_t n = (uint32_t)(walk.m + 15) & ~15u;
-                uint32_t idesc;
-                if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kM >> 7) << 27);
-                else idesc = (1u << 4) | ((n >> 3) << 17) | ((kM >> 4) << 24);
-                if (FMT == FMT_16BIT && !p.f16) idesc |= (1u << 7) | (1u << 10);
-                const int left = p.kbytes - (chunks - 1) * kChunk;
-                const int last_steps = (left + 31) / 32;
-                for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
-                    const int buf = use & 1;
-                    if (C::kB128 || kc == 0) {
-                        ok = tc::bar_wait(acc_empty + 8 * buf, ((use >> 1) & 1) ^ 1, stop);
-                        if (!ok) break;
-                    }
-                    ok = tc::bar_wait(full + 8 * st, ph, stop);
+        int st = 0, use = 0;
+        uint32_t ph = 0, chunk_no = 0;
+        bool ok = true;
+        while (ok && walk.next()) {
+            const uint32_t n = (uint32_t)(walk.m + 15) & ~15u;
+            uint32_t idesc;
+            if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kM >> 7) << 27);
+            else idesc = (1u << 4) | ((n >> 3) << 17) | ((kM >> 4) << 24);
+            if (FMT == FMT_16BIT && !p.f16) idesc |= (1u << 7) | (1u << 10);
+            const int left = p.kbytes - (chunks - 1) * kChunk;
+            const int last_steps = (left + 31) / 32;
+            for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
+                const int buf = use & 1;
+                if (C::kB128 || kc == 0) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + 8 * buf, ((use >> 1) & 1) ^ 1, stop));
                     if (!ok) break;
-                    tc::fence_after();
+                }
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full + 8 * st, ph, stop));
+                if (!ok) break;
+                tc::fence_after();
+                const bool done_acc = C::kB128 || kc == chunks - 1;
+                if (tc::elect()) {
                     const uint32_t w_at = tiles_at + st * (C::kW + C::kX);
                     const uint64_t dw = tc::desc_sw128(w_at), dx = tc::desc_sw128(w_at + C::kW);
                     const uint32_t d = tmem + buf * BN;
@@ -228,28 +229,30 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                         for (int h = 0; h < C::kHalves; ++h) tc::copy_scales(sx + 4 * h, tc::desc_rows16(s_at + 512 + 512 * h));
                     }
                     const int steps = kc == chunks - 1 ? last_steps : 4;
-                    for (int k = 0; k < steps; ++k) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
                         const uint32_t add = k > 0 || (!C::kB128 && kc > 0);
+                        if (k >= steps) break;
                         if (C::kMx) tc::mma_mx8(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
                         else if (FMT == FMT_16BIT) tc::mma_f16(d, dw + 2 * k, dx + 2 * k, idesc, add);
                         else tc::mma_f8(d, dw + 2 * k, dx + 2 * k, idesc, add);
                     }
                     tc::commit(empty + 8 * st);
-                    if (C::kB128 || kc == chunks - 1) {
-                        tc::commit(acc_full + 8 * buf);
-                        ++use;
-                    }
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1;
-                    }
+                    if (done_acc) tc::commit(acc_full + 8 * buf);
+                }
+                __syncwarp();
+                use += done_acc;
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
-            if (!ok) {
-                uint32_t never = 0;
-                tc::commit(done);
-                tc::bar_wait(done, 0, &never, 1 << 27);
-            }
+        }
+        if (!ok) {
+            uint32_t never = 0;
+            if (tc::elect()) tc::commit(done);
+            __syncwarp();
+            tc::bar_wait(done, 0, &never, 1 << 27);
         }
     } else if (warp < 4) {
         // ------------------------------------------------- scales of the slots

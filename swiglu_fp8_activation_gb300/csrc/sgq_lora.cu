@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, acc = empty + 8 * kMaxStages, done = acc + 8;
     const uint32_t stages_at = tc::smem_addr(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int split = p.split, rank = blockIdx.x % split;
     const int cols = R <= 32 ? 32 : R <= 64 ? 64 : 128;
 
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     // may start only now that this CTA has its own
     pdl_trigger();
     cluster_wait();                  // every CTA of the cluster runs: its shared memory may be written
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     int g, s0, m;
     const bool any = find_tile(lo, first, l.groups, blockIdx.x / split, g, s0, m);   // the same in the whole cluster
     const int per = (p.chunks + split - 1) / split;
@@ -144,57 +144,63 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
             uint32_t ph = 0;
             int issued = 0;
             bool ok = true;
-            if (lane == 0) {
-                for (int kc = k_from; kc < k_to; ++kc) {
-                    ok = tc::bar_wait(empty + 8 * st, ph ^ 1, stop);
-                    if (!ok) break;
+            for (int kc = k_from; kc < k_to; ++kc) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
+                if (!ok) break;
+                if (tc::elect()) {
                     tc::bar_arrive_expect(full + 8 * st, (uint32_t)R * kChunk);
                     tc::load_3d(stages_at + st * p.stage_bytes + kM * kChunk, &p.ma, full + 8 * st, kc * kChunk, 0, g);
-                    ++issued;
-                    if (++st == stages) {
-                        st = 0;
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) {
+                // gave up: wait (a while) for the copies in flight
+                for (int i = 0; i < stages && i < issued; ++i) {
+                    uint32_t never = 0;
+                    if (--st < 0) {
+                        st = stages - 1;
                         ph ^= 1;
                     }
-                }
-                if (!ok) {
-                    // gave up: wait (a while) for the copies in flight
-                    for (int i = 0; i < stages && i < issued; ++i) {
-                        uint32_t never = 0;
-                        if (--st < 0) {
-                            st = stages - 1;
-                            ph ^= 1;
-                        }
-                        tc::bar_wait(full + 8 * st, ph, &never, 1 << 27);
-                    }
+                    tc::bar_wait(full + 8 * st, ph, &never, 1 << 27);
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint32_t idesc = idesc_f16(DT, (R + 15) & ~15);
-                int st = 0;
-                uint32_t ph = 0;
-                bool ok = true;
-                for (int kc = k_from; kc < k_to; ++kc) {
-                    ok = tc::bar_wait(full + 8 * st, ph, stop);
-                    if (!ok) break;
-                    tc::fence_after();
+            const uint32_t idesc = idesc_f16(DT, (R + 15) & ~15);
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int kc = k_from; kc < k_to; ++kc) {
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full + 8 * st, ph, stop));
+                if (!ok) break;
+                tc::fence_after();
+                if (tc::elect()) {
                     const uint64_t dx = tc::desc_sw128(stages_at + st * p.stage_bytes);
                     const uint64_t da = tc::desc_sw128(stages_at + st * p.stage_bytes + kM * kChunk);
                     const int left = p.kbytes - kc * kChunk, steps = left >= kChunk ? 4 : (left + 31) / 32;
-                    for (int k = 0; k < steps; ++k) tc::mma_f16(tmem, dx + 2 * k, da + 2 * k, idesc, kc > k_from || k > 0);
-                    tc::commit(empty + 8 * st);
-                    if (++st == stages) {
-                        st = 0;
-                        ph ^= 1;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k >= steps) break;
+                        tc::mma_f16(tmem, dx + 2 * k, da + 2 * k, idesc, kc > k_from || k > 0);
                     }
+                    tc::commit(empty + 8 * st);
+                    if (kc == k_to - 1) tc::commit(acc);
                 }
-                if (ok) {
-                    tc::commit(acc);
-                } else {
-                    uint32_t never = 0;
-                    tc::commit(done);
-                    tc::bar_wait(done, 0, &never, 1 << 27);
+                __syncwarp();
+                if (++st == stages) {
+                    st = 0;
+                    ph ^= 1;
                 }
+            }
+            if (!ok) {
+                uint32_t never = 0;
+                if (tc::elect()) tc::commit(done);
+                __syncwarp();
+                tc::bar_wait(done, 0, &never, 1 << 27);
             }
         } else if (warp >= 4) {
             // thread u copies 16-byte piece u % 8 of rows u / 8 + 16 i
@@ -363,7 +369,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), acc = full + 8;
     const LoraArgs& l = p.l;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, R = l.R;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), R = l.R;
     if (tid == 0) {
         tc::bar_init(full, 1);
         tc::bar_init(acc, 1);
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     int g, s0, m;
     const bool any = find_tile(lo, first, l.groups, blockIdx.x / (uint32_t)p.n_tiles, g, s0, m);
     const int n0 = (int)(blockIdx.x % (uint32_t)p.n_tiles) * NT;
@@ -388,29 +394,41 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
         pdl_wait();
         pdl_trigger();
     } else if (warp == 8) {
-        if (lane == 0) {
-            const uint32_t at = tc::smem_addr(smem), v_at = at + VC * C::kB;
+        const uint32_t at = tc::smem_addr(smem), v_at = at + VC * C::kB;
+        if (tc::elect()) {
             tc::bar_arrive_expect(full, VC * C::kB + 2 * VC * C::kV);
+#pragma unroll
             for (int c = 0; c < VC; ++c) tc::load_3d(at + c * C::kB, &p.mb, full, c * kChunk, n0, g);
-            pdl_wait();
-            pdl_trigger();
+        }
+        __syncwarp();
+        pdl_wait();
+        pdl_trigger();
+        if (tc::elect()) {
+#pragma unroll
             for (int h = 0; h < 2; ++h)
+#pragma unroll
                 for (int c = 0; c < VC; ++c)
                     tc::load_2d(v_at + (h * VC + c) * C::kV, &p.mv, full, h * 2 * R + c * kChunk, s0);
-            bool ok = tc::bar_wait(full, 0, stop);
-            if (ok) {
-                tc::fence_after();
+        }
+        __syncwarp();
+        if (__all_sync(0xFFFFFFFFu, tc::bar_wait(full, 0, stop))) {
+            tc::fence_after();
+            if (tc::elect()) {
                 const uint32_t idesc = idesc_f16(DT, NT);
                 const int steps = (R + 15) / 16;                         // of 16 values
+#pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    for (int k = 0; k < steps; ++k)
+#pragma unroll
+                    for (int k = 0; k < 4 * VC; ++k) {
+                        if (k >= steps) break;
                         tc::mma_f16(tmem, tc::desc_sw128(v_at + (h * VC + k / 4) * C::kV) + 2 * (k % 4),
                                     tc::desc_sw128(at + (k / 4) * C::kB) + 2 * (k % 4), idesc, h > 0 || k > 0);
+                    }
                 tc::commit(acc);
-            } else {
-                uint32_t never = 0;
-                tc::bar_wait(full, 0, &never, 1 << 27);
             }
+        } else {
+            uint32_t never = 0;
+            tc::bar_wait(full, 0, &never, 1 << 27);
         }
         __syncwarp();
     } else {
