@@ -9,7 +9,7 @@
 //            split over the CTAs of a cluster while the tiles are too few to
 //            fill the device; the parts are summed through distributed shared
 //            memory in the order of the CTAs.
-//   expand   y += c (v . b^T), tiles of 128 slots x 128 or 256 columns. Bound
+//   expand   y += c (v . b^T), tiles of 128 slots x 128 columns. Bound
 //            by reading and writing y.
 //
 // v is kept to about 16 bits and more between them: a row of the workspace
@@ -29,7 +29,8 @@ constexpr int kM = 128;              // slots a tile
 constexpr int kMaxStages = 8;
 constexpr int kShrinkThreads = 256;  // warp 0 copies of a, 1 products, 4-7 rows of x, then the result
 constexpr int kGather = 128;
-constexpr int kExpandThreads = 288;  // warps 0-7 the result, warp 8 copies and products
+constexpr int kLoaders = 128;
+constexpr int kExpandThreads = 288 + kLoaders;   // warps 0-7 the sums, 8 copies and products, 9-12 loads of y
 
 __device__ uint32_t g_gave_up;       // launches in which a wait ran out of time
 
@@ -40,11 +41,10 @@ struct alignas(128) ShrinkParams {
 };
 
 struct alignas(128) ExpandParams {
-    CUtensorMap mb;                  // b as bytes [groups][N][R], box 128 x NT rows
+    CUtensorMap mb;                  // b as bytes [groups][N][R], box 128 x 128 rows
     CUtensorMap mv;                  // workspace rows, box 128 x 128 rows
     LoraArgs l;
     int n_tiles;
-    int wide;                        // rows of y are 32-byte aligned
 };
 
 // The token of slot s, or -1 where it is outside or its own slot is another.
@@ -54,20 +54,15 @@ __device__ __forceinline__ int64_t token_of(const LoraArgs& l, int s) {
     return t >= 0 && t < l.T && l.slots[t] == s ? t : -1;
 }
 
-// The group and slots [s0, s0 + m) of tile q; false behind the last. Binary
-// search in the scanned offsets.
-__device__ __forceinline__ bool find_tile(const int* lo, const int* first, int G, int q, int& g, int& s0, int& m) {
-    if (q >= first[G]) return false;
-    int a = 0, b = G;                // first[a] <= q < first[b]
-    while (b - a > 1) {
-        const int c = (a + b) >> 1;
-        if (first[c] <= q) a = c;
-        else b = c;
-    }
-    g = a;
-    s0 = lo[a] + (q - first[a]) * kM;
-    m = min(kM, lo[a + 1] - s0);
-    return true;
+// Barrier `ID` of THREADS threads of the block; true when `ok` is in all of them.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool all_agree(bool ok) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ok), "n"(ID), "n"(THREADS)
+                 : "memory");
+    return r != 0;
 }
 
 // fp32 sums over kind::f16 operands: M = 128, N = n.
@@ -91,15 +86,17 @@ __device__ __forceinline__ void st_cluster16(const void* p, uint32_t rank, float
 // Shared memory: stages of (x 16 KB, a R x 128 bytes), the parts of v that
 // this CTA sums [split][128 / split][R + 4] floats, offsets, barriers.
 template <int DT, int BEHIND>
-__global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __grid_constant__ ShrinkParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
     const LoraArgs& l = p.l;
     const int R = l.R, stages = p.stages, ld = R + 4;
     float* parts = reinterpret_cast<float*>(smem + stages * p.stage_bytes);
-    int* lo = reinterpret_cast<int*>(parts + kM * ld);
-    int* first = lo + kMaxGroups + 8;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(first + kMaxGroups + 8);
+    int* tokens = reinterpret_cast<int*>(parts + kM * ld);       // of the tile's slots
+    float* factors = reinterpret_cast<float*>(tokens + kM);      // of the slots that this CTA sums
+    int* lo = reinterpret_cast<int*>(factors + kM);
+    int* first = lo + table_ints(l.groups);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(first + table_ints(l.groups));
     uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 2);
     int* part = reinterpret_cast<int*>(misc + 4);
     volatile uint32_t* stop = misc + 1;
@@ -133,7 +130,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     cluster_wait();                  // every CTA of the cluster runs: its shared memory may be written
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     int g, s0, m;
-    const bool any = find_tile(lo, first, l.groups, blockIdx.x / split, g, s0, m);   // the same in the whole cluster
+    const bool any = find_tile(lo, first, l.groups, kM, blockIdx.x / split, g, s0, m);   // the same in the whole cluster
+    if (any && tid < kM) tokens[tid] = tid < m ? (int)token_of(l, s0 + tid) : -1;
+    __syncthreads();
     const int per = (p.chunks + split - 1) / split;
     const int k_from = rank * per, k_to = min(p.chunks, k_from + per);
     const int active = (p.chunks + per - 1) / per;                                   // CTAs that have chunks
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
 #pragma unroll
             for (int i = 0; i < kM / 16; ++i) {
                 const int c = (u >> 3) + 16 * i;
-                const int64_t t = c < m ? token_of(l, s0 + c) : -1;
+                const int64_t t = tokens[c];
                 src[i] = t >= 0 ? reinterpret_cast<const uint8_t*>(l.x) + t * p.kbytes + piece * 16 : nullptr;
             }
             int st = 0, lag_st = 0, behind = 0;
@@ -269,48 +268,51 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    if (any && warp >= 4) {
-        const int share = kM / split, c = rank * share + tid - 128;
-        if (tid - 128 < share && c < m) {
-            const float* from = parts + (size_t)(tid - 128) * ld;
-            auto sum4 = [&](int r) {                     // v[r .. r + 3], the parts in the order of the CTAs
-                float4 f = *reinterpret_cast<const float4*>(from + r);
-                for (int q = 1; q < active; ++q) {
-                    const float4 o = *reinterpret_cast<const float4*>(from + (size_t)q * share * ld + r);
-                    f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
-                }
-                return f;
-            };
-            float factor = 1.0f, down = 1.0f;
-            if (DT == DT_F16) {
+    if (any) {
+        const int share = kM / split, mine = min(share, m - rank * share);       // slots that this CTA sums
+        auto sum4 = [&](int c, int r) {                  // v[r .. r + 3] of slot c, the parts in the order of the CTAs
+            const float* from = parts + (size_t)c * ld + r;
+            float4 f = *reinterpret_cast<const float4*>(from);
+            for (int q = 1; q < active; ++q) {
+                const float4 o = *reinterpret_cast<const float4*>(from + (size_t)q * share * ld);
+                f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+            }
+            return f;
+        };
+        if (DT == DT_F16) {
+            if (tid < mine) {
                 float top = 0.0f;
                 for (int r = 0; r < R; r += 4) {
-                    const float4 f = sum4(r);
+                    const float4 f = sum4(tid, r);
                     top = fmaxf(top, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
                 }
                 // 2^e with top / 2^e in [1, 2), e held to where both powers are normal
                 const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 227);
-                factor = __uint_as_float((uint32_t)e << 23);
-                down = __uint_as_float((uint32_t)(254 - e) << 23);
+                factors[tid] = __uint_as_float((uint32_t)e << 23);
             }
-            uint8_t* row = reinterpret_cast<uint8_t*>(l.v) + (int64_t)(s0 + c) * lora_row_bytes(R);
-            for (int r = 0; r < R; r += 8) {
-                uint32_t hi[4], low[4];
+            __syncthreads();
+        }
+        const int pieces = R / 8;
+        for (int i = tid; i < mine * pieces; i += kShrinkThreads) {
+            const int c = i / pieces, r = (i - c * pieces) * 8;
+            const float factor = DT == DT_F16 ? factors[c] : 1.0f;
+            const float down = DT == DT_F16 ? __uint_as_float((254u << 23) - __float_as_uint(factor)) : 1.0f;   // 1 / factor
+            uint8_t* row = static_cast<uint8_t*>(l.v) + (int64_t)(s0 + rank * share + c) * lora_row_bytes(R);
+            uint32_t hi[4], low[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4 f = sum4(r + 4 * h);
-                    const float v[4] = {f.x * down, f.y * down, f.z * down, f.w * down};
+            for (int h = 0; h < 2; ++h) {
+                const float4 f = sum4(c, r + 4 * h);
+                const float v[4] = {f.x * down, f.y * down, f.z * down, f.w * down};
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float a0 = round_io<DT>(v[2 * i]), a1 = round_io<DT>(v[2 * i + 1]);
-                        hi[2 * h + i] = pack2<DT>(a0, a1);
-                        low[2 * h + i] = pack2<DT>(v[2 * i] - a0, v[2 * i + 1] - a1);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    const float a0 = round_io<DT>(v[2 * j]), a1 = round_io<DT>(v[2 * j + 1]);
+                    hi[2 * h + j] = pack2<DT>(a0, a1);
+                    low[2 * h + j] = pack2<DT>(v[2 * j] - a0, v[2 * j + 1] - a1);
                 }
-                *reinterpret_cast<uint4*>(row + 2 * r) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(row + 2 * R + 2 * r) = make_uint4(low[0], low[1], low[2], low[3]);
             }
-            *reinterpret_cast<float4*>(row + 4 * R) = make_float4(factor, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<uint4*>(row + 2 * r) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(row + 2 * R + 2 * r) = make_uint4(low[0], low[1], low[2], low[3]);
+            if (r == 0) *reinterpret_cast<float4*>(row + 4 * R) = make_float4(factor, 0.0f, 0.0f, 0.0f);
         }
     }
     tc::fence_before();
@@ -320,59 +322,77 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_kernel(const __
     if (tid == 0 && *stop) atomicAdd(&g_gave_up, 1);
 }
 
-// 16 values of y from p on (8 where the row ends there), in 32- or 16-byte accesses.
-__device__ __forceinline__ void load_y(const uint16_t* p, int n, int N, bool wide, uint32_t (&v)[8]) {
-    if (wide && n + 16 <= N) {
-        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                     : "l"(p)
-                     : "memory");
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (n + 8 * h < N) {
-            const uint4 t = *reinterpret_cast<const uint4*>(p + 8 * h);
-            v[4 * h] = t.x, v[4 * h + 1] = t.y, v[4 * h + 2] = t.z, v[4 * h + 3] = t.w;
-        }
-}
-
-__device__ __forceinline__ void store_y(uint16_t* p, int n, int N, bool wide, const uint32_t (&v)[8]) {
-    if (wide && n + 16 <= N) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (n + 8 * h < N) *reinterpret_cast<uint4*>(p + 8 * h) = make_uint4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
-}
-
-// y rows of one tile: 128 slots x NT columns. VC chunks of 128 bytes hold R values.
-template <int DT, int NT, int VC>
+// A tile of y: 128 slots x 128 columns, in shared memory in rows of 272 bytes
+// (the 16 over let a warp read 32 rows' same columns without bank conflicts).
+// VC chunks of 128 bytes hold R values.
+template <int VC>
 struct ExpandCfg {
-    static constexpr int kB = NT * kChunk, kV = kM * kChunk;
-    static constexpr int kSmem = 1024 + VC * kB + 2 * VC * kV + 2 * 4 * (kMaxGroups + 8) + 256;
+    static constexpr int kNT = 128, kPitch = 2 * kNT + 16;
+    static constexpr int kB = kNT * kChunk, kV = kM * kChunk, kY = kM * kPitch;
+    static constexpr int kBufs = VC == 1 ? 2 : 1;                    // of b: the next tile's under this one's
+    static constexpr int kYBufs = VC == 1 ? 4 : 3;                   // of y: loads two or three tiles ahead
+    static constexpr int kYAt = kBufs * VC * kB + 2 * VC * kV;
+    static constexpr int kTokensAt = kYAt + kYBufs * kY;
+    static constexpr int kTablesAt = kTokensAt + kYBufs * 4 * kM;
+    static int smem(int groups) { return 1024 + kTablesAt + 2 * 4 * table_ints(groups) + 256; }
 };
 
-template <int DT, int NT, int VC>
-__global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
-    using C = ExpandCfg<DT, NT, VC>;
+// The tiles of one CTA: a piece of their list, in which the columns' tiles of
+// one set of slots follow one another, so that a CTA mostly keeps its slots
+// (their tokens and v) from tile to tile.
+struct ExpandWalk {
+    const int* lo;
+    const int* first;
+    int G, n_tiles, nt;
+    int64_t tile, end;
+    int q, g, s0, m, n0;
+    bool fresh;                      // other slots than the tile before
+    __device__ ExpandWalk(const int* lo_, const int* first_, int G_, int n_tiles_, int nt_)
+        : lo(lo_), first(first_), G(G_), n_tiles(n_tiles_), nt(nt_), q(-1) {
+        const int64_t all = (int64_t)first_[G_] * n_tiles_;
+        tile = all * blockIdx.x / gridDim.x;
+        end = all * (blockIdx.x + 1) / gridDim.x;
+    }
+    __device__ bool next() {
+        if (tile >= end) return false;
+        const int at = (int)(tile / n_tiles);
+        n0 = (int)(tile - (int64_t)at * n_tiles) * nt;
+        fresh = at != q;
+        if (fresh) find_tile(lo, first, G, kM, at, g, s0, m);
+        q = at;
+        ++tile;
+        return true;
+    }
+};
+
+template <int DT, int VC>
+__global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
+    using C = ExpandCfg<VC>;
+    constexpr int NT = C::kNT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
-    int* lo = reinterpret_cast<int*>(smem + VC * C::kB + 2 * VC * C::kV);
-    int* first = lo + kMaxGroups + 8;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(first + kMaxGroups + 8);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 3);
+    const LoraArgs& l = p.l;
+    int* tokens = reinterpret_cast<int*>(smem + C::kTokensAt);           // [kYBufs][128]
+    int* lo = reinterpret_cast<int*>(smem + C::kTablesAt);
+    int* first = lo + table_ints(l.groups);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(first + table_ints(l.groups));
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 15);
     int* part = reinterpret_cast<int*>(misc + 4);
     volatile uint32_t* stop = misc + 1;
-    const uint32_t full = tc::smem_addr(bars), acc = full + 8;
-    const LoraArgs& l = p.l;
+    const uint32_t full_b = tc::smem_addr(bars), full_v = full_b + 16, acc = full_v + 8, acc_empty = acc + 16;
+    const uint32_t y_full = acc_empty + 16, y_empty = y_full + 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), R = l.R;
     if (tid == 0) {
-        tc::bar_init(full, 1);
-        tc::bar_init(acc, 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(full_b + 8 * i, 1);
+            tc::bar_init(acc + 8 * i, 1);
+            tc::bar_init(acc_empty + 8 * i, 8);
+        }
+        tc::bar_init(full_v, 1);
+        for (int i = 0; i < C::kYBufs; ++i) {
+            tc::bar_init(y_full + 8 * i, kLoaders + kLoaders / 32);
+            tc::bar_init(y_empty + 8 * i, 8);
+        }
         tc::fence_barrier_init();
         *stop = 0;
         tc::prefetch_map(&p.mb);
@@ -381,112 +401,314 @@ __global__ void __launch_bounds__(kExpandThreads, 2) lora_expand_kernel(const __
     // The shrink launch before this one lets it start after it has waited for
     // everything before itself, and writes the workspace alone: all but the
     // workspace may be read before the wait.
-    if (warp == 8) tc::tmem_alloc(tc::smem_addr(misc), NT);
+    if (warp == 8) tc::tmem_alloc(tc::smem_addr(misc), 2 * NT);
     scan_groups(l.offsets, l.groups, l.S, kM, lo, first, part);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
-    int g, s0, m;
-    const bool any = find_tile(lo, first, l.groups, blockIdx.x / (uint32_t)p.n_tiles, g, s0, m);
-    const int n0 = (int)(blockIdx.x % (uint32_t)p.n_tiles) * NT;
-    if (!any) {
+    ExpandWalk walk(lo, first, l.groups, p.n_tiles, NT);
+    if (warp > 8) {
+        // ------------------------------------------------------- loads of y
+        const int u = tid - 288, piece = u & 15;
+        bool ok = true;
+        int t = -1;
+        for (uint32_t i = 0; walk.next(); ++i) {
+            const uint32_t buf = i % C::kYBufs;
+            if (walk.fresh) t = u < walk.m ? (int)token_of(l, walk.s0 + u) : -1;
+            ok = tc::bar_wait(y_empty + 8 * buf, ((i / C::kYBufs) & 1) ^ 1, stop);
+            int* tk = tokens + buf * kM;
+            if (ok) tk[u] = t;
+            if (!all_agree<1, kLoaders>(ok)) break;
+            if (lane == 0) tc::bar_arrive(y_full + 8 * buf);             // the tokens; the copies arrive by themselves
+            uint8_t* to = smem + C::kYAt + buf * C::kY + piece * 16;
+            const int n = walk.n0 + piece * 8;
+#pragma unroll
+            for (int j = 0; j < kM / 8; ++j) {
+                const int c = (u >> 4) + 8 * j, row = tk[c];
+                if (row >= 0 && n < l.N) cp_async16(to + c * C::kPitch, l.y + (int64_t)row * l.N + n, 16);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(y_full + 8 * buf) : "memory");
+        }
+        cp_async_wait<0>();
         pdl_wait();
         pdl_trigger();
     } else if (warp == 8) {
-        const uint32_t at = tc::smem_addr(smem), v_at = at + VC * C::kB;
-        if (tc::elect()) {
-            tc::bar_arrive_expect(full, VC * C::kB + 2 * VC * C::kV);
+        // ------------------------------------------ copies of b and v, products
+        const uint32_t at = tc::smem_addr(smem), v_at = at + C::kBufs * VC * C::kB;
+        auto load_b = [&](const ExpandWalk& w, uint32_t i) {             // tile i's rows of b into buffer i % kBufs
+            if (tc::elect()) {
+                const uint32_t bar = full_b + 8 * (i % C::kBufs), to = at + (i % C::kBufs) * VC * C::kB;
+                tc::bar_arrive_expect(bar, VC * C::kB);
 #pragma unroll
-            for (int c = 0; c < VC; ++c) tc::load_3d(at + c * C::kB, &p.mb, full, c * kChunk, n0, g);
-        }
-        __syncwarp();
+                for (int c = 0; c < VC; ++c) tc::load_3d(to + c * C::kB, &p.mb, bar, c * kChunk, w.n0, w.g);
+            }
+            __syncwarp();
+        };
+        ExpandWalk ahead = walk;
+        bool more = ahead.next();
+        if (more) load_b(ahead, 0);
         pdl_wait();
         pdl_trigger();
-        if (tc::elect()) {
+        bool ok = true;
+        uint32_t vs = 0;                                                 // loads of v so far
+        for (uint32_t i = 0; ok && walk.next(); ++i) {
+            const uint32_t buf = i & 1;
+            // the product before is done with v and with the other buffer of b
+            if (i > 0) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc + 8 * (buf ^ 1), ((i - 1) >> 1) & 1, stop));
+            if (!ok) break;
+            if (walk.fresh) {
+                if (tc::elect()) {
+                    tc::bar_arrive_expect(full_v, 2 * VC * C::kV);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int c = 0; c < VC; ++c)
-                    tc::load_2d(v_at + (h * VC + c) * C::kV, &p.mv, full, h * 2 * R + c * kChunk, s0);
-        }
-        __syncwarp();
-        if (__all_sync(0xFFFFFFFFu, tc::bar_wait(full, 0, stop))) {
+                        for (int c = 0; c < VC; ++c)
+                            tc::load_2d(v_at + (h * VC + c) * C::kV, &p.mv, full_v, h * 2 * R + c * kChunk, walk.s0);
+                }
+                __syncwarp();
+                ++vs;
+            }
+            if (C::kBufs == 1) {
+                if (i > 0) load_b(walk, i);
+                more = false;
+            } else {
+                more = ahead.next();
+                if (more) load_b(ahead, i + 1);
+            }
+            ok = tc::bar_wait(full_v, (vs - 1) & 1, stop) &&
+                 tc::bar_wait(full_b + 8 * (i % C::kBufs), (i / C::kBufs) & 1, stop) &&
+                 tc::bar_wait(acc_empty + 8 * buf, ((i >> 1) & 1) ^ 1, stop);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) {
+                // gave up: wait (a while) for the copies in flight
+                uint32_t never = 0;
+                tc::bar_wait(full_v, (vs - 1) & 1, &never, 1 << 27);
+                never = 0;
+                tc::bar_wait(full_b + 8 * (i % C::kBufs), (i / C::kBufs) & 1, &never, 1 << 27);
+                never = 0;
+                if (more) tc::bar_wait(full_b + 8 * ((i + 1) % C::kBufs), ((i + 1) / C::kBufs) & 1, &never, 1 << 27);
+                break;
+            }
             tc::fence_after();
             if (tc::elect()) {
-                const uint32_t idesc = idesc_f16(DT, NT);
+                const uint32_t idesc = idesc_f16(DT, NT), b_at = at + (i % C::kBufs) * VC * C::kB;
                 const int steps = (R + 15) / 16;                         // of 16 values
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4 * VC; ++k) {
                         if (k >= steps) break;
-                        tc::mma_f16(tmem, tc::desc_sw128(v_at + (h * VC + k / 4) * C::kV) + 2 * (k % 4),
-                                    tc::desc_sw128(at + (k / 4) * C::kB) + 2 * (k % 4), idesc, h > 0 || k > 0);
+                        tc::mma_f16(tmem + buf * NT, tc::desc_sw128(v_at + (h * VC + k / 4) * C::kV) + 2 * (k % 4),
+                                    tc::desc_sw128(b_at + (k / 4) * C::kB) + 2 * (k % 4), idesc, h > 0 || k > 0);
                     }
-                tc::commit(acc);
+                tc::commit(acc + 8 * buf);
             }
-        } else {
-            uint32_t never = 0;
-            tc::bar_wait(full, 0, &never, 1 << 27);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // this thread: slot s0 + c, columns n0 + first_n ..
-        const int quarter = warp & 3, c = quarter * 32 + lane;
-        const int first_n = (warp >> 2) * (NT / 2);
-        const int64_t t = c < m ? token_of(l, s0 + c) : -1;
-        const float scale = l.scaling ? l.scaling[g] : 1.0f;
-        uint16_t* y = l.y + (t >= 0 ? t : 0) * l.N + n0 + first_n;
-        const int n = n0 + first_n;
-        constexpr int kBlocks = NT / 2 / 32;
-        uint32_t next[2][8];
-        if (t >= 0)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) load_y(y + 16 * h, n + 16 * h, l.N, p.wide, next[h]);
+        // -------------------------------------- sums: 64 columns of slot c a thread
+        const int quarter = warp & 3, c = quarter * 32 + lane, first_n = (warp >> 2) * (NT / 2), piece = tid & 15;
+        bool ok = true;
+        float f = 0.0f;
         pdl_wait();
-        float f = scale;
-        if (DT == DT_F16 && t >= 0)
-            f *= *reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(l.v) + (int64_t)(s0 + c) * lora_row_bytes(R) + 4 * R);
-        const bool ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc, 0, stop));
-        if (ok) {
-            tc::fence_after();
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                uint32_t v[32], cur[2][8];
-                tc::tmem_load32(tmem + ((uint32_t)quarter << 21) + first_n + 32 * b, v);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) cur[h][i] = next[h][i];
-                if (b + 1 < kBlocks && t >= 0)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        load_y(y + 32 * (b + 1) + 16 * h, n + 32 * (b + 1) + 16 * h, l.N, p.wide, next[h]);
-                tc::tmem_load_wait(v);
-                if (t >= 0)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t w = cur[h][i];
-                            const float2 old = DT == DT_BF16
-                                                   ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u))
-                                                   : f16x2_to_f32x2(w);
-                            o[i] = pack2<DT>(fmaf(f, __uint_as_float(v[16 * h + 2 * i]), old.x),
-                                             fmaf(f, __uint_as_float(v[16 * h + 2 * i + 1]), old.y));
-                        }
-                        store_y(y + 32 * b + 16 * h, n + 32 * b + 16 * h, l.N, p.wide, o);
-                    }
+        for (uint32_t i = 0; walk.next(); ++i) {
+            const uint32_t buf = i & 1, y_buf = i % C::kYBufs;
+            uint8_t* y = smem + C::kYAt + y_buf * C::kY;
+            const int* tk = tokens + y_buf * kM;
+            if (walk.fresh) {
+                f = l.scaling ? l.scaling[walk.g] : 1.0f;
+                if (DT == DT_F16 && c < walk.m)
+                    f *= *reinterpret_cast<const float*>(static_cast<const uint8_t*>(l.v) +
+                                                         (int64_t)(walk.s0 + c) * lora_row_bytes(R) + 4 * R);
             }
+            ok = tc::bar_wait(y_full + 8 * y_buf, (i / C::kYBufs) & 1, stop) && tc::bar_wait(acc + 8 * buf, (i >> 1) & 1, stop);
+            if (!all_agree<2, 256>(ok)) break;
+            tc::fence_after();
+            uint4* row = reinterpret_cast<uint4*>(y + c * C::kPitch + 2 * first_n);
+#pragma unroll
+            for (int h = 0; h < NT / 2 / 32; ++h) {
+                uint32_t v[32];
+                tc::tmem_load32(tmem + ((uint32_t)quarter << 21) + buf * NT + first_n + 32 * h, v);
+                tc::tmem_load_wait(v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 was = row[4 * h + j];
+                    float o[8];
+                    load8<DT>(was, o);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = fmaf(f, __uint_as_float(v[8 * j + k]), o[k]);
+                    row[4 * h + j] = pack8<DT>(o);
+                }
+            }
+            tc::fence_before();
+            asm volatile("bar.sync 2, 256;" ::: "memory");               // the tile's rows are done
+            if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+            const int n = walk.n0 + piece * 8;
+#pragma unroll
+            for (int j = 0; j < kM / 16; ++j) {
+                const int r = (tid >> 4) + 16 * j, t = tk[r];
+                if (t >= 0 && n < l.N)
+                    st16_if(l.y + (int64_t)t * l.N + n, *reinterpret_cast<const uint4*>(y + r * C::kPitch + piece * 16), true);
+            }
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(y_empty + 8 * y_buf);
         }
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 8) tc::tmem_free(tmem, NT);
+    if (warp == 8) tc::tmem_free(tmem, 2 * NT);
     if (tid == 0 && *stop) atomicAdd(&g_gave_up, 1);
+}
+
+// ------------------------------------------------ few slots an adapter
+//
+// A decode batch: one or a few slots an adapter, so that the tensor cores'
+// tiles of 128 slots would be empty and their latency most of the time. Plain
+// fp32 arithmetic instead, v in fp32 in the workspace. A CTA takes up to 8
+// slots of one adapter and each value of a or b once for all of them.
+
+constexpr int kFew = 8;              // slots a tile
+constexpr int kFewThreads = 256;
+// Slots an adapter (on average) x rank up to which this form runs. K = N = 4096,
+// this form and the tensor cores': rank 16, 16 slots 16.7 and 22.4 us; rank 64,
+// 8 slots 17.2 and 15, 16 slots 21.5 and 15.7; rank 128, 16 slots 25.3 and 14.4.
+constexpr int64_t kFewWork = 256;
+constexpr int kFewRanks = 2;         // ranks a CTA of the shrink takes: 4 warps each, a quarter of K
+
+template <int DT>
+__global__ void __launch_bounds__(kFewThreads) lora_few_shrink_kernel(const LoraArgs l) {
+    extern __shared__ int few_smem[];
+    int* lo = few_smem;
+    int* first = lo + table_ints(l.groups);
+    __shared__ float sums[kFewRanks * 4][kFew];
+    __shared__ int part[kFewThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    scan_groups(l.offsets, l.groups, l.S, kFew, lo, first, part);
+    const int blocks = (l.R + kFewRanks - 1) / kFewRanks;
+    int g, s0, m;
+    if (!find_tile(lo, first, l.groups, kFew, blockIdx.x / (uint32_t)blocks, g, s0, m)) return;
+    const int r0 = (int)(blockIdx.x % (uint32_t)blocks) * kFewRanks, r = r0 + warp / 4, slice = warp & 3;   // R is even
+    const int64_t mine = lane < m ? token_of(l, s0 + lane) : -1;
+    const uint16_t* x[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, mine, i);
+        x[i] = t >= 0 ? l.x + t * l.K : nullptr;
+    }
+    const uint16_t* a = l.a + ((int64_t)g * l.R + r) * l.K;
+    float sum[kFew] = {};
+    // chunks of 8 values: lane, 32 + lane, .. of this warp's slice
+    const int chunks = l.K / 8, per = (chunks + 3) / 4, from = slice * per, to = min(chunks, from + per);
+#pragma unroll 4
+    for (int c = from + lane; c < to; c += 32) {
+        float fa[8];
+        load8<DT>(*reinterpret_cast<const uint4*>(a + 8 * c), fa);
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            if (x[i]) {
+                float fx[8];
+                load8<DT>(*reinterpret_cast<const uint4*>(x[i] + 8 * c), fx);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[i] = fmaf(fa[j], fx[j], sum[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+        float v = sum[i];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        if (lane == 0) sums[warp][i] = v;
+    }
+    __syncthreads();
+    if (tid < kFewRanks * kFew) {
+        const int i = tid % kFew, k = tid / kFew;
+        if (i < m)
+            static_cast<float*>(l.v)[(int64_t)(s0 + i) * l.R + r0 + k] =
+                (sums[4 * k][i] + sums[4 * k + 1][i]) + (sums[4 * k + 2][i] + sums[4 * k + 3][i]);
+    }
+}
+
+// A CTA: up to 8 slots x 512 columns, two columns a thread.
+template <int DT>
+__global__ void __launch_bounds__(kFewThreads) lora_few_expand_kernel(const LoraArgs l) {
+    extern __shared__ int few_smem[];
+    int* lo = few_smem;
+    int* first = lo + table_ints(l.groups);
+    __shared__ __align__(16) float v[kFew][kMaxRank];
+    __shared__ int part[kFewThreads / 32];
+    const int tid = threadIdx.x;
+    // (what may be read before the wait: see lora_expand_kernel)
+    scan_groups(l.offsets, l.groups, l.S, kFew, lo, first, part);
+    const int blocks = (l.N + 2 * kFewThreads - 1) / (2 * kFewThreads);
+    int g, s0, m;
+    if (!find_tile(lo, first, l.groups, kFew, blockIdx.x / (uint32_t)blocks, g, s0, m)) {
+        pdl_wait();
+        pdl_trigger();
+        return;
+    }
+    const int n = ((int)(blockIdx.x % (uint32_t)blocks) * kFewThreads + tid) * 2;
+    const bool in = n < l.N;                             // N is even
+    const int64_t mine = (tid & 31) < m ? token_of(l, s0 + (tid & 31)) : -1;
+    int64_t t[kFew];
+    uint32_t old[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) t[i] = __shfl_sync(0xFFFFFFFFu, mine, i);
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+        if (t[i] >= 0 && in) old[i] = *reinterpret_cast<const uint32_t*>(l.y + t[i] * l.N + n);
+    const float scale = l.scaling ? l.scaling[g] : 1.0f;
+    const uint16_t* b = l.b + ((int64_t)g * l.N + (in ? n : 0)) * l.R;
+    uint4 b0 = *reinterpret_cast<const uint4*>(b), b1 = *reinterpret_cast<const uint4*>(b + l.R);
+    pdl_wait();
+    pdl_trigger();
+    for (int i = tid; i < m * l.R; i += kFewThreads) v[i / l.R][i % l.R] = static_cast<const float*>(l.v)[(int64_t)s0 * l.R + i];
+    __syncthreads();
+    float acc[kFew][2] = {};
+    for (int r = 0; r < l.R; r += 8) {
+        float f0[8], f1[8];
+        load8<DT>(b0, f0);
+        load8<DT>(b1, f1);
+        if (r + 8 < l.R) {
+            b0 = *reinterpret_cast<const uint4*>(b + r + 8);
+            b1 = *reinterpret_cast<const uint4*>(b + l.R + r + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+            if (i < m) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(&v[i][r + j]);
+                    acc[i][0] = fmaf(w.x, f0[j], fmaf(w.y, f0[j + 1], fmaf(w.z, f0[j + 2], fmaf(w.w, f0[j + 3], acc[i][0]))));
+                    acc[i][1] = fmaf(w.x, f1[j], fmaf(w.y, f1[j + 1], fmaf(w.z, f1[j + 2], fmaf(w.w, f1[j + 3], acc[i][1]))));
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kFew; ++i)
+        if (t[i] >= 0 && in) {
+            const float2 was = DT == DT_BF16 ? make_float2(__uint_as_float(old[i] << 16), __uint_as_float(old[i] & 0xFFFF0000u))
+                                             : f16x2_to_f32x2(old[i]);
+            *reinterpret_cast<uint32_t*>(l.y + t[i] * l.N + n) =
+                pack2<DT>(fmaf(scale, acc[i][0], was.x), fmaf(scale, acc[i][1], was.y));
+        }
+}
+
+template <int DT>
+cudaError_t run_few(const Device& dev, const LoraArgs& l, cudaStream_t stream) {
+    const int64_t tiles = (int64_t)l.S / kFew + (l.S < l.groups ? l.S : l.groups);   // at most
+    const int64_t shrink = tiles * ((l.R + kFewRanks - 1) / kFewRanks);
+    const int64_t expand = tiles * ((l.N + 2 * kFewThreads - 1) / (2 * kFewThreads));
+    if (shrink > 0x7FFFFFFF || expand > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const int smem = 2 * 4 * table_ints(l.groups);
+    const cudaError_t e =
+        launch_grid(lora_few_shrink_kernel<DT>, dim3((unsigned)shrink), kFewThreads, smem, 1, dev.id, l, stream);
+    if (e != cudaSuccess) return e;
+    return launch_grid(lora_few_expand_kernel<DT>, dim3((unsigned)expand), kFewThreads, smem, 1, dev.id, l, stream);
 }
 
 template <int DT, int BEHIND>
@@ -496,43 +718,45 @@ cudaError_t shrink(const Device& dev, ShrinkParams& p, int64_t tiles, int smem, 
     return launch_grid(lora_shrink_kernel<DT, BEHIND>, dim3((unsigned)ctas), kShrinkThreads, smem, p.split, dev.id, p, stream);
 }
 
-template <int DT, int NT, int VC>
+template <int DT, int VC>
 cudaError_t expand(const Device& dev, ExpandParams& p, int64_t tiles, cudaStream_t stream) {
+    using C = ExpandCfg<VC>;
     const LoraArgs& l = p.l;
     const cuuint64_t bd[3] = {(cuuint64_t)(2 * l.R), (cuuint64_t)l.N, (cuuint64_t)l.groups};
     const cuuint64_t vd[2] = {(cuuint64_t)lora_row_bytes(l.R), (cuuint64_t)l.S};
-    if (!encode_rows(&p.mb, l.b, 3, bd, NT) || !encode_rows(&p.mv, l.v, 2, vd, kM)) return cudaErrorInvalidValue;
-    p.n_tiles = (l.N + NT - 1) / NT;
-    const int64_t ctas = tiles * p.n_tiles;
-    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    return launch_grid(lora_expand_kernel<DT, NT, VC>, dim3((unsigned)ctas), kExpandThreads, ExpandCfg<DT, NT, VC>::kSmem, 1,
-                       dev.id, p, stream);
+    if (!encode_rows(&p.mb, l.b, 3, bd, C::kNT) || !encode_rows(&p.mv, l.v, 2, vd, kM)) return cudaErrorInvalidValue;
+    p.n_tiles = (l.N + C::kNT - 1) / C::kNT;
+    const int64_t most = tiles * p.n_tiles, room = dev.sms > 0 ? dev.sms : 1;
+    return launch_grid(lora_expand_kernel<DT, VC>, dim3((unsigned)(most < room ? most : room)), kExpandThreads,
+                       C::smem(l.groups), 1, dev.id, p, stream);
 }
 
 template <int DT>
 cudaError_t run(const Device& dev, const LoraArgs& l, cudaStream_t stream) {
+    if ((int64_t)l.S * l.R <= kFewWork * l.groups) return run_few<DT>(dev, l, stream);
     ShrinkParams p;
     p.l = l;
     p.kbytes = 2 * l.K;
     p.chunks = (p.kbytes + kChunk - 1) / kChunk;
     p.stage_bytes = (kM + l.R) * kChunk;
-    const int fixed = 1024 + 4 * kM * (l.R + 4) + 2 * 4 * (kMaxGroups + 8) + 512;
-    p.stages = (kMaxDynamicSmem - fixed) / p.stage_bytes;
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
     const cuuint64_t ad[3] = {(cuuint64_t)p.kbytes, (cuuint64_t)l.R, (cuuint64_t)l.groups};
     if (!encode_rows(&p.ma, l.a, 3, ad, l.R)) return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)l.S / kM + (l.S < l.groups ? l.S : l.groups);     // at most
-    // the length of x over a cluster while the tiles leave multiprocessors
-    // idle and a CTA keeps at least 4 chunks
+    const int fixed = 1024 + 4 * kM * (l.R + 4) + 2 * 4 * kM + 2 * 4 * table_ints(l.groups) + 512;
+    // two CTAs a multiprocessor where at least 5 stages of each fit
+    const bool two = (kMaxDynamicSmem - 2048) / 2 - fixed >= 5 * p.stage_bytes;
+    p.stages = ((two ? (kMaxDynamicSmem - 2048) / 2 : kMaxDynamicSmem) - fixed) / p.stage_bytes;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    // the length of x over a cluster while all the tiles' parts are resident
+    // at once and a CTA keeps at least 4 chunks
     p.split = 1;
-    while (p.split < kMaxCluster && tiles * p.split * 2 <= dev.sms && p.chunks >= 8 * p.split) p.split *= 2;
+    while (p.split < kMaxCluster && tiles * p.split * 2 <= (two ? 2 : 1) * dev.sms && p.chunks >= 8 * p.split) p.split *= 2;
     const int smem = fixed + p.stages * p.stage_bytes;
     cudaError_t e = p.stages >= 7 ? shrink<DT, 5>(dev, p, tiles, smem, stream) : shrink<DT, 3>(dev, p, tiles, smem, stream);
     if (e != cudaSuccess) return e;
     ExpandParams q;
     q.l = l;
-    q.wide = reinterpret_cast<uintptr_t>(l.y) % 32 == 0 && l.N % 16 == 0;
-    return l.R <= 64 ? expand<DT, 256, 1>(dev, q, tiles, stream) : expand<DT, 128, 2>(dev, q, tiles, stream);
+    return l.R <= 64 ? expand<DT, 1>(dev, q, tiles, stream) : expand<DT, 2>(dev, q, tiles, stream);
 }
 
 }  // namespace

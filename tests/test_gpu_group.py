@@ -288,6 +288,13 @@ def test_lora_ranks(R, dtype):
     run_lora(mixed(70, 4), 4, R, 264, 520, dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R", [8, 24, 56, 128])
+def test_lora_ranks_few_slots_an_adapter(R, dtype):
+    run_lora(mixed(90, 20), 20, R, 520, 1032, dtype)
+    run_lora([3] * 40 + mixed(20, 16), 16, R, 136, 520, dtype)      # 40 slots of one, few on average
+
+
 @pytest.mark.parametrize("T,G,K,N", [(1, 1, 8, 8), (1, 5, 1024, 2048), (2, 2, 4096, 72), (64, 32, 512, 512), (65, 64, 136, 1032), (333, 3, 1000, 264),
                                      (600, 7, 256, 4096), (1500, 2, 2048, 128)])
 def test_lora_shapes(T, G, K, N):
