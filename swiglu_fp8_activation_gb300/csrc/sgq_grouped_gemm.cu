@@ -41,6 +41,7 @@ namespace {
 constexpr int kGatherThreads = 128;
 constexpr int kM = 128;            // channels a tile
 constexpr int kScaleThreads = 64;
+constexpr int kTurn = 32 * 64;       // bytes in which an epilogue warp turns 32 slots x 32 channels
 constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
 
 struct alignas(128) GemmParams {
@@ -62,14 +63,17 @@ struct Cfg {
     static constexpr int kSw = kMx ? 512 : 0;                     // weights' scales of a chunk
     static constexpr int kSx = kMx ? 512 * kHalves : kB128 ? 4 * BN : 0;
     static constexpr int kStage = kW + kX + kSw + kSx;
-    static constexpr int kFixed = 1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + 4 * 4 * BN + 1024;
+    static constexpr int kEpiWarps = kB128 ? 8 : 4;
+    static constexpr int kXbuf = FMT == FMT_PT ? 4 * 4 * BN : 0;  // the slots' scales, for each quarter of the channels
+    static constexpr int kFixed =
+        1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurn + 1024;
     static constexpr int kFit = (kMaxDynamicSmem - kFixed) / kStage;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
-    static constexpr int kAccCols = 2 * BN;
+    static constexpr int kAccs = kB128 ? 4 : 2;                   // accumulators
+    static constexpr int kAccCols = kAccs * BN;
     static constexpr int kScaleCols = kMx ? kScaleBufs * 4 * (1 + kHalves) : 0;
     static constexpr int kNeed = kAccCols + kScaleCols;
     static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
-    static constexpr int kEpiWarps = kB128 ? 8 : 4;
     static constexpr int kGatherWarp = 4 + kEpiWarps;             // first of the four
     static constexpr int kThreads = 32 * kGatherWarp;             // without the gather's
     static constexpr int kEpiCols = kB128 && BN >= 64 ? BN / 2 : BN;   // slots of an epilogue warp
@@ -100,6 +104,16 @@ struct Walk {
     }
 };
 
+// a * b + c of two floats in one instruction, each rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
 template <int FMT, int BN>
@@ -113,12 +127,13 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
     int* lo = reinterpret_cast<int*>(scales + kStages * (C::kSw + C::kSx));
     int* first = lo + kMaxGroups + 8;
     float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4 warps][BN]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(xbuf + 4 * BN);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    uint8_t* turns = reinterpret_cast<uint8_t*>(xbuf) + C::kXbuf;         // [epilogue warps][32 slots][32 channels]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(turns + C::kEpiWarps * kTurn);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 9);
     int* part = reinterpret_cast<int*>(misc + 4);                        // 16 ints
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, done = acc_empty + 32;
     const uint32_t tiles_at = tc::smem_addr(tiles), scales_at = tc::smem_addr(scales);
 
     const GroupGemmArgs& a = p.a;
@@ -131,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             tc::bar_init(full + 8 * i, 1 + (C::kMx || C::kB128 ? kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0));
             tc::bar_init(empty + 8 * i, C::kB128 ? 1 + C::kEpiWarps : 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kAccs; ++i) {
             tc::bar_init(acc_full + 8 * i, 1);
             tc::bar_init(acc_empty + 8 * i, C::kEpiWarps);
         }
@@ -208,9 +223,9 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             const int left = p.kbytes - (chunks - 1) * kChunk;
             const int last_steps = (left + 31) / 32;
             for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
-                const int buf = use & 1;
+                const int buf = use % C::kAccs;
                 if (C::kB128 || kc == 0) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + 8 * buf, ((use >> 1) & 1) ^ 1, stop));
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop));
                     if (!ok) break;
                 }
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full + 8 * st, ph, stop));
@@ -263,43 +278,62 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             uint32_t ph = 0;
             bool ok = true;
             const int64_t row_bytes = C::kMx ? p.kbytes / 32 : (int64_t)chunks * 4;
-            while (ok && walk.next()) {
-                const uint8_t* src[kRows];
+            // a tile's row indices are read during the tile before it, its first scales during that tile's last chunks
+            Walk ahead = walk;
+            int64_t row[kRows];
+            const uint8_t* src[kRows];
+            auto read_rows = [&]() {
+                const bool more = ahead.next();
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
                     const int c = u + i * kScaleThreads;
-                    int64_t r = c < walk.m ? (gather ? a.rows[walk.s0 + c] : walk.s0 + c) : -1;
-                    src[i] = r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.xs) + r * row_bytes : nullptr;
+                    row[i] = more && c < ahead.m ? (gather ? a.rows[ahead.s0 + c] : ahead.s0 + c) : -1;
                 }
+            };
+            auto sources = [&]() {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    src[i] = row[i] >= 0 && row[i] < a.x_rows ? static_cast<const uint8_t*>(a.xs) + row[i] * row_bytes : nullptr;
+            };
+            // four chunks' scales a row at a time, the next four in flight
+            uint32_t cur[kRows][4], nxt[kRows][4];
+            auto fetch = [&](uint32_t (&v)[kRows][4], int kc) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[i][q] = 0;
+                    if (!src[i]) continue;
+                    const uint8_t* s = src[i] + (int64_t)kc * 4;
+                    if (p.xs_align == 16) {
+                        const uint4 t = *reinterpret_cast<const uint4*>(s);
+                        v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+                    } else if (p.xs_align == 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (kc + q < chunks) v[i][q] = reinterpret_cast<const uint32_t*>(s)[q];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            if (kc * 4 + q < row_bytes) v[i][q / 4] |= (uint32_t)s[q] << (8 * (q % 4));
+                    }
+                }
+            };
+            read_rows();
+            sources();
+            fetch(cur, 0);
+            read_rows();
+            while (ok && walk.next()) {
                 const float* ws = C::kB128 ? static_cast<const float*>(a.ws) +
                                                  ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * chunks
                                            : nullptr;
-                // four chunks' scales a row at a time, the next four in flight
-                uint32_t cur[kRows][4], nxt[kRows][4];
-                auto fetch = [&](uint32_t (&v)[kRows][4], int kc) {
-#pragma unroll
-                    for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[i][q] = 0;
-                        if (!src[i]) continue;
-                        const uint8_t* s = src[i] + (int64_t)kc * 4;
-                        if (p.xs_align == 16) {
-                            const uint4 t = *reinterpret_cast<const uint4*>(s);
-                            v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
-                        } else if (p.xs_align == 4) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (kc + q < chunks) v[i][q] = reinterpret_cast<const uint32_t*>(s)[q];
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                if (kc * 4 + q < row_bytes) v[i][q / 4] |= (uint32_t)s[q] << (8 * (q % 4));
-                        }
-                    }
-                };
-                fetch(cur, 0);
                 for (int kc0 = 0; ok && kc0 < chunks; kc0 += 4) {
-                    if (kc0 + 4 < chunks) fetch(nxt, kc0 + 4);
+                    if (kc0 + 4 < chunks) {
+                        fetch(nxt, kc0 + 4);
+                    } else {
+                        sources();
+                        fetch(nxt, 0);
+                        read_rows();
+                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (kc0 + q >= chunks) break;
@@ -348,14 +382,26 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             if (++lag_st == kStages) lag_st = 0;
             --behind;
         };
-        while (ok && walk.next()) {
-            const uint8_t* src[kRows];
+        // a tile's row indices are read while the copies of the tile before it are issued
+        Walk ahead = walk;
+        int row[kRows];
+        auto read_rows = [&]() {
+            const bool more = ahead.next();
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 const int c = (u >> 3) + 16 * i;
-                const int64_t r = c < walk.m ? a.rows[walk.s0 + c] : -1;
-                src[i] = r >= 0 && r < a.x_rows ? static_cast<const uint8_t*>(a.x) + r * p.kbytes + piece * 16 : nullptr;
+                row[i] = more && c < ahead.m ? a.rows[ahead.s0 + c] : -1;
             }
+        };
+        read_rows();
+        while (ok && walk.next()) {
+            const uint8_t* src[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                src[i] = row[i] >= 0 && row[i] < a.x_rows
+                             ? static_cast<const uint8_t*>(a.x) + (int64_t)row[i] * p.kbytes + piece * 16
+                             : nullptr;
+            read_rows();
             for (int kc = 0; kc < chunks; ++kc) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                 if (!ok) break;
@@ -404,41 +450,59 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             }
             if (FMT == FMT_PT && n < a.N) wn = static_cast<const float*>(a.ws)[(int64_t)walk.g * a.N + n];
             __syncwarp();
-            uint16_t* out = a.out + (int64_t)walk.s0 * a.N + n;
-            // columns c0 .. c0 + 31 of the tile: rounded once and stored, channel by channel
+            // columns c0 .. c0 + 31 of the tile: rounded once, turned in shared
+            // memory from a channel a thread to rows of slots, stored in 16-byte
+            // pieces (as 2-byte stores of a channel a thread, 192 slots took 4.4 us)
+            uint8_t* turn = turns + (warp - 4) * kTurn;
             auto store = [&](int c0, uint32_t valid, const float (&v)[32]) {
+                __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const float r = (valid >> c) & 1 ? v[c] : 0.0f;
-                    const uint32_t b = p.f16 ? f32x2_to_f16x2(r, 0.0f) : f32x2_to_bf16x2(r, 0.0f);
-                    if (c0 + c < m && n < a.N) out[(int64_t)(c0 + c) * a.N] = (uint16_t)b;
+                    *reinterpret_cast<uint16_t*>(turn + c * 64 + lane * 2) =
+                        (uint16_t)(p.f16 ? f32x2_to_f16x2(r, 0.0f) : f32x2_to_bf16x2(r, 0.0f));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 8 * i + (lane >> 2), ch = walk.n0 + quarter * 32 + (lane & 3) * 8;
+                    if (c0 + c < m && ch < a.N)
+                        st16_if(a.out + (int64_t)(walk.s0 + c0 + c) * a.N + ch,
+                                *reinterpret_cast<const uint4*>(turn + c * 64 + (lane & 3) * 16), true);
                 }
             };
             if (C::kB128) {
-                float acc[C::kEpiCols];
+                float2 acc[C::kEpiCols / 2];
 #pragma unroll
-                for (int c = 0; c < C::kEpiCols; ++c) acc[c] = 0.0f;
+                for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
                 for (int kc = 0; kc < chunks; ++kc, ++use) {
-                    const int buf = use & 1;
-                    ok = tc::bar_wait(full + 8 * st, ph, stop) && tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop);
+                    const int buf = use % C::kAccs;
+                    ok = tc::bar_wait(full + 8 * st, ph, stop) && tc::bar_wait(acc_full + 8 * buf, (use / C::kAccs) & 1, stop);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc::fence_after();
                     const float4* s = reinterpret_cast<const float4*>(scales + st * (C::kSw + C::kSx)) + first_c / 4;
+                    // 16 columns at a time, the next 16 on their way from tensor memory
+                    if (first_c < m && !idle) {
+                        const uint32_t at = tmem + lanes + buf * BN + first_c;
+                        uint32_t v[2][16];
+                        tc::tmem_load16(at, v[0]);
+                        tc::tmem_load_wait(v[0]);
 #pragma unroll
-                    for (int c0 = 0; c0 < C::kEpiCols; c0 += 32) {
-                        if (first_c + c0 < m && !idle) {
-                            uint32_t v[32];
-                            tc::tmem_load32(tmem + lanes + buf * BN + first_c + c0, v);
-                            tc::tmem_load_wait(v);
+                        for (int c0 = 0; c0 < C::kEpiCols; c0 += 16) {
+                            uint32_t(&cur)[16] = v[(c0 / 16) & 1];
+                            uint32_t(&nxt)[16] = v[((c0 / 16) & 1) ^ 1];
+                            if (c0 + 16 < C::kEpiCols) tc::tmem_load16(at + c0 + 16, nxt);
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
+                            for (int c = 0; c < 16; c += 4) {
                                 const float4 f = s[(c0 + c) / 4];
-                                acc[c0 + c] = fmaf(__uint_as_float(v[c]), f.x, acc[c0 + c]);
-                                acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y, acc[c0 + c + 1]);
-                                acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z, acc[c0 + c + 2]);
-                                acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w, acc[c0 + c + 3]);
+                                float2* to = acc + (c0 + c) / 2;
+                                to[0] = fma2(make_float2(__uint_as_float(cur[c]), __uint_as_float(cur[c + 1])),
+                                             make_float2(f.x, f.y), to[0]);
+                                to[1] = fma2(make_float2(__uint_as_float(cur[c + 2]), __uint_as_float(cur[c + 3])),
+                                             make_float2(f.z, f.w), to[1]);
                             }
+                            if (c0 + 16 < C::kEpiCols) tc::tmem_load_wait(nxt);
                         }
                     }
                     tc::fence_before();
@@ -457,12 +521,12 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                 for (int c0 = 0; c0 < C::kEpiCols; c0 += 32) {
                     float v[32];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = acc[c0 + c];
+                    for (int c = 0; c < 32; ++c) v[c] = c & 1 ? acc[(c0 + c) / 2].y : acc[(c0 + c) / 2].x;
                     if (first_c + c0 < m && !idle) store(first_c + c0, there[(first_c + c0) / 32], v);
                 }
             } else {
-                const int buf = use & 1;
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
+                const int buf = use % C::kAccs;
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use / C::kAccs) & 1, stop));
                 if (!ok) break;
                 ++use;
                 tc::fence_after();
