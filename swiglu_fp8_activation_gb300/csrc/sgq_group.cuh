@@ -69,6 +69,9 @@ struct LoraArgs {
 // swizzle, zeros outside. False when the driver refuses it.
 bool encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, int box_rows);
 
+// `tiles` pieces of 512 bytes, one below the other, box one piece, no swizzle.
+bool encode_tiles512(CUtensorMap* m, const void* base, int64_t tiles);
+
 // Bytes of a row of lora_add's workspace: two parts of R 16-bit values, then
 // the row's factor (fp32) and 12 bytes of zeros.
 __host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }

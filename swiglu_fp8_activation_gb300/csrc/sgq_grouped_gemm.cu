@@ -46,7 +46,8 @@ constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
 
 struct alignas(128) GemmParams {
     CUtensorMap mw;                // w as bytes [groups][N][K], box 128 x 128 rows
-    CUtensorMap mx;                // x as bytes [x_rows][K], box 128 x BN rows (not used with row indices)
+    CUtensorMap mx;                // x as bytes [x_rows][K], box 128 x a CTA's slots (not used with row indices)
+    CUtensorMap ms;                // MXFP8: w_scale as tiles of 512 bytes
     GroupGemmArgs a;
     int n_tiles;                   // tiles of 128 channels
     int chunks;                    // chunks of K
@@ -55,16 +56,18 @@ struct alignas(128) GemmParams {
     int xs_align;                  // 16, 4 or 1: alignment of every 4-byte (4 chunks: 16-byte) piece of x_scale
 };
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR>
 struct Cfg {
     static constexpr bool kMx = FMT == FMT_MX, kB128 = FMT == FMT_B128;
-    static constexpr int kW = kM * kChunk, kX = BN * kChunk;
+    static constexpr int kXRows = PAIR ? BN / 2 : BN;             // slots whose rows a CTA holds
+    static constexpr int kW = kM * kChunk, kX = kXRows * kChunk;
     static constexpr int kHalves = (BN + 127) / 128;              // 128-slot pieces of the slots' scales
     static constexpr int kSw = kMx ? 512 : 0;                     // weights' scales of a chunk
-    static constexpr int kSx = kMx ? 512 * kHalves : kB128 ? 4 * BN : 0;
+    static constexpr int kSx = kMx ? 512 * kHalves : 0;           // slots' scales of a chunk
     static constexpr int kStage = kW + kX + kSw + kSx;
     static constexpr int kEpiWarps = kB128 ? 8 : 4;
-    static constexpr int kXbuf = FMT == FMT_PT ? 4 * 4 * BN : 0;  // the slots' scales, for each quarter of the channels
+    // fp32 scales of the slots: for each quarter of the channels, or for each accumulator
+    static constexpr int kXbuf = FMT == FMT_PT || kB128 ? 4 * 4 * BN : 0;
     static constexpr int kFixed =
         1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurn + 1024;
     static constexpr int kFit = (kMaxDynamicSmem - kFixed) / kStage;
@@ -86,20 +89,21 @@ struct Cfg {
 struct Walk {
     const int* lo;
     const int* first;
-    int G, n_tiles, bn;
+    int n_tiles, bn, ctas, rank;     // tiles of `ctas` x 128 channels, this CTA's being the rank-th 128
     int64_t tile, end;
     int g, s0, m, n0;
 
-    __device__ Walk(const int* lo_, const int* first_, int G_, int n_tiles_, int bn_)
-        : lo(lo_), first(first_), G(G_), n_tiles(n_tiles_), bn(bn_), tile(blockIdx.x), end((int64_t)first_[G_] * n_tiles_), g(0) {}
+    __device__ Walk(const int* lo_, const int* first_, int G, int n_tiles_, int bn_, int ctas_)
+        : lo(lo_), first(first_), n_tiles((n_tiles_ + ctas_ - 1) / ctas_), bn(bn_), ctas(ctas_), rank((int)(blockIdx.x % ctas_)),
+          tile(blockIdx.x / ctas_), end((int64_t)first_[G] * n_tiles), g(0) {}
     __device__ bool next() {
         if (tile >= end) return false;
         const int q = (int)(tile / n_tiles);
         while (first[g + 1] <= q) ++g;
         s0 = lo[g] + (q - first[g]) * bn;
         m = min(bn, lo[g + 1] - s0);
-        n0 = (int)(tile % n_tiles) * kM;
-        tile += gridDim.x;
+        n0 = ((int)(tile % n_tiles) * ctas + rank) * kM;
+        tile += gridDim.x / ctas;
         return true;
     }
 };
@@ -116,9 +120,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
-template <int FMT, int BN>
-__global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
-    using C = Cfg<FMT, BN>;
+template <int FMT, int BN, bool PAIR>
+__global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads, 1)
+    grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
+    using C = Cfg<FMT, BN, PAIR>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
@@ -126,14 +131,14 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
     uint8_t* scales = smem + kStages * (C::kW + C::kX);
     int* lo = reinterpret_cast<int*>(scales + kStages * (C::kSw + C::kSx));
     int* first = lo + kMaxGroups + 8;
-    float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4 warps][BN]
+    float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4][BN]
     uint8_t* turns = reinterpret_cast<uint8_t*>(xbuf) + C::kXbuf;         // [epilogue warps][32 slots][32 channels]
     uint64_t* bars = reinterpret_cast<uint64_t*>(turns + C::kEpiWarps * kTurn);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 9);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 13);
     int* part = reinterpret_cast<int*>(misc + 4);                        // 16 ints
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, done = acc_empty + 32;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, xs_empty = acc_empty + 32, done = xs_empty + 32;
     const uint32_t tiles_at = tc::smem_addr(tiles), scales_at = tc::smem_addr(scales);
 
     const GroupGemmArgs& a = p.a;
@@ -143,30 +148,48 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::bar_init(full + 8 * i, 1 + (C::kMx || C::kB128 ? kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0));
-            tc::bar_init(empty + 8 * i, C::kB128 ? 1 + C::kEpiWarps : 1);
+            // the copies' thread and the warps that write scales or rows (in a pair, of both CTAs)
+            const int writers = (C::kMx ? kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0);
+            tc::bar_init(full + 8 * i, 1 + (PAIR ? 2 : 1) * writers);
+            tc::bar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < C::kAccs; ++i) {
-            tc::bar_init(acc_full + 8 * i, 1);
-            tc::bar_init(acc_empty + 8 * i, C::kEpiWarps);
+            tc::bar_init(acc_full + 8 * i, 1 + (C::kB128 ? kScaleThreads / 32 : 0));
+            tc::bar_init(acc_empty + 8 * i, (PAIR ? 2 : 1) * C::kEpiWarps);
+            tc::bar_init(xs_empty + 8 * i, C::kEpiWarps);
         }
         tc::bar_init(done, 1);
         tc::fence_barrier_init();
         *stop = 0;
         tc::prefetch_map(&p.mw);
         tc::prefetch_map(&p.mx);
+        if (C::kMx) tc::prefetch_map(&p.ms);
     }
-    if (warp == 2) tc::tmem_alloc(tc::smem_addr(misc), C::kCols);
+    if (warp == 2) tc::tmem_alloc<PAIR>(tc::smem_addr(misc), C::kCols);
     pdl_wait();
     scan_groups(a.offsets, a.groups, a.S, BN, lo, first, part);
     tc::fence_before();
     __syncthreads();
+    if (PAIR) {                      // the other's barriers and tensor memory are there
+        cluster_arrive();
+        cluster_wait();
+    }
     tc::fence_after();
     // a next launch that holds tensor memory while it waits for this one may
     // start only now that this CTA has its own
     pdl_trigger();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
-    Walk walk(lo, first, a.groups, p.n_tiles, BN);
+    Walk walk(lo, first, a.groups, p.n_tiles, BN, PAIR ? 2 : 1);
+    // In a pair the first CTA issues the products: what makes a stage full, and
+    // an accumulator free, arrives at its barriers, and the products' ends at both CTAs'.
+    const bool leader = !PAIR || walk.rank == 0;
+    const uint32_t full_at = PAIR ? tc::at_rank(full, 0) : full, acc_empty_at = PAIR ? tc::at_rank(acc_empty, 0) : acc_empty;
+    auto arrive = [&](uint32_t bar) {
+        if (PAIR) tc::bar_arrive_cluster(bar);
+        else tc::bar_arrive(bar);
+    };
+    // slots of a tile whose rows this CTA holds: the product's N, a multiple of 16 a CTA, half each in a pair
+    auto columns = [](int m) { return PAIR ? (m + 31) & ~31 : (m + 15) & ~15; };
 
     if (warp == 0) {
         // ---------------------------------------------------------- copies
@@ -174,21 +197,20 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         uint32_t ph = 0;
         bool ok = true;
         int64_t issued = 0;
-        const int scale_tiles = C::kMx ? (p.kbytes / 32 + 3) / 4 : 0;
         while (ok && walk.next()) {
-            const uint8_t* ws = static_cast<const uint8_t*>(a.ws) +
-                                ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * scale_tiles * 512;
-            const uint32_t bytes = C::kW + C::kSw + (gather ? 0 : C::kX);
+            const int scale_row = (walk.g * p.n_tiles + min(walk.n0 / kM, p.n_tiles - 1)) * chunks;
+            const uint32_t bytes = (PAIR ? 2 : 1) * (C::kW + C::kSw + (gather ? 0 : C::kX));
+            const int s0 = walk.s0 + walk.rank * (columns(walk.m) / 2);
             for (int kc = 0; kc < chunks; ++kc) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                 if (!ok) break;
                 const uint32_t w_at = tiles_at + st * (C::kW + C::kX), x_at = w_at + C::kW;
-                const uint32_t bar = full + 8 * st;
+                const uint32_t bar = full_at + 8 * st;
                 if (tc::elect()) {
-                    tc::bar_arrive_expect(bar, bytes);
-                    tc::load_3d(w_at, &p.mw, bar, kc * kChunk, walk.n0, walk.g);
-                    if (C::kMx) tc::load_bulk(scales_at + st * (C::kSw + C::kSx), ws + (int64_t)kc * 512, 512, bar);
-                    if (!gather) tc::load_2d(x_at, &p.mx, bar, kc * kChunk, walk.s0);
+                    if (leader) tc::bar_arrive_expect(full + 8 * st, bytes);
+                    tc::load_3d<PAIR>(w_at, &p.mw, bar, kc * kChunk, walk.n0, walk.g);
+                    if (C::kMx) tc::load_2d<PAIR>(scales_at + st * (C::kSw + C::kSx), &p.ms, bar, 0, scale_row + kc);
+                    if (!gather) tc::load_2d<PAIR>(x_at, &p.mx, bar, kc * kChunk, s0);
                 }
                 ++issued;
                 if (++st == kStages) {
@@ -197,7 +219,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                 }
             }
         }
-        if (!ok && lane == 0) {
+        if (!ok && lane == 0 && leader) {
             // gave up: wait (a while) for the copies in flight before the block's memory goes
             uint32_t never = 0;
             for (int i = 0; i < kStages && i < issued; ++i) {
@@ -213,25 +235,33 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         // -------------------------------------------------------- products
         int st = 0, use = 0;
         uint32_t ph = 0, chunk_no = 0;
-        bool ok = true;
-        while (ok && walk.next()) {
-            const uint32_t n = (uint32_t)(walk.m + 15) & ~15u;
+        bool ok = true, ready = false;
+        while (ok && leader && walk.next()) {
+            const uint32_t n = (uint32_t)columns(walk.m);
+            constexpr int kRows = PAIR ? 2 * kM : kM;
             uint32_t idesc;
-            if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kM >> 7) << 27);
-            else idesc = (1u << 4) | ((n >> 3) << 17) | ((kM >> 4) << 24);
+            if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kRows >> 7) << 27);
+            else idesc = (1u << 4) | ((n >> 3) << 17) | ((kRows >> 4) << 24);
             if (FMT == FMT_16BIT && !p.f16) idesc |= (1u << 7) | (1u << 10);
             const int left = p.kbytes - (chunks - 1) * kChunk;
             const int last_steps = (left + 31) / 32;
             for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
                 const int buf = use % C::kAccs;
-                if (C::kB128 || kc == 0) {
-                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop));
+                if (!ready) {
+                    ok = true;
+                    if (C::kB128 || kc == 0) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
+                    ok = __all_sync(0xFFFFFFFFu, ok && tc::bar_wait<PAIR>(full + 8 * st, ph, stop));
                     if (!ok) break;
                 }
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full + 8 * st, ph, stop));
-                if (!ok) break;
                 tc::fence_after();
                 const bool done_acc = C::kB128 || kc == chunks - 1;
+                const int next_st = st + 1 == kStages ? 0 : st + 1;
+                const uint32_t next_ph = ph ^ (next_st == 0);
+                // whether the next chunk can follow at once: asked for now, so that
+                // the answer (90 cycles) is there when this chunk's products are issued
+                bool next_ready = tc::bar_test<PAIR>(full + 8 * next_st, next_ph);
+                if (C::kB128 || kc == chunks - 1)
+                    next_ready &= tc::bar_test<PAIR>(acc_empty + 8 * ((use + 1) % C::kAccs), (((use + 1) / C::kAccs) & 1) ^ 1);
                 if (tc::elect()) {
                     const uint32_t w_at = tiles_at + st * (C::kW + C::kX);
                     const uint64_t dw = tc::desc_sw128(w_at), dx = tc::desc_sw128(w_at + C::kW);
@@ -239,33 +269,32 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                     const uint32_t sw = tmem + C::kAccCols + (chunk_no % kScaleBufs) * 4 * (1 + C::kHalves), sx = sw + 4;
                     if (C::kMx) {
                         const uint32_t s_at = scales_at + st * (C::kSw + C::kSx);
-                        tc::copy_scales(sw, tc::desc_rows16(s_at));
+                        tc::copy_scales<PAIR>(sw, tc::desc_rows16(s_at));
 #pragma unroll
-                        for (int h = 0; h < C::kHalves; ++h) tc::copy_scales(sx + 4 * h, tc::desc_rows16(s_at + 512 + 512 * h));
+                        for (int h = 0; h < C::kHalves; ++h)
+                            tc::copy_scales<PAIR>(sx + 4 * h, tc::desc_rows16(s_at + 512 + 512 * h));
                     }
                     const int steps = kc == chunks - 1 ? last_steps : 4;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t add = k > 0 || (!C::kB128 && kc > 0);
                         if (k >= steps) break;
-                        if (C::kMx) tc::mma_mx8(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
-                        else if (FMT == FMT_16BIT) tc::mma_f16(d, dw + 2 * k, dx + 2 * k, idesc, add);
-                        else tc::mma_f8(d, dw + 2 * k, dx + 2 * k, idesc, add);
+                        if (C::kMx) tc::mma_mx8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
+                        else if (FMT == FMT_16BIT) tc::mma_f16<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
+                        else tc::mma_f8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
                     }
-                    tc::commit(empty + 8 * st);
-                    if (done_acc) tc::commit(acc_full + 8 * buf);
+                    tc::commit<PAIR>(empty + 8 * st);
+                    if (done_acc) tc::commit<PAIR>(acc_full + 8 * buf);
                 }
-                __syncwarp();
+                ready = __all_sync(0xFFFFFFFFu, next_ready);
                 use += done_acc;
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
+                st = next_st;
+                ph = next_ph;
             }
         }
         if (!ok) {
             uint32_t never = 0;
-            if (tc::elect()) tc::commit(done);
+            if (tc::elect()) tc::commit<PAIR>(done);
             __syncwarp();
             tc::bar_wait(done, 0, &never, 1 << 27);
         }
@@ -274,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         if (C::kMx || C::kB128) {
             constexpr int kRows = (BN + kScaleThreads - 1) / kScaleThreads;
             const int u = tid - 64;
-            int st = 0;
+            int st = 0, use = 0;
             uint32_t ph = 0;
             bool ok = true;
             const int64_t row_bytes = C::kMx ? p.kbytes / 32 : (int64_t)chunks * 4;
@@ -282,6 +311,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             Walk ahead = walk;
             int64_t row[kRows];
             const uint8_t* src[kRows];
+            const float *ws = nullptr, *next_ws = nullptr;
             auto read_rows = [&]() {
                 const bool more = ahead.next();
 #pragma unroll
@@ -289,15 +319,24 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                     const int c = u + i * kScaleThreads;
                     row[i] = more && c < ahead.m ? (gather ? a.rows[ahead.s0 + c] : ahead.s0 + c) : -1;
                 }
+                next_ws = C::kB128 && more ? static_cast<const float*>(a.ws) +
+                                                 ((int64_t)ahead.g * p.n_tiles + min(ahead.n0 / kM, p.n_tiles - 1)) * chunks
+                                           : nullptr;
             };
             auto sources = [&]() {
+                ws = next_ws;
 #pragma unroll
                 for (int i = 0; i < kRows; ++i)
                     src[i] = row[i] >= 0 && row[i] < a.x_rows ? static_cast<const uint8_t*>(a.xs) + row[i] * row_bytes : nullptr;
             };
             // four chunks' scales a row at a time, the next four in flight
             uint32_t cur[kRows][4], nxt[kRows][4];
-            auto fetch = [&](uint32_t (&v)[kRows][4], int kc) {
+            float cur_w[4], nxt_w[4];                                    // 1x128: the weights' scales of the same chunks
+            auto fetch = [&](uint32_t (&v)[kRows][4], float (&w)[4], int kc) {
+                if (C::kB128) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = ws && kc + q < chunks ? ws[kc + q] : 0.0f;
+                }
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) {
 #pragma unroll
@@ -320,27 +359,25 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
             };
             read_rows();
             sources();
-            fetch(cur, 0);
+            fetch(cur, cur_w, 0);
             read_rows();
             while (ok && walk.next()) {
-                const float* ws = C::kB128 ? static_cast<const float*>(a.ws) +
-                                                 ((int64_t)walk.g * p.n_tiles + walk.n0 / kM) * chunks
-                                           : nullptr;
                 for (int kc0 = 0; ok && kc0 < chunks; kc0 += 4) {
                     if (kc0 + 4 < chunks) {
-                        fetch(nxt, kc0 + 4);
+                        fetch(nxt, nxt_w, kc0 + 4);
                     } else {
                         sources();
-                        fetch(nxt, 0);
+                        fetch(nxt, nxt_w, 0);
                         read_rows();
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (kc0 + q >= chunks) break;
-                        const float w = C::kB128 ? ws[kc0 + q] : 0.0f;
-                        ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
+                        const int buf = use % C::kAccs;
+                        ok = __all_sync(0xFFFFFFFFu, C::kMx ? tc::bar_wait(empty + 8 * st, ph ^ 1, stop)
+                                                            : tc::bar_wait(xs_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop));
                         if (!ok) break;
-                        uint8_t* dst = scales + st * (C::kSw + C::kSx) + C::kSw;
+                        uint8_t* dst = C::kMx ? scales + st * (C::kSw + C::kSx) + C::kSw : reinterpret_cast<uint8_t*>(xbuf + buf * BN);
 #pragma unroll
                         for (int i = 0; i < kRows; ++i) {
                             const int c = u + i * kScaleThreads;
@@ -348,28 +385,34 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                                 if (C::kMx)
                                     *reinterpret_cast<uint32_t*>(dst + (c >> 7) * 512 + (c & 31) * 16 + ((c >> 5) & 3) * 4) = cur[i][q];
                                 else
-                                    *reinterpret_cast<float*>(dst + 4 * c) = __uint_as_float(cur[i][q]) * w;
+                                    *reinterpret_cast<float*>(dst + 4 * c) = __uint_as_float(cur[i][q]) * cur_w[q];
                             }
                         }
-                        tc::fence_async_smem();
+                        if (C::kMx) tc::fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) tc::bar_arrive(full + 8 * st);
+                        if (lane == 0) {
+                            if (C::kMx) arrive(full_at + 8 * st);
+                            else tc::bar_arrive(acc_full + 8 * buf);
+                        }
+                        ++use;
                         if (++st == kStages) {
                             st = 0;
                             ph ^= 1;
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < kRows; ++i)
+                    for (int q = 0; q < 4; ++q) {
+                        if (C::kB128) cur_w[q] = nxt_w[q];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) cur[i][q] = nxt[i][q];
+                        for (int i = 0; i < kRows; ++i) cur[i][q] = nxt[i][q];
+                    }
                 }
             }
         }
     } else if (warp >= C::kGatherWarp) {
         // ------------------------------------------- gathered rows of the slots
         // thread u copies 16-byte piece u % 8 of rows u / 8 + 16 i of the chunk
-        constexpr int kRows = BN / 16;
+        constexpr int kRows = C::kXRows / 16;
         const int u = tid - 32 * C::kGatherWarp, piece = u & 7;
         int st = 0, lag_st = 0;
         uint32_t ph = 0;
@@ -378,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         auto hand_over = [&]() {
             tc::fence_async_smem();
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(full + 8 * lag_st);
+            if (lane == 0) arrive(full_at + 8 * lag_st);
             if (++lag_st == kStages) lag_st = 0;
             --behind;
         };
@@ -387,10 +430,11 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         int row[kRows];
         auto read_rows = [&]() {
             const bool more = ahead.next();
+            const int n = more ? columns(ahead.m) : 0, from = PAIR ? ahead.rank * (n / 2) : 0, to = PAIR ? min(ahead.m, from + n / 2) : ahead.m;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const int c = (u >> 3) + 16 * i;
-                row[i] = more && c < ahead.m ? a.rows[ahead.s0 + c] : -1;
+                const int c = from + (u >> 3) + 16 * i;
+                row[i] = more && c < to ? a.rows[ahead.s0 + c] : -1;
             }
         };
         read_rows();
@@ -431,8 +475,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
         const int first_c = C::kB128 && BN >= 64 ? ((warp - 4) >> 2) * C::kEpiCols : 0;   // this warp's slots of a tile
         const bool idle = C::kB128 && BN < 64 && warp >= 8;
         float* xrow = xbuf + quarter * BN;
-        int use = 0, st = 0;
-        uint32_t ph = 0;
+        int use = 0;
         bool ok = true;
         while (ok && walk.next()) {
             const int n = walk.n0 + quarter * 32 + lane;
@@ -475,46 +518,57 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                 float2 acc[C::kEpiCols / 2];
 #pragma unroll
                 for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+                // 16 columns at a time, the next 16 on their way from tensor
+                // memory, the next chunk's first ones too
+                const bool busy = first_c < m && !idle;
+                const uint32_t at = tmem + lanes + first_c;
+                uint32_t v[2][16];
+                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * (use % C::kAccs), (use / C::kAccs) & 1, stop));
+                if (!ok) break;
+                tc::fence_after();
+                if (busy) tc::tmem_load16(at + (use % C::kAccs) * BN, v[0]);
                 for (int kc = 0; kc < chunks; ++kc, ++use) {
-                    const int buf = use % C::kAccs;
-                    ok = tc::bar_wait(full + 8 * st, ph, stop) && tc::bar_wait(acc_full + 8 * buf, (use / C::kAccs) & 1, stop);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tc::fence_after();
-                    const float4* s = reinterpret_cast<const float4*>(scales + st * (C::kSw + C::kSx)) + first_c / 4;
-                    // 16 columns at a time, the next 16 on their way from tensor memory
-                    if (first_c < m && !idle) {
-                        const uint32_t at = tmem + lanes + buf * BN + first_c;
-                        uint32_t v[2][16];
-                        tc::tmem_load16(at, v[0]);
-                        tc::tmem_load_wait(v[0]);
+                    const int buf = use % C::kAccs, next = (use + 1) % C::kAccs;
+                    // this chunk's scales as they are now: their place is free once the accumulator is
+                    const float4* s = reinterpret_cast<const float4*>(xbuf + buf * BN + first_c);
 #pragma unroll
-                        for (int c0 = 0; c0 < C::kEpiCols; c0 += 16) {
-                            uint32_t(&cur)[16] = v[(c0 / 16) & 1];
-                            uint32_t(&nxt)[16] = v[((c0 / 16) & 1) ^ 1];
-                            if (c0 + 16 < C::kEpiCols) tc::tmem_load16(at + c0 + 16, nxt);
+                    for (int c0 = 0; c0 < C::kEpiCols; c0 += 16) {
+                        uint32_t(&cur)[16] = v[(c0 / 16) & 1];
+                        uint32_t(&nxt)[16] = v[((c0 / 16) & 1) ^ 1];
+                        float4 f[4];
+                        if (busy) {
+                            tc::tmem_load_wait(cur);
 #pragma unroll
-                            for (int c = 0; c < 16; c += 4) {
-                                const float4 f = s[(c0 + c) / 4];
-                                float2* to = acc + (c0 + c) / 2;
-                                to[0] = fma2(make_float2(__uint_as_float(cur[c]), __uint_as_float(cur[c + 1])),
-                                             make_float2(f.x, f.y), to[0]);
-                                to[1] = fma2(make_float2(__uint_as_float(cur[c + 2]), __uint_as_float(cur[c + 3])),
-                                             make_float2(f.z, f.w), to[1]);
+                            for (int c = 0; c < 4; ++c) f[c] = s[c0 / 4 + c];
+                        }
+                        if (c0 + 16 < C::kEpiCols) {
+                            if (busy) tc::tmem_load16(at + buf * BN + c0 + 16, nxt);
+                        } else {
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                arrive(acc_empty_at + 8 * buf);
+                                tc::bar_arrive(xs_empty + 8 * buf);
                             }
-                            if (c0 + 16 < C::kEpiCols) tc::tmem_load_wait(nxt);
+                            if (kc + 1 < chunks) {
+                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * next, ((use + 1) / C::kAccs) & 1, stop));
+                                if (!ok) break;
+                                tc::fence_after();
+                                if (busy) tc::tmem_load16(at + next * BN, nxt);
+                            }
+                        }
+                        if (busy) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float2* to = acc + c0 / 2 + 2 * c;
+                                to[0] = fma2(make_float2(__uint_as_float(cur[4 * c]), __uint_as_float(cur[4 * c + 1])),
+                                             make_float2(f[c].x, f[c].y), to[0]);
+                                to[1] = fma2(make_float2(__uint_as_float(cur[4 * c + 2]), __uint_as_float(cur[4 * c + 3])),
+                                             make_float2(f[c].z, f[c].w), to[1]);
+                            }
                         }
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::bar_arrive(acc_empty + 8 * buf);
-                        tc::bar_arrive(empty + 8 * st);
-                    }
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1;
-                    }
+                    if (!ok) break;
                 }
                 if (!ok) break;
 #pragma unroll
@@ -547,33 +601,39 @@ __global__ void __launch_bounds__(Cfg<FMT, BN>::kThreads + kGatherThreads, 1) gr
                 }
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+                if (lane == 0) arrive(acc_empty_at + 8 * buf);
             }
         }
     }
     tc::fence_before();
     __syncthreads();
+    if (PAIR) {                      // the other may still arrive here, or read this CTA's operands
+        cluster_arrive();
+        cluster_wait();
+    }
     tc::fence_after();
-    if (warp == 2) tc::tmem_free(tmem, C::kCols);
+    if (warp == 2) tc::tmem_free<PAIR>(tmem, C::kCols);
     if (tid == 0 && *stop) atomicAdd(&g_gave_up, 1);
 }
 
 // --------------------------------------------------------------------- host
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR = false>
 cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
-    using C = Cfg<FMT, BN>;
+    using C = Cfg<FMT, BN, PAIR>;
     const GroupGemmArgs& a = p.a;
     const cuuint64_t wd[3] = {(cuuint64_t)p.kbytes, (cuuint64_t)a.N, (cuuint64_t)a.groups};
     // with no row of x at all nothing of it is used: any memory serves as its map
     const cuuint64_t xd[2] = {(cuuint64_t)p.kbytes, (cuuint64_t)(a.x_rows ? a.x_rows : 1)};
-    if (!encode_rows(&p.mw, a.w, 3, wd, kM) || !encode_rows(&p.mx, a.x_rows ? a.x : a.w, 2, xd, BN))
+    if (!encode_rows(&p.mw, a.w, 3, wd, kM) || !encode_rows(&p.mx, a.x_rows ? a.x : a.w, 2, xd, C::kXRows))
         return cudaErrorInvalidValue;
-    const int64_t most = ((int64_t)a.S / BN + (a.S < a.groups ? a.S : a.groups)) * p.n_tiles;   // tiles at most
-    const int64_t grid = most < dev.sms ? most : dev.sms > 0 ? dev.sms : 1;
-    return launch_grid(grouped_gemm_kernel<FMT, BN>, dim3((unsigned)(grid > 0 ? grid : 1)), C::kThreads + (a.rows ? kGatherThreads : 0),
-                       C::kSmem, 1, dev.id, p,
-                       stream);
+    if (C::kMx && !encode_tiles512(&p.ms, a.ws, (int64_t)a.groups * p.n_tiles * p.chunks)) return cudaErrorInvalidValue;
+    constexpr int kCtas = PAIR ? 2 : 1;
+    // tiles at most
+    const int64_t most = ((int64_t)a.S / BN + (a.S < a.groups ? a.S : a.groups)) * ((p.n_tiles + kCtas - 1) / kCtas);
+    const int64_t room = dev.sms >= kCtas ? dev.sms / kCtas : 1, tiles = most < room ? most : room;
+    return launch_grid(grouped_gemm_kernel<FMT, BN, PAIR>, dim3((unsigned)(tiles * kCtas)),
+                       C::kThreads + (a.rows ? kGatherThreads : 0), C::kSmem, kCtas, dev.id, p, stream);
 }
 
 template <int FMT>
@@ -581,8 +641,8 @@ cudaError_t pick(const Device& dev, GemmParams& p, cudaStream_t stream) {
     const int64_t mean = ((int64_t)p.a.S + p.a.groups - 1) / p.a.groups;
     if (mean <= 24) return run<FMT, 32>(dev, p, stream);
     if (mean <= 64) return run<FMT, 64>(dev, p, stream);
-    if (FMT == FMT_B128 || mean <= 128) return run<FMT, 128>(dev, p, stream);
-    return run<FMT, FMT == FMT_B128 ? 128 : 192>(dev, p, stream);
+    if (FMT == FMT_B128 || mean <= 128 || p.n_tiles < 2) return run<FMT, 128>(dev, p, stream);
+    return run<FMT, FMT == FMT_B128 ? 128 : FMT == FMT_MX ? 224 : 256, FMT != FMT_B128>(dev, p, stream);
 }
 
 }  // namespace

@@ -35,4 +35,14 @@ bool encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* d
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tiles512(CUtensorMap* m, const void* base, int64_t tiles) {
+    const EncodeTiled f = encoder();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)tiles}, strides[1] = {512};
+    const cuuint32_t box[2] = {128, 1}, step[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace sgq

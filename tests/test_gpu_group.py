@@ -177,6 +177,18 @@ def test_grouped_gemm_many_rows(fmt):
     run_gemm(fmt, [700, 1, 1300, 0, 255], 512, 512)
 
 
+@pytest.mark.parametrize("sizes,N,units", [([300], 256, 4), ([257, 0, 140, 500], 136, 5), ([130, 400, 1], 264, 9), ([1000, 16, 33], 640, 33)], ids=str)
+@pytest.mark.parametrize("gather", [None, some_rows, wild_rows], ids=["rows in order", "gathered", "rows outside"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_gemm_large_groups(fmt, sizes, N, units, gather):
+    run_gemm(fmt, sizes, N, units * ref.UNIT[fmt] if fmt != "none" else units * 24, gather=gather, lead=2, tail=5)
+
+
+def test_grouped_gemm_large_groups_long_products():
+    for fmt in FMTS:
+        run_gemm(fmt, [290, 31], 384, 6144, gather=some_rows)
+
+
 def test_grouped_gemm_padding_of_w_scale_is_not_read_into_the_result():
     """Codes behind N and behind K/32 in the scales' padding hold NaN codes (255)."""
     sizes, N, K = [9, 200], 72, 96
