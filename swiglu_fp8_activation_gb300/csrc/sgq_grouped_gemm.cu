@@ -18,16 +18,20 @@
 //   1     the products (one thread), four instructions of 32 bytes of K a chunk
 //   2, 3  the slots' scales (MXFP8 and 1x128): row-major in memory, written
 //         into the operand's layout in shared memory
-//   4-7   the epilogue, one quarter of the channels each; with 1x128 scales
-//         4-11, half of the slots each
+//   4-7   the epilogue, one quarter of the channels each (with 1x128 scales
+//         4-11, one quarter of the slots and half of the channels each)
 //   last 4  with row indices: the slots' rows, gathered in 16-byte
 //         asynchronous copies into the swizzled layout. (TMA's four-row gather
 //         took 76 cycles an instruction of 512 bytes: 32768 MXFP8 rows of N =
 //         4096, K = 6144 ran in 3687 us with it.)
 // Two accumulators in tensor memory let the epilogue of one tile run under
 // the products of the next. With 1x128 scales, which fp32 holds and no block
-// scale of the tensor core can, every chunk is its own accumulator and the
-// epilogue warps sum the chunks in registers, scaled.
+// scale of the tensor core can, every chunk is its own accumulator (two pairs)
+// and the epilogue warps sum the chunks in registers, scaled. There the slots
+// are the M side: a lane is a slot, whose scale (times the weights', one for
+// all 128 channels) is one register. With the channels as lanes every thread
+// had to read every slot's scale from shared memory for each chunk, 512 cycles
+// a chunk by itself (32768 rows, N = 4096, K = 6144: 1381 us).
 #include <stddef.h>
 
 #include "sgq_group.cuh"
@@ -42,6 +46,7 @@ constexpr int kGatherThreads = 128;
 constexpr int kM = 128;            // channels a tile
 constexpr int kScaleThreads = 64;
 constexpr int kTurn = 32 * 64;       // bytes in which an epilogue warp turns 32 slots x 32 channels
+constexpr int kTurnPitch = 80;       // ... with 1x128 scales in rows of 64 + 16 bytes, free of bank conflicts
 constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
 
 struct alignas(128) GemmParams {
@@ -68,18 +73,19 @@ struct Cfg {
     static constexpr int kEpiWarps = kB128 ? 8 : 4;
     // fp32 scales of the slots: for each quarter of the channels, or for each accumulator
     static constexpr int kXbuf = FMT == FMT_PT || kB128 ? 4 * 4 * BN : 0;
+    static constexpr int kTurnBytes = kB128 ? 32 * kTurnPitch : kTurn;
     static constexpr int kFixed =
-        1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurn + 1024;
+        1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurnBytes + (kB128 && BN < kM ? (kM - BN) * kChunk : 0) + 1024;
     static constexpr int kFit = (kMaxDynamicSmem - kFixed) / kStage;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
-    static constexpr int kAccs = kB128 ? 4 : 2;                   // accumulators
-    static constexpr int kAccCols = kAccs * BN;
+    static constexpr int kAccs = 2;                               // accumulators
+    static constexpr int kAccWidth = kB128 ? 2 * kM : BN;         // columns of one: two chunks' channels, or slots
+    static constexpr int kAccCols = kAccs * kAccWidth;
     static constexpr int kScaleCols = kMx ? kScaleBufs * 4 * (1 + kHalves) : 0;
     static constexpr int kNeed = kAccCols + kScaleCols;
     static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static constexpr int kGatherWarp = 4 + kEpiWarps;             // first of the four
     static constexpr int kThreads = 32 * kGatherWarp;             // without the gather's
-    static constexpr int kEpiCols = kB128 && BN >= 64 ? BN / 2 : BN;   // slots of an epilogue warp
     static constexpr int kBehind = kStages / 2;                   // chunks of a gather's copies in flight
     static constexpr int kSmem = kFixed + kStages * kStage;
     static_assert(kNeed <= 512 && kStages >= 3, "tile too large");
@@ -108,16 +114,6 @@ struct Walk {
     }
 };
 
-// a * b + c of two floats in one instruction, each rounded once.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
 template <int FMT, int BN, bool PAIR>
@@ -133,12 +129,12 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
     int* first = lo + kMaxGroups + 8;
     float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4][BN]
     uint8_t* turns = reinterpret_cast<uint8_t*>(xbuf) + C::kXbuf;         // [epilogue warps][32 slots][32 channels]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(turns + C::kEpiWarps * kTurn);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 13);
-    int* part = reinterpret_cast<int*>(misc + 4);                        // 16 ints
+    uint64_t* bars = reinterpret_cast<uint64_t*>(turns + C::kEpiWarps * C::kTurnBytes);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    int* part = reinterpret_cast<int*>(misc + 4);                        // 24 ints
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, xs_empty = acc_empty + 32, done = xs_empty + 32;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
     const uint32_t tiles_at = tc::smem_addr(tiles), scales_at = tc::smem_addr(scales);
 
     const GroupGemmArgs& a = p.a;
@@ -156,7 +152,6 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         for (int i = 0; i < C::kAccs; ++i) {
             tc::bar_init(acc_full + 8 * i, 1 + (C::kB128 ? kScaleThreads / 32 : 0));
             tc::bar_init(acc_empty + 8 * i, (PAIR ? 2 : 1) * C::kEpiWarps);
-            tc::bar_init(xs_empty + 8 * i, C::kEpiWarps);
         }
         tc::bar_init(done, 1);
         tc::fence_barrier_init();
@@ -237,7 +232,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         uint32_t ph = 0, chunk_no = 0;
         bool ok = true, ready = false;
         while (ok && leader && walk.next()) {
-            const uint32_t n = (uint32_t)columns(walk.m);
+            const uint32_t n = C::kB128 ? kM : (uint32_t)columns(walk.m);
             constexpr int kRows = PAIR ? 2 * kM : kM;
             uint32_t idesc;
             if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kRows >> 7) << 27);
@@ -249,23 +244,23 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                 const int buf = use % C::kAccs;
                 if (!ready) {
                     ok = true;
-                    if (C::kB128 || kc == 0) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
+                    if (C::kB128 ? (kc & 1) == 0 : kc == 0) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
                     ok = __all_sync(0xFFFFFFFFu, ok && tc::bar_wait<PAIR>(full + 8 * st, ph, stop));
                     if (!ok) break;
                 }
                 tc::fence_after();
-                const bool done_acc = C::kB128 || kc == chunks - 1;
+                const bool done_acc = kc == chunks - 1 || (C::kB128 && (kc & 1));
                 const int next_st = st + 1 == kStages ? 0 : st + 1;
                 const uint32_t next_ph = ph ^ (next_st == 0);
                 // whether the next chunk can follow at once: asked for now, so that
                 // the answer (90 cycles) is there when this chunk's products are issued
                 bool next_ready = tc::bar_test<PAIR>(full + 8 * next_st, next_ph);
-                if (C::kB128 || kc == chunks - 1)
+                if (done_acc)
                     next_ready &= tc::bar_test<PAIR>(acc_empty + 8 * ((use + 1) % C::kAccs), (((use + 1) / C::kAccs) & 1) ^ 1);
                 if (tc::elect()) {
                     const uint32_t w_at = tiles_at + st * (C::kW + C::kX);
                     const uint64_t dw = tc::desc_sw128(w_at), dx = tc::desc_sw128(w_at + C::kW);
-                    const uint32_t d = tmem + buf * BN;
+                    const uint32_t d = tmem + buf * C::kAccWidth + (C::kB128 ? (kc & 1) * kM : 0);
                     const uint32_t sw = tmem + C::kAccCols + (chunk_no % kScaleBufs) * 4 * (1 + C::kHalves), sx = sw + 4;
                     if (C::kMx) {
                         const uint32_t s_at = scales_at + st * (C::kSw + C::kSx);
@@ -281,6 +276,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                         if (k >= steps) break;
                         if (C::kMx) tc::mma_mx8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
                         else if (FMT == FMT_16BIT) tc::mma_f16<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
+                        else if (C::kB128) tc::mma_f8<PAIR>(d, dx + 2 * k, dw + 2 * k, idesc, add);
                         else tc::mma_f8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
                     }
                     tc::commit<PAIR>(empty + 8 * st);
@@ -374,10 +370,11 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                     for (int q = 0; q < 4; ++q) {
                         if (kc0 + q >= chunks) break;
                         const int buf = use % C::kAccs;
-                        ok = __all_sync(0xFFFFFFFFu, C::kMx ? tc::bar_wait(empty + 8 * st, ph ^ 1, stop)
-                                                            : tc::bar_wait(xs_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop));
+                        if (C::kMx) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
+                        else if (q % 2 == 0)
+                            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop));
                         if (!ok) break;
-                        uint8_t* dst = C::kMx ? scales + st * (C::kSw + C::kSx) + C::kSw : reinterpret_cast<uint8_t*>(xbuf + buf * BN);
+                        uint8_t* dst = C::kMx ? scales + st * (C::kSw + C::kSx) + C::kSw : reinterpret_cast<uint8_t*>(xbuf + (2 * buf + q % 2) * BN);
 #pragma unroll
                         for (int i = 0; i < kRows; ++i) {
                             const int c = u + i * kScaleThreads;
@@ -390,11 +387,12 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                         }
                         if (C::kMx) tc::fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (C::kMx) arrive(full_at + 8 * st);
-                            else tc::bar_arrive(acc_full + 8 * buf);
+                        if (C::kMx) {
+                            if (lane == 0) arrive(full_at + 8 * st);
+                        } else if (q % 2 == 1 || kc0 + q == chunks - 1) {
+                            if (lane == 0) tc::bar_arrive(acc_full + 8 * buf);
+                            ++use;
                         }
-                        ++use;
                         if (++st == kStages) {
                             st = 0;
                             ph ^= 1;
@@ -472,13 +470,11 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         // -------------------------------------------------------- epilogue
         const int quarter = warp & 3;
         const uint32_t lanes = (uint32_t)quarter << 21;                  // first lane of the quarter, in the address
-        const int first_c = C::kB128 && BN >= 64 ? ((warp - 4) >> 2) * C::kEpiCols : 0;   // this warp's slots of a tile
-        const bool idle = C::kB128 && BN < 64 && warp >= 8;
         float* xrow = xbuf + quarter * BN;
         int use = 0;
         bool ok = true;
         while (ok && walk.next()) {
-            const int n = walk.n0 + quarter * 32 + lane;
+            const int n = walk.n0 + quarter * 32 + lane;                 // this thread's channel (not with 1x128 scales)
             const int m = walk.m;
             uint32_t there[BN / 32];
             float wn = 1.0f;
@@ -496,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
             // columns c0 .. c0 + 31 of the tile: rounded once, turned in shared
             // memory from a channel a thread to rows of slots, stored in 16-byte
             // pieces (as 2-byte stores of a channel a thread, 192 slots took 4.4 us)
-            uint8_t* turn = turns + (warp - 4) * kTurn;
+            uint8_t* turn = turns + (warp - 4) * C::kTurnBytes;
             auto store = [&](int c0, uint32_t valid, const float (&v)[32]) {
                 __syncwarp();
 #pragma unroll
@@ -515,68 +511,73 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                 }
             };
             if (C::kB128) {
-                float2 acc[C::kEpiCols / 2];
+                // this thread's slot, 64 channels: the chunks' products scaled and
+                // summed in registers, two chunks to a wait (one at a time, the
+                // waits and arrivals were most of the loop's instructions)
+                const int c = quarter * 32 + lane, first = ((warp - 4) >> 2) * 64;
+                const bool busy = quarter * 32 < m;
+                const float* scale = xbuf + (c < m ? c : 0);
+                float acc[64];
 #pragma unroll
-                for (int c = 0; c < C::kEpiCols / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-                // 16 columns at a time, the next 16 on their way from tensor
-                // memory, the next chunk's first ones too
-                const bool busy = first_c < m && !idle;
-                const uint32_t at = tmem + lanes + first_c;
-                uint32_t v[2][16];
-                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * (use % C::kAccs), (use / C::kAccs) & 1, stop));
-                if (!ok) break;
-                tc::fence_after();
-                if (busy) tc::tmem_load16(at + (use % C::kAccs) * BN, v[0]);
-                for (int kc = 0; kc < chunks; ++kc, ++use) {
-                    const int buf = use % C::kAccs, next = (use + 1) % C::kAccs;
-                    // this chunk's scales as they are now: their place is free once the accumulator is
-                    const float4* s = reinterpret_cast<const float4*>(xbuf + buf * BN + first_c);
+                for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+                bool ready = false;
+                for (int kc = 0; kc < chunks; kc += 2, ++use) {
+                    const int buf = use & 1;
+                    if (!ready) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t at = tmem + lanes + buf * C::kAccWidth + first;
+                    const bool next_ready = tc::bar_test(acc_full + 8 * (buf ^ 1), ((use + 1) >> 1) & 1);
+                    if (busy) {
+                        // 16 columns at a time, the next 16 on their way
+                        uint32_t v[2][16];
+                        tc::tmem_load16(at, v[0]);
+                        const float f0 = scale[2 * buf * BN], f1 = scale[(2 * buf + 1) * BN];
+                        const bool two = kc + 1 < chunks;
 #pragma unroll
-                    for (int c0 = 0; c0 < C::kEpiCols; c0 += 16) {
-                        uint32_t(&cur)[16] = v[(c0 / 16) & 1];
-                        uint32_t(&nxt)[16] = v[((c0 / 16) & 1) ^ 1];
-                        float4 f[4];
-                        if (busy) {
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t(&cur)[16] = v[j & 1];
+                            uint32_t(&nxt)[16] = v[(j & 1) ^ 1];
+                            if (j == 4 && !two) break;
                             tc::tmem_load_wait(cur);
+                            if (j < 7 && (j != 3 || two)) tc::tmem_load16(at + (j + 1) / 4 * kM + (j + 1) % 4 * 16, nxt);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) f[c] = s[c0 / 4 + c];
-                        }
-                        if (c0 + 16 < C::kEpiCols) {
-                            if (busy) tc::tmem_load16(at + buf * BN + c0 + 16, nxt);
-                        } else {
-                            tc::fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                arrive(acc_empty_at + 8 * buf);
-                                tc::bar_arrive(xs_empty + 8 * buf);
-                            }
-                            if (kc + 1 < chunks) {
-                                ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * next, ((use + 1) / C::kAccs) & 1, stop));
-                                if (!ok) break;
-                                tc::fence_after();
-                                if (busy) tc::tmem_load16(at + next * BN, nxt);
-                            }
-                        }
-                        if (busy) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float2* to = acc + c0 / 2 + 2 * c;
-                                to[0] = fma2(make_float2(__uint_as_float(cur[4 * c]), __uint_as_float(cur[4 * c + 1])),
-                                             make_float2(f[c].x, f[c].y), to[0]);
-                                to[1] = fma2(make_float2(__uint_as_float(cur[4 * c + 2]), __uint_as_float(cur[4 * c + 3])),
-                                             make_float2(f[c].z, f[c].w), to[1]);
-                            }
+                            for (int i = 0; i < 16; ++i)
+                                acc[j % 4 * 16 + i] = fmaf(__uint_as_float(cur[i]), j < 4 ? f0 : f1, acc[j % 4 * 16 + i]);
                         }
                     }
-                    if (!ok) break;
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+                    ready = kc + 2 < chunks && __all_sync(0xFFFFFFFFu, next_ready);
                 }
                 if (!ok) break;
+                // half of the channels at a time through shared memory, so that four lanes store a slot's 64 bytes
+                uint32_t valid = 0;
 #pragma unroll
-                for (int c0 = 0; c0 < C::kEpiCols; c0 += 32) {
-                    float v[32];
+                for (int i = 0; i < BN / 32; ++i)
+                    if (i == quarter) valid = there[i];
+                const bool real = (valid >> lane) & 1;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = c & 1 ? acc[(c0 + c) / 2].y : acc[(c0 + c) / 2].x;
-                    if (first_c + c0 < m && !idle) store(first_c + c0, there[(first_c + c0) / 32], v);
+                for (int h = 0; h < 2; ++h) {
+                    if (!busy) break;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float o[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = real ? acc[32 * h + 8 * i + j] : 0.0f;
+                        *reinterpret_cast<uint4*>(turn + lane * kTurnPitch + 16 * i) = p.f16 ? pack8<DT_F16>(o) : pack8<DT_BF16>(o);
+                    }
+                    __syncwarp();
+                    const int ch = walk.n0 + first + 32 * h + (lane & 3) * 8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2), slot = quarter * 32 + r;
+                        if (slot < m && ch < a.N)
+                            st16_if(a.out + (int64_t)(walk.s0 + slot) * a.N + ch,
+                                    *reinterpret_cast<const uint4*>(turn + r * kTurnPitch + (lane & 3) * 16), true);
+                    }
                 }
             } else {
                 const int buf = use % C::kAccs;

@@ -49,10 +49,13 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
 // writers' fence_async_smem has put it there, and the other CTA's thread only
 // starts that reading. So the arrival does not release to the cluster, which
 // would wait for every access of its thread under way: 1 us, and 1652 us for
-// 490 (32768 MXFP8 rows, N = 4096, K = 6144).
+// 529 (32768 MXFP8 rows, N = 4096, K = 6144).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+
+// Nanoseconds for which a waiting thread may sleep before it looks at its limit.
+constexpr uint32_t kSuspendNs = 100000;
 
 // Waits see what was released before the arrivals: in this CTA, or (CLUSTER) by
 // any CTA of the cluster. bar_try may suspend the thread for a while, bar_test does not.
@@ -60,14 +63,14 @@ template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     if (CLUSTER)
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(bar), "r"(parity)
+                     : "r"(bar), "r"(parity), "r"(kSuspendNs)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(bar), "r"(parity)
+                     : "r"(bar), "r"(parity), "r"(kSuspendNs)
                      : "memory");
     return ok != 0;
 }
