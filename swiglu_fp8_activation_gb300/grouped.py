@@ -10,12 +10,11 @@ allocates belongs to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 
 import torch
 
-from .binding import F_FP16, FORMATS, GROUP, SgqError, _act_dtype, _check, _want, library
+from .binding import F_FP16, FORMATS, GROUP, SgqError, _act_dtype, _check, library
 
 MAX_GROUPS = 1024
 MAX_RANK = 128
@@ -50,26 +49,35 @@ def _dims(t: torch.Tensor, n: int, name: str):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
-_here = contextlib.nullcontext()
 
 
-def _on(stream, what: str, *tensors):
-    """(device, stream handle, context) of a call: every tensor (or None) on
-    one CUDA device; the context makes it the current one, with `stream` its
-    current stream, so that what the call allocates belongs to that stream."""
+def _need(t: torch.Tensor, shape, dtype, name: str):
+    if t.dtype != dtype or t.shape != shape:
+        raise SgqError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise SgqError(f"{name}: must be contiguous")
+
+
+def _here(stream, what: str, *tensors):
+    """The current stream's handle, where every tensor (or None) is on the
+    current CUDA device and no other stream is asked for; else None."""
     d = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != d:
             raise SgqError(f"{what}: a tensor on {t.device}, another on {tensors[0].device}")
     if d < 0:
         raise SgqError(f"{what}: expected CUDA tensors, got {tensors[0].device}")
-    if stream is None:
-        if d == torch.cuda.current_device():
-            return tensors[0].device, _raw_stream(d), _here
-        stream = torch.cuda.current_stream(d)
-    elif stream.device != tensors[0].device:
-        raise SgqError(f"{what}: a stream of {stream.device}, tensors on {tensors[0].device}")
-    return tensors[0].device, stream.cuda_stream, torch.cuda.stream(stream)
+    if stream is not None:
+        if stream.device != tensors[0].device:
+            raise SgqError(f"{what}: a stream of {stream.device}, tensors on {tensors[0].device}")
+        return None
+    return _raw_stream(d) if d == torch.cuda.current_device() else None
+
+
+def _there(stream, t: torch.Tensor):
+    """Makes t's device the current one and `stream` (default: that device's
+    current stream) its current stream: what a call allocates inside belongs to it."""
+    return torch.cuda.stream(torch.cuda.current_stream(t.device) if stream is None else stream)
 
 
 def _at(t: torch.Tensor | None):
@@ -92,27 +100,33 @@ def group_rows(ids: torch.Tensor, groups: int, *, offsets_out: torch.Tensor | No
         raise SgqError(f"ids: expected [T, k] or [T], got {tuple(ids.shape)}")
     if ids.dtype not in (torch.int32, torch.int64):
         raise SgqError(f"ids: expected int32 or int64, got {ids.dtype}")
-    _want(ids, ids.shape, ids.dtype, "ids")
-    T, k = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1
+    if not ids.is_contiguous():
+        raise SgqError("ids: must be contiguous")
+    shape = ids.shape
+    T, k = shape[0], shape[1] if len(shape) == 2 else 1
     groups = int(groups)
     if not 1 <= groups <= MAX_GROUPS or k < 1:
         raise SgqError(f"groups: 1 to {MAX_GROUPS}, got {groups}; ids a token: at least 1, got {k}")
-    for t, shape, name in ((offsets_out, (groups + 1,), "offsets_out"), (rows_out, (T * k,), "rows_out"),
-                           (slots_out, tuple(ids.shape), "slots_out")):
-        if t is not None:
-            _want(t, shape, torch.int32, name)
-    dev, at, ctx = _on(stream, "group_rows", ids, offsets_out, rows_out, slots_out)
-    with ctx:
-        if offsets_out is None:
-            offsets_out = torch.empty((groups + 1,), dtype=torch.int32, device=dev)
-        if rows_out is None:
-            rows_out = torch.empty((T * k,), dtype=torch.int32, device=dev)
-        if slots_out is None:
-            slots_out = torch.empty(tuple(ids.shape), dtype=torch.int32, device=dev)
-        st = _lib().group_rows(ids.element_size(), T, k, groups, _at(ids), _at(offsets_out), _at(rows_out),
-                               _at(slots_out), at)
-        if st:
-            _check(st, "group_rows")
+    if offsets_out is not None:
+        _need(offsets_out, (groups + 1,), torch.int32, "offsets_out")
+    if rows_out is not None:
+        _need(rows_out, (T * k,), torch.int32, "rows_out")
+    if slots_out is not None:
+        _need(slots_out, shape, torch.int32, "slots_out")
+    at = _here(stream, "group_rows", ids, offsets_out, rows_out, slots_out)
+    if at is None:
+        with _there(stream, ids):
+            return group_rows(ids, groups, offsets_out=offsets_out, rows_out=rows_out, slots_out=slots_out)
+    if offsets_out is None:
+        offsets_out = ids.new_empty((groups + 1,), dtype=torch.int32)
+    if rows_out is None:
+        rows_out = ids.new_empty((T * k,), dtype=torch.int32)
+    if slots_out is None:
+        slots_out = ids.new_empty(shape, dtype=torch.int32)
+    st = _lib().group_rows(ids.element_size(), T, k, groups, ids.data_ptr(), offsets_out.data_ptr(), rows_out.data_ptr(),
+                           slots_out.data_ptr(), at)
+    if st:
+        _check(st, "group_rows")
     return offsets_out, rows_out, slots_out
 
 
@@ -149,8 +163,8 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt
     X, K = _dims(x, 2, "x")
     groups, N, _ = _dims(w, 3, "w")
     dt = _act_dtype(x, "x") if fmt == "none" else torch.uint8
-    _want(x, (X, K), dt, "x")
-    _want(w, (groups, N, K), dt, "w")
+    _need(x, (X, K), dt, "x")
+    _need(w, (groups, N, K), dt, "w")
     unit = {"per_token": 16, "none": 8, **GROUP}[fmt]
     if K < 1 or K % unit or N < 1 or N % 8:
         raise SgqError(f"{fmt}: K has to be a multiple of {unit} and N of 8, got K = {K}, N = {N}", 2)
@@ -159,25 +173,27 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt
         if (t is None) != (shape is None):
             raise SgqError(f"{name}: {'missing' if t is None else 'of no use'} with format {fmt!r}")
         if t is not None:
-            _want(t, shape, sdt, name)
-    _want(offsets, (groups + 1,), torch.int32, "offsets")
+            _need(t, shape, sdt, name)
+    _need(offsets, (groups + 1,), torch.int32, "offsets")
     S = X
     if rows is not None:
         S, = _dims(rows, 1, "rows")
-        _want(rows, (S,), torch.int32, "rows")
+        _need(rows, (S,), torch.int32, "rows")
     odt = out_dtype or (out.dtype if out is not None else dt if fmt == "none" else torch.bfloat16)
     if odt not in (torch.bfloat16, torch.float16) or (fmt == "none" and odt != dt):
         raise SgqError(f"out: {odt} does not go with x of {x.dtype}")
     if out is not None:
-        _want(out, (S, N), odt, "out")
-    dev, at, ctx = _on(stream, "grouped_gemm", x, w, offsets, x_scale, w_scale, rows, out)
-    with ctx:
-        if out is None:
-            out = torch.empty((S, N), dtype=odt, device=dev)
-        st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, _at(x),
-                                 _at(x_scale), _at(w), _at(w_scale), _at(offsets), _at(rows), _at(out), at)
-        if st:
-            _check(st, "grouped_gemm")
+        _need(out, (S, N), odt, "out")
+    at = _here(stream, "grouped_gemm", x, w, offsets, x_scale, w_scale, rows, out)
+    if at is None:
+        with _there(stream, x):
+            return grouped_gemm(x, w, offsets, fmt=fmt, x_scale=x_scale, w_scale=w_scale, rows=rows, out=out, out_dtype=odt)
+    if out is None:
+        out = x.new_empty((S, N), dtype=odt)
+    st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, x.data_ptr(),
+                             _at(x_scale), w.data_ptr(), _at(w_scale), offsets.data_ptr(), _at(rows), out.data_ptr(), at)
+    if st:
+        _check(st, "grouped_gemm")
     return out
 
 
@@ -193,20 +209,22 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
     S, N = _dims(y, 2, "y")
     T, k = _dims(slots, 2, "slots")
     dt = _act_dtype(y, "y")
-    _want(y, (S, N), dt, "y")
-    _want(slots, (T, k), torch.int32, "slots")
+    _need(y, (S, N), dt, "y")
+    _need(slots, (T, k), torch.int32, "slots")
     if weights is not None:
-        _want(weights, (T, k), torch.float32, "weights")
+        _need(weights, (T, k), torch.float32, "weights")
     if out is not None:
-        _want(out, (T, N), dt, "out")
-    dev, at, ctx = _on(stream, "combine_rows", y, slots, weights, out)
-    with ctx:
-        if out is None:
-            out = torch.empty((T, N), dtype=dt, device=dev)
-        st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, _at(y), _at(slots), _at(weights),
-                                 _at(out), at)
-        if st:
-            _check(st, "combine_rows")
+        _need(out, (T, N), dt, "out")
+    at = _here(stream, "combine_rows", y, slots, weights, out)
+    if at is None:
+        with _there(stream, y):
+            return combine_rows(y, slots, weights, out=out)
+    if out is None:
+        out = y.new_empty((T, N))
+    st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, y.data_ptr(), slots.data_ptr(), _at(weights),
+                             out.data_ptr(), at)
+    if st:
+        _check(st, "combine_rows")
     return out
 
 
@@ -234,30 +252,30 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
     groups, R, _ = _dims(a, 3, "a")
     _, N = _dims(y, 2, "y")
     dt = _act_dtype(x, "x")
-    _want(x, (T, K), dt, "x")
-    _want(a, (groups, R, K), dt, "a")
-    _want(b, (groups, N, R), dt, "b")
-    _want(y, (T, N), dt, "y")
-    _want(offsets, (groups + 1,), torch.int32, "offsets")
+    _need(x, (T, K), dt, "x")
+    _need(a, (groups, R, K), dt, "a")
+    _need(b, (groups, N, R), dt, "b")
+    _need(y, (T, N), dt, "y")
+    _need(offsets, (groups + 1,), torch.int32, "offsets")
     if (rows is None) != (slots is None):
         raise SgqError("rows and slots go together")
     S = T
     if rows is not None:
         S, = _dims(rows, 1, "rows")
-        _want(rows, (S,), torch.int32, "rows")
-        if slots.dim() == 2 and slots.shape[1] == 1:
-            slots = slots.view(-1) if slots.is_contiguous() else slots
-        _want(slots, (T,), torch.int32, "slots")
+        _need(rows, (S,), torch.int32, "rows")
+        _need(slots, (T, 1) if slots.dim() == 2 else (T,), torch.int32, "slots")
     if scaling is not None:
-        _want(scaling, (groups,), torch.float32, "scaling")
+        _need(scaling, (groups,), torch.float32, "scaling")
     if workspace is not None:
-        _want(workspace, (lora_workspace_bytes(S, R),), torch.uint8, "workspace")
-    dev, at, ctx = _on(stream, "lora_add", x, a, b, y, offsets, rows, slots, scaling, workspace)
-    with ctx:
-        if workspace is None:
-            workspace = torch.empty((lora_workspace_bytes(S, R),), dtype=torch.uint8, device=dev)
-        st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, _at(x), _at(a), _at(b),
-                             _at(scaling), _at(offsets), _at(rows), _at(slots), _at(y), _at(workspace), at)
-        if st:
-            _check(st, "lora_add")
+        _need(workspace, (S * (4 * R + 16),), torch.uint8, "workspace")
+    at = _here(stream, "lora_add", x, a, b, y, offsets, rows, slots, scaling, workspace)
+    if at is None:
+        with _there(stream, x):
+            return lora_add(x, a, b, y, offsets, rows=rows, slots=slots, scaling=scaling, workspace=workspace)
+    if workspace is None:
+        workspace = x.new_empty((S * (4 * R + 16),), dtype=torch.uint8)      # lora_workspace_bytes(S, R)
+    st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, x.data_ptr(), a.data_ptr(), b.data_ptr(),
+                      _at(scaling), offsets.data_ptr(), _at(rows), _at(slots), y.data_ptr(), workspace.data_ptr(), at)
+    if st:
+        _check(st, "lora_add")
     return y

@@ -160,6 +160,8 @@ def test_lora_refusals(L):
     assert lora(L, ws=P(7)) == INVALID
     assert L.sgq_lora_workspace_bytes(8, 16) == 8 * (16 * 4 + 16)
     assert L.sgq_lora_workspace_bytes(8, 200) == 0
+    for S, R in ((1, 8), (77, 40), (1 << 30, 128)):
+        assert sgq.lora_workspace_bytes(S, R) == S * (4 * R + 16)      # what lora_add allocates
     assert L.sgq_lora_workspace_bytes(-1, 8) == 0
 
 
