@@ -25,7 +25,7 @@
  * kernels: a value outside reads as the nearest one inside, so no offsets
  * make a kernel touch memory outside the tensors.
  *
- * Conventions are sgq.h's: device pointers owned by the caller, contiguous
+ * Conventions are sgq.h's: pointers of the current device, owned by the caller, contiguous
  * row-major tensors, E4M3 bytes, status codes, host checks before any launch
  * with every buffer untouched by a refused call, nothing allocated, no
  * synchronisation, CUDA-graph capture allowed, programmatic dependent launch
@@ -46,6 +46,7 @@ extern "C" {
 
 #define SGQ_MAX_GROUPS 1024     /* groups of one call */
 #define SGQ_MAX_RANK 128        /* rank of lora_add */
+#define SGQ_MAX_ROWS 0x7FFF0000 /* rows, slots or ids of one call */
 
 /* grouped_gemm's fmt beside sgq_format_t: 16-bit rows and weights, no scales. */
 #define SGQ_FMT_16BIT 3
@@ -62,7 +63,7 @@ extern "C" {
  *
  * Arguments:
  *   id_bytes      4 (int32 ids) or 8 (int64 ids)
- *   T, k          ids is [T, k]; T * k < 2^31; k >= 1
+ *   T, k          ids is [T, k]; T * k <= SGQ_MAX_ROWS; k >= 1
  *   groups        1 .. SGQ_MAX_GROUPS
  *   ids           [T, k], read; aligned to id_bytes
  *   offsets       [groups + 1] int32, written (also when T = 0)
@@ -88,12 +89,12 @@ int group_rows(int id_bytes, int64_t T, int64_t k, int64_t groups, const void* i
  *   fmt           sgq_format_t or SGQ_FMT_16BIT
  *   flags         SGQ_F_FP16: out is fp16, not bf16, and so are x and w with
  *                 SGQ_FMT_16BIT (others rejected)
- *   S             slots, < 2^31
+ *   S             slots, at most SGQ_MAX_ROWS
  *   groups        1 .. SGQ_MAX_GROUPS
  *   N             output width, a multiple of 8, at most SGQ_MAX_WIDTH
  *   K             length of the products, at most SGQ_MAX_WIDTH: a multiple of
  *                 32 (MXFP8), 128 (1x128), 16 (per-token) or 8 (16-bit)
- *   x_rows        rows of x, < 2^31; S where rows is NULL
+ *   x_rows        rows of x, at most SGQ_MAX_ROWS; S where rows is NULL
  *   x             [x_rows, K], read
  *   x_scale       what sgq.h's quantisation wrote row-major: [x_rows, K/32]
  *                 E8M0, [x_rows, K/128] or [x_rows, 1] fp32; NULL for 16-bit
@@ -125,9 +126,10 @@ int grouped_gemm(int fmt, uint32_t flags, int64_t S, int64_t groups, int64_t N, 
  *
  * Arguments:
  *   flags         SGQ_F_FP16: y and out are fp16, not bf16 (others rejected)
- *   T, k          tokens, rows a token (k >= 1); T * k < 2^31
- *   S             rows of y, < 2^31
- *   N             width, a multiple of 8, at most SGQ_MAX_WIDTH
+ *   T, k          tokens, rows a token (k >= 1); T * k <= SGQ_MAX_ROWS
+ *   S             rows of y, at most SGQ_MAX_ROWS
+ *   N             width, a multiple of 8, at most SGQ_MAX_WIDTH;
+ *                 T * ceil(N / 512) < 2^31
  *   y             [S, N], read
  *   slots         [T, k] int32, read
  *   weights       [T, k] fp32, read, or NULL (every weight 1)
@@ -151,8 +153,8 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
  *
  * Arguments:
  *   flags         SGQ_F_FP16: x, a, b and y are fp16, not bf16 (others rejected)
- *   T             rows of x and y, < 2^31
- *   S             slots, < 2^31; T where rows is NULL
+ *   T             rows of x and y, at most SGQ_MAX_ROWS
+ *   S             slots, at most SGQ_MAX_ROWS; T where rows is NULL
  *   groups        adapters, 1 .. SGQ_MAX_GROUPS
  *   R             rank, a multiple of 8, at most SGQ_MAX_RANK
  *   K, N          widths of x and y, multiples of 8, at most SGQ_MAX_WIDTH
@@ -173,6 +175,15 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
 
 /* Bytes of lora_add's workspace; 0 where S or R is outside its range. */
 int64_t sgq_lora_workspace_bytes(int64_t S, int64_t R);
+
+/*
+ * Launches of grouped_gemm and lora_add on the current device, since the
+ * library was loaded, in which a wait inside the kernel ran out of time (some
+ * seconds: the device was not making progress). Such a launch ends and leaves
+ * its outputs unspecified. A diagnosis: it waits for the device, and may not be
+ * called during graph capture. NULL returns SGQ_ERR_INVALID_ARG.
+ */
+int sgq_wait_timeouts(uint32_t* count);
 
 #ifdef __cplusplus
 }

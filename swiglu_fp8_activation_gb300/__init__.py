@@ -37,5 +37,5 @@ from .binding import (  # noqa: F401
 )
 from .grouped import (  # noqa: F401
     GEMM_FORMATS, MAX_GROUPS, MAX_RANK, combine_rows, gemm_scale_shapes, group_rows, grouped_gemm, lora_add,
-    lora_workspace_bytes,
+    lora_workspace_bytes, wait_timeouts,
 )

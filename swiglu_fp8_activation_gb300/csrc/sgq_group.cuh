@@ -81,6 +81,10 @@ cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupG
 cudaError_t launch_combine(int dt, const Device& dev, const CombineArgs& a, cudaStream_t stream);
 cudaError_t launch_lora(int dt, const Device& dev, const LoraArgs& a, cudaStream_t stream);
 
+// Launches on the current device in which a wait ran out of time (waits for the device).
+cudaError_t gemm_gave_up(uint32_t* n);
+cudaError_t lora_gave_up(uint32_t* n);
+
 // Launch k on `stream` with programmatic stream serialisation (as launch_pdl,
 // for any grid), in clusters of `cluster` CTAs along x.
 template <typename Args>

@@ -8,7 +8,7 @@ using namespace sgq;
 
 namespace {
 
-constexpr int64_t kMaxRows = 0x7FFFFFFF;   // slots, rows and ids are counted in 32 bits
+constexpr int64_t kMaxRows = SGQ_MAX_ROWS;   // counted in 32 bits, with room for a tile behind the last
 
 bool bad_count(int64_t v) { return v < 0 || v > kMaxRows; }
 
@@ -44,7 +44,7 @@ int grouped_gemm(int fmt, uint32_t flags, int64_t S, int64_t groups, int64_t N, 
                  const int32_t* rows, void* out, sgq_stream_t stream) {
     if (fmt < SGQ_FMT_MXFP8 || fmt > SGQ_FMT_16BIT || (flags & ~SGQ_F_FP16)) return SGQ_ERR_INVALID_ARG;
     if (bad_count(S) || bad_count(x_rows) || groups < 1 || N <= 0 || K <= 0) return SGQ_ERR_INVALID_ARG;
-    if (!rows && x_rows != S) return SGQ_ERR_INVALID_ARG;
+    if (S > 0 && !rows && x_rows != S) return SGQ_ERR_INVALID_ARG;
     const int unit = fmt == SGQ_FMT_MXFP8 ? 32 : fmt == SGQ_FMT_FP8_BLOCK128 ? 128 : fmt == SGQ_FMT_FP8_PER_TOKEN ? 16 : 8;
     if (groups > SGQ_MAX_GROUPS || N % 8 != 0 || N > SGQ_MAX_WIDTH || K % unit != 0 || K > SGQ_MAX_WIDTH)
         return SGQ_ERR_UNSUPPORTED;
@@ -95,7 +95,7 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
                  const float* weights, void* out, sgq_stream_t stream) {
     if (flags & ~SGQ_F_FP16) return SGQ_ERR_INVALID_ARG;
     if (bad_count(T) || k < 1 || k > kMaxRows || T > kMaxRows / k || bad_count(S) || N <= 0) return SGQ_ERR_INVALID_ARG;
-    if (N % 8 != 0 || N > SGQ_MAX_WIDTH) return SGQ_ERR_UNSUPPORTED;
+    if (N % 8 != 0 || N > SGQ_MAX_WIDTH || T > 0x7FFFFFFF / ((N + 511) / 512)) return SGQ_ERR_UNSUPPORTED;   // a CTA each 512 columns
     if (T == 0) return SGQ_OK;
     if (!slots || !out || (S > 0 && !y)) return SGQ_ERR_INVALID_ARG;
     if (!aligned(y, 16) || !aligned(out, 16) || !aligned(slots, 4) || !aligned(weights, 4)) return SGQ_ERR_MISALIGNED;
@@ -127,11 +127,11 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
              const int32_t* slots, void* y, void* workspace, sgq_stream_t stream) {
     if (flags & ~SGQ_F_FP16) return SGQ_ERR_INVALID_ARG;
     if (bad_count(T) || bad_count(S) || groups < 1 || R <= 0 || K <= 0 || N <= 0) return SGQ_ERR_INVALID_ARG;
-    if (!rows != !slots || (!rows && S != T)) return SGQ_ERR_INVALID_ARG;
     if (groups > SGQ_MAX_GROUPS || R % 8 != 0 || R > SGQ_MAX_RANK || K % 8 != 0 || K > SGQ_MAX_WIDTH || N % 8 != 0 ||
         N > SGQ_MAX_WIDTH)
         return SGQ_ERR_UNSUPPORTED;
     if (S == 0 || T == 0) return SGQ_OK;
+    if (!rows != !slots || (!rows && S != T)) return SGQ_ERR_INVALID_ARG;
     if (!x || !a || !b || !offsets || !y || !workspace) return SGQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(workspace, 16) ||
         !aligned(scaling, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
@@ -162,6 +162,15 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
     l.N = (int)N;
     return launched(launch_lora((flags & SGQ_F_FP16) ? DT_F16 : DT_BF16, current_device(), l,
                                 static_cast<cudaStream_t>(stream)));
+}
+
+int sgq_wait_timeouts(uint32_t* count) {
+    if (!count) return SGQ_ERR_INVALID_ARG;
+    uint32_t gemm = 0, lora = 0;
+    cudaError_t e = gemm_gave_up(&gemm);
+    if (e == cudaSuccess) e = lora_gave_up(&lora);
+    if (e == cudaSuccess) *count = gemm + lora;
+    return launched(e);
 }
 
 }  // extern "C"

@@ -58,10 +58,11 @@ struct alignas(128) GemmParams {
     int chunks;                    // chunks of K
     int kbytes;                    // bytes of a row
     int f16;                       // out (and 16-bit operands) are fp16
+    int split;                     // CTAs of a cluster that share a tile's K (1: none)
     int xs_align;                  // 16, 4 or 1: alignment of every 4-byte (4 chunks: 16-byte) piece of x_scale
 };
 
-template <int FMT, int BN, bool PAIR>
+template <int FMT, int BN, bool PAIR, bool SPLIT = false>
 struct Cfg {
     static constexpr bool kMx = FMT == FMT_MX, kB128 = FMT == FMT_B128;
     static constexpr int kXRows = PAIR ? BN / 2 : BN;             // slots whose rows a CTA holds
@@ -74,8 +75,9 @@ struct Cfg {
     // fp32 scales of the slots: for each quarter of the channels, or for each accumulator
     static constexpr int kXbuf = FMT == FMT_PT || kB128 ? 4 * 4 * BN : 0;
     static constexpr int kTurnBytes = kB128 ? 32 * kTurnPitch : kTurn;
+    static constexpr int kParts = SPLIT ? 4 * BN * kM : 0;       // the tile's parts that this CTA sums
     static constexpr int kFixed =
-        1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurnBytes + (kB128 && BN < kM ? (kM - BN) * kChunk : 0) + 1024;
+        1024 /* alignment */ + 2 * 4 * (kMaxGroups + 8) + kXbuf + kEpiWarps * kTurnBytes + kParts + (kB128 && BN < kM ? (kM - BN) * kChunk : 0) + 1024;
     static constexpr int kFit = (kMaxDynamicSmem - kFixed) / kStage;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kAccs = 2;                               // accumulators
@@ -86,7 +88,7 @@ struct Cfg {
     static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
     static constexpr int kGatherWarp = 4 + kEpiWarps;             // first of the four
     static constexpr int kThreads = 32 * kGatherWarp;             // without the gather's
-    static constexpr int kBehind = kStages / 2;                   // chunks of a gather's copies in flight
+    static constexpr int kBehind = 2;                             // chunks of a gather's copies in flight
     static constexpr int kSmem = kFixed + kStages * kStage;
     static_assert(kNeed <= 512 && kStages >= 3, "tile too large");
 };
@@ -116,10 +118,10 @@ struct Walk {
 
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
-template <int FMT, int BN, bool PAIR>
-__global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads, 1)
+template <int FMT, int BN, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ GemmParams p) {
-    using C = Cfg<FMT, BN, PAIR>;
+    using C = Cfg<FMT, BN, PAIR, SPLIT>;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
@@ -129,7 +131,8 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
     int* first = lo + kMaxGroups + 8;
     float* xbuf = reinterpret_cast<float*>(first + kMaxGroups + 8);      // [4][BN]
     uint8_t* turns = reinterpret_cast<uint8_t*>(xbuf) + C::kXbuf;         // [epilogue warps][32 slots][32 channels]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(turns + C::kEpiWarps * C::kTurnBytes);
+    float* parts = reinterpret_cast<float*>(turns + C::kEpiWarps * C::kTurnBytes);   // [split][BN / split][128 channels]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(parts) + C::kParts);
     uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
     int* part = reinterpret_cast<int*>(misc + 4);                        // 24 ints
     volatile uint32_t* stop = misc + 1;
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         if (C::kMx) tc::prefetch_map(&p.ms);
     }
     if (warp == 2) tc::tmem_alloc<PAIR>(tc::smem_addr(misc), C::kCols);
+    if (SPLIT) cluster_arrive_relaxed();
     pdl_wait();
     scan_groups(a.offsets, a.groups, a.S, BN, lo, first, part);
     tc::fence_before();
@@ -169,12 +173,26 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         cluster_arrive();
         cluster_wait();
     }
+    if (SPLIT) cluster_wait();       // every CTA of the cluster runs: its shared memory may be written
     tc::fence_after();
     // a next launch that holds tensor memory while it waits for this one may
     // start only now that this CTA has its own
     pdl_trigger();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     Walk walk(lo, first, a.groups, p.n_tiles, BN, PAIR ? 2 : 1);
+    // Where few tiles would leave multiprocessors idle, the CTAs of a cluster
+    // share one: each takes a piece of K (a multiple of 4 chunks), and each sums
+    // the pieces, in order, for some of the slots.
+    int k_from = 0, k_to = chunks, share = 0, part_no = 0;
+    if (SPLIT) {
+        part_no = (int)(blockIdx.x % (uint32_t)p.split);
+        share = BN / p.split;
+        walk.tile = blockIdx.x / (uint32_t)p.split;                      // and no second one
+        const int per = ((chunks + p.split - 1) / p.split + 3) & ~3;
+        k_from = min(chunks, part_no * per);
+        k_to = min(chunks, k_from + per);
+        if (k_from == k_to) walk.tile = walk.end;
+    }
     // In a pair the first CTA issues the products: what makes a stage full, and
     // an accumulator free, arrives at its barriers, and the products' ends at both CTAs'.
     const bool leader = !PAIR || walk.rank == 0;
@@ -183,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
         if (PAIR) tc::bar_arrive_cluster(bar);
         else tc::bar_arrive(bar);
     };
-    // slots of a tile whose rows this CTA holds: the product's N, a multiple of 16 a CTA, half each in a pair
+    // the product's N, a multiple of 16 a CTA, half each in a pair
     auto columns = [](int m) { return PAIR ? (m + 31) & ~31 : (m + 15) & ~15; };
 
     if (warp == 0) {
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
             const int scale_row = (walk.g * p.n_tiles + min(walk.n0 / kM, p.n_tiles - 1)) * chunks;
             const uint32_t bytes = (PAIR ? 2 : 1) * (C::kW + C::kSw + (gather ? 0 : C::kX));
             const int s0 = walk.s0 + walk.rank * (columns(walk.m) / 2);
-            for (int kc = 0; kc < chunks; ++kc) {
+            for (int kc = k_from; kc < k_to; ++kc) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                 if (!ok) break;
                 const uint32_t w_at = tiles_at + st * (C::kW + C::kX), x_at = w_at + C::kW;
@@ -240,16 +258,16 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
             if (FMT == FMT_16BIT && !p.f16) idesc |= (1u << 7) | (1u << 10);
             const int left = p.kbytes - (chunks - 1) * kChunk;
             const int last_steps = (left + 31) / 32;
-            for (int kc = 0; kc < chunks; ++kc, ++chunk_no) {
+            for (int kc = k_from; kc < k_to; ++kc, ++chunk_no) {
                 const int buf = use % C::kAccs;
                 if (!ready) {
                     ok = true;
-                    if (C::kB128 ? (kc & 1) == 0 : kc == 0) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
+                    if (C::kB128 ? (kc & 1) == 0 : kc == k_from) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
                     ok = __all_sync(0xFFFFFFFFu, ok && tc::bar_wait<PAIR>(full + 8 * st, ph, stop));
                     if (!ok) break;
                 }
                 tc::fence_after();
-                const bool done_acc = kc == chunks - 1 || (C::kB128 && (kc & 1));
+                const bool done_acc = kc == k_to - 1 || (C::kB128 && (kc & 1));
                 const int next_st = st + 1 == kStages ? 0 : st + 1;
                 const uint32_t next_ph = ph ^ (next_st == 0);
                 // whether the next chunk can follow at once: asked for now, so that
@@ -272,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                     const int steps = kc == chunks - 1 ? last_steps : 4;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t add = k > 0 || (!C::kB128 && kc > 0);
+                        const uint32_t add = k > 0 || (!C::kB128 && kc > k_from);
                         if (k >= steps) break;
                         if (C::kMx) tc::mma_mx8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
                         else if (FMT == FMT_16BIT) tc::mma_f16<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
@@ -355,11 +373,11 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
             };
             read_rows();
             sources();
-            fetch(cur, cur_w, 0);
+            fetch(cur, cur_w, k_from);
             read_rows();
             while (ok && walk.next()) {
-                for (int kc0 = 0; ok && kc0 < chunks; kc0 += 4) {
-                    if (kc0 + 4 < chunks) {
+                for (int kc0 = k_from; ok && kc0 < k_to; kc0 += 4) {
+                    if (kc0 + 4 < k_to) {
                         fetch(nxt, nxt_w, kc0 + 4);
                     } else {
                         sources();
@@ -368,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if (kc0 + q >= chunks) break;
+                        if (kc0 + q >= k_to) break;
                         const int buf = use % C::kAccs;
                         if (C::kMx) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                         else if (q % 2 == 0)
@@ -389,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                         __syncwarp();
                         if (C::kMx) {
                             if (lane == 0) arrive(full_at + 8 * st);
-                        } else if (q % 2 == 1 || kc0 + q == chunks - 1) {
+                        } else if (q % 2 == 1 || kc0 + q == k_to - 1) {
                             if (lane == 0) tc::bar_arrive(acc_full + 8 * buf);
                             ++use;
                         }
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                              ? static_cast<const uint8_t*>(a.x) + (int64_t)row[i] * p.kbytes + piece * 16
                              : nullptr;
             read_rows();
-            for (int kc = 0; kc < chunks; ++kc) {
+            for (int kc = k_from; kc < k_to; ++kc) {
                 ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(empty + 8 * st, ph ^ 1, stop));
                 if (!ok) break;
                 uint8_t* dst = tiles + st * (C::kW + C::kX) + C::kW + (u >> 3) * kChunk + ((piece ^ ((u >> 3) & 7)) << 4);
@@ -521,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
 #pragma unroll
                 for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
                 bool ready = false;
-                for (int kc = 0; kc < chunks; kc += 2, ++use) {
+                for (int kc = k_from; kc < k_to; kc += 2, ++use) {
                     const int buf = use & 1;
                     if (!ready) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
                     if (!ok) break;
@@ -533,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                         uint32_t v[2][16];
                         tc::tmem_load16(at, v[0]);
                         const float f0 = scale[2 * buf * BN], f1 = scale[(2 * buf + 1) * BN];
-                        const bool two = kc + 1 < chunks;
+                        const bool two = kc + 1 < k_to;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             uint32_t(&cur)[16] = v[j & 1];
@@ -549,9 +567,19 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
-                    ready = kc + 2 < chunks && __all_sync(0xFFFFFFFFu, next_ready);
+                    ready = kc + 2 < k_to && __all_sync(0xFFFFFFFFu, next_ready);
                 }
                 if (!ok) break;
+                if (SPLIT) {
+                    // this slot's 64 sums to the CTA that adds the parts up for it
+                    if (c < m) {
+                        const float* to = parts + (part_no * share + c % share) * kM + first;
+#pragma unroll
+                        for (int i = 0; i < 64; i += 4)
+                            st_cluster16(to + i, (uint32_t)(c / share), make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]));
+                    }
+                    continue;
+                }
                 // half of the channels at a time through shared memory, so that four lanes store a slot's 64 bytes
                 uint32_t valid = 0;
 #pragma unroll
@@ -597,12 +625,45 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
                             f[c] = __uint_as_float(v[c]);
                             if (FMT == FMT_PT) f[c] = f[c] * xrow[c0 + c] * wn;
                         }
-                        store(c0, there[c0 / 32], f);
+                        if (SPLIT) {
+                            // this channel's sums to the CTAs that add the parts up
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c0 + c < m)
+                                    st_cluster4(parts + (part_no * share + (c0 + c) % share) * kM + quarter * 32 + lane,
+                                                (uint32_t)((c0 + c) / share), f[c]);
+                        } else {
+                            store(c0, there[c0 / 32], f);
+                        }
                     }
                 }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(acc_empty_at + 8 * buf);
+            }
+        }
+    }
+    if (SPLIT) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        Walk one(lo, first, a.groups, p.n_tiles, BN, 1);
+        one.tile = blockIdx.x / (uint32_t)p.split;
+        if (one.next()) {
+            const int per = ((chunks + p.split - 1) / p.split + 3) & ~3, active = (chunks + per - 1) / per;
+            const int mine = min(share, one.m - part_no * share);
+            for (int i = tid; i < mine * (kM / 8); i += blockDim.x) {
+                const int c = i / (kM / 8), ch = i % (kM / 8) * 8, slot = one.s0 + part_no * share + c;
+                float v[8] = {};
+                const int64_t r = gather ? a.rows[slot] : slot;
+                if (r >= 0 && r < a.x_rows)
+                    for (int q = 0; q < active; ++q) {
+                        const float* from = parts + (q * share + c) * kM + ch;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] += from[j];
+                    }
+                if (one.n0 + ch < a.N)
+                    st16_if(a.out + (int64_t)slot * a.N + one.n0 + ch, p.f16 ? pack8<DT_F16>(v) : pack8<DT_BF16>(v), true);
             }
         }
     }
@@ -619,9 +680,14 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR>::kThreads + kGatherThreads,
 
 // --------------------------------------------------------------------- host
 
-template <int FMT, int BN, bool PAIR = false>
+// Tiles of bn slots x one of n_tiles at most, whatever the offsets.
+int64_t most_tiles(const GroupGemmArgs& a, int bn, int n_tiles) {
+    return ((int64_t)a.S / bn + (a.S < a.groups ? a.S : a.groups)) * n_tiles;
+}
+
+template <int FMT, int BN, bool PAIR = false, bool SPLIT = false>
 cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
-    using C = Cfg<FMT, BN, PAIR>;
+    using C = Cfg<FMT, BN, PAIR, SPLIT>;
     const GroupGemmArgs& a = p.a;
     const cuuint64_t wd[3] = {(cuuint64_t)p.kbytes, (cuuint64_t)a.N, (cuuint64_t)a.groups};
     // with no row of x at all nothing of it is used: any memory serves as its map
@@ -630,15 +696,24 @@ cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     if (C::kMx && !encode_tiles512(&p.ms, a.ws, (int64_t)a.groups * p.n_tiles * p.chunks)) return cudaErrorInvalidValue;
     constexpr int kCtas = PAIR ? 2 : 1;
-    // tiles at most
-    const int64_t most = ((int64_t)a.S / BN + (a.S < a.groups ? a.S : a.groups)) * ((p.n_tiles + kCtas - 1) / kCtas);
-    const int64_t room = dev.sms >= kCtas ? dev.sms / kCtas : 1, tiles = most < room ? most : room;
-    return launch_grid(grouped_gemm_kernel<FMT, BN, PAIR>, dim3((unsigned)(tiles * kCtas)),
-                       C::kThreads + (a.rows ? kGatherThreads : 0), C::kSmem, kCtas, dev.id, p, stream);
+    const int64_t most = most_tiles(a, BN, (p.n_tiles + kCtas - 1) / kCtas);
+    const int64_t room = dev.sms >= kCtas ? dev.sms / kCtas : 1, tiles = SPLIT || most < room ? most : room;
+    const int cluster = SPLIT ? p.split : kCtas;
+    return launch_grid(grouped_gemm_kernel<FMT, BN, PAIR, SPLIT>, dim3((unsigned)(tiles * cluster)),
+                       C::kThreads + (a.rows ? kGatherThreads : 0), C::kSmem, cluster, dev.id, p, stream);
 }
 
 template <int FMT>
 cudaError_t pick(const Device& dev, GemmParams& p, cudaStream_t stream) {
+    // Few tiles: a cluster a tile, from 24 chunks on, while that leaves
+    // multiprocessors idle and a CTA keeps at least 8 chunks. One row, MXFP8, N =
+    // 1536, K = 6144: 14.1 us whole, 8.5 in 4 pieces; 16 bf16 rows, N = 1024, K =
+    // 4096: 15.0 and 7.2; 100 rows, per-token, N = 256, K = 2048: 7.3 whole, 9.2 in two.
+    const int64_t few = most_tiles(p.a, 32, p.n_tiles);
+    p.split = 1;
+    while (p.split < kMaxCluster && few * p.split * 2 <= dev.sms && p.chunks >= (p.split == 1 ? 24 : 16 * p.split))
+        p.split *= 2;
+    if (p.split > 1) return run<FMT, 32, false, true>(dev, p, stream);
     const int64_t mean = ((int64_t)p.a.S + p.a.groups - 1) / p.a.groups;
     if (mean <= 24) return run<FMT, 32>(dev, p, stream);
     if (mean <= 64) return run<FMT, 64>(dev, p, stream);
@@ -647,6 +722,8 @@ cudaError_t pick(const Device& dev, GemmParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t gemm_gave_up(uint32_t* n) { return cudaMemcpyFromSymbol(n, g_gave_up, sizeof *n); }
 
 cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream) {
     GemmParams p;

@@ -75,14 +75,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return DT == DT_BF16 ? f32x2_to_bf16x2(lo, hi) : f32x2_to_f16x2(lo, hi);
 }
 
-__device__ __forceinline__ void st_cluster16(const void* p, uint32_t rank, float4 v) {
-    const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
 // Shared memory: stages of (x 16 KB, a R x 128 bytes), the parts of v that
 // this CTA sums [split][128 / split][R + 4] floats, offsets, barriers.
 template <int DT, int BEHIND>
@@ -760,6 +752,8 @@ cudaError_t run(const Device& dev, const LoraArgs& l, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t lora_gave_up(uint32_t* n) { return cudaMemcpyFromSymbol(n, g_gave_up, sizeof *n); }
 
 cudaError_t launch_lora(int dt, const Device& dev, const LoraArgs& a, cudaStream_t stream) {
     return dt == DT_F16 ? run<DT_F16>(dev, a, stream) : run<DT_BF16>(dev, a, stream);

@@ -91,6 +91,22 @@ __device__ inline void scan_groups(const int32_t* offsets, int G, int S, int bn,
     __syncthreads();
 }
 
+// Stores into the copy of the shared memory at p that the cluster's CTA `rank` holds.
+__device__ __forceinline__ void st_cluster16(const void* p, uint32_t rank, float4 v) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_cluster4(const void* p, uint32_t rank, float v) {
+    const uint32_t local = (uint32_t)__cvta_generic_to_shared(p);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+}
+
 // Entries of a table of the groups' offsets in shared memory (16-byte multiple).
 __host__ __device__ constexpr int table_ints(int groups) { return (groups + 8 + 3) & ~3; }
 

@@ -54,23 +54,20 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Nanoseconds for which a waiting thread may sleep before it looks at its limit.
-constexpr uint32_t kSuspendNs = 100000;
-
 // Waits see what was released before the arrivals: in this CTA, or (CLUSTER) by
 // any CTA of the cluster. bar_try may suspend the thread for a while, bar_test does not.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     if (CLUSTER)
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(bar), "r"(parity), "r"(kSuspendNs)
+                     : "r"(bar), "r"(parity)
                      : "memory");
     else
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(bar), "r"(parity), "r"(kSuspendNs)
+                     : "r"(bar), "r"(parity)
                      : "memory");
     return ok != 0;
 }

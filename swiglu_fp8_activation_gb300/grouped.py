@@ -36,6 +36,8 @@ def _lib() -> C.CDLL:
         L.combine_rows.argtypes = [u32, i64, i64, i64, i64, vp, vp, vp, vp, vp]
         L.lora_add.restype = C.c_int
         L.lora_add.argtypes = [u32, i64, i64, i64, i64, i64, i64] + [vp] * 10
+        L.sgq_wait_timeouts.restype = C.c_int
+        L.sgq_wait_timeouts.argtypes = [C.POINTER(C.c_uint32)]
         L.sgq_lora_workspace_bytes.restype = i64
         L.sgq_lora_workspace_bytes.argtypes = [i64, i64]
         _bound = L
@@ -226,6 +228,14 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
     if st:
         _check(st, "combine_rows")
     return out
+
+
+def wait_timeouts() -> int:
+    """Launches of grouped_gemm and lora_add on the current device in which a
+    wait inside the kernel ran out of time (waits for the device)."""
+    n = C.c_uint32(0)
+    _check(_lib().sgq_wait_timeouts(C.byref(n)), "sgq_wait_timeouts")
+    return n.value
 
 
 def lora_workspace_bytes(S: int, R: int) -> int:

@@ -10,13 +10,20 @@ import torch
 
 import group_ref as ref
 import swiglu_fp8_activation_gb300 as sgq
+from swiglu_fp8_activation_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
 GUARD = 4096
 
 
-def guarded(shape, dtype, fill=0xFF):
+@pytest.fixture(autouse=True, scope="module")
+def no_wait_ran_out():
+    yield
+    assert sgq.wait_timeouts() == 0
+
+
+def guarded(shape, dtype):
     """A tensor inside a buffer of 0xFF bytes, and a function that checks the bytes around it."""
     n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
     raw = torch.full((n + 2 * GUARD,), 0xFF, dtype=torch.uint8, device=DEV)
@@ -172,6 +179,17 @@ def test_grouped_gemm_single_tokens_wide(fmt):
     run_gemm(fmt, [1, 0, 1, 1], 2048, 1024)
 
 
+@pytest.mark.parametrize("K", [1024, 1152, 2688, 4480])
+@pytest.mark.parametrize("sizes,N", [([1], 72), ([31], 136), ([2, 0, 33], 264), ([0, 0], 128)], ids=str)
+@pytest.mark.parametrize("gather", [None, wild_rows], ids=["rows in order", "rows outside"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_gemm_few_tiles_and_long_products(fmt, gather, sizes, N, K):
+    """Few enough tiles that the CTAs of a cluster share one, in pieces of K of unlike lengths."""
+    run_gemm(fmt, sizes, N, K, gather=gather, lead=1, tail=2)
+    if fmt in ("none", "per_token"):
+        run_gemm(fmt, sizes, N, K + 16, gather=gather, dtype=torch.float16)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_grouped_gemm_many_rows(fmt):
     run_gemm(fmt, [700, 1, 1300, 0, 255], 512, 512)
@@ -228,6 +246,76 @@ def test_grouped_gemm_keeps_a_nan_row_to_itself():
         assert got[29].isnan().all()
         keep = torch.arange(64) != 29
         ref.check(got[keep], res[keep], tol[keep], fmt)
+
+
+def test_grouped_gemm_scales_at_any_address():
+    """x_scale is a byte tensor of MXFP8 codes: no alignment is asked of it, whatever its rows' length."""
+    for K in (96, 512, 640, 1024):
+        off = sizes_to_offsets([9, 31])
+        x, xs, w, ws = ref.operands("mxfp8", 40, 2, 72, K, K)
+        res, tol = ref.grouped_gemm("mxfp8", x, xs, w, ws, off, None, 40, torch.zeros(40, 72), torch.bfloat16)
+        dx, dw, doff, dws = cuda(x, w, off, ref.swizzled(ws))
+        for shift in (1, 4, 8, 13):
+            raw = torch.zeros(xs.numel() + 16, dtype=torch.uint8, device=DEV)
+            at = raw[shift:shift + xs.numel()].view(xs.shape)
+            at.copy_(xs)
+            ref.check(sgq.grouped_gemm(dx, dw, doff, x_scale=at, w_scale=dws).cpu(), res, tol, f"K={K} shift={shift}")
+
+
+@pytest.mark.parametrize("sms", [1, 7, 64, 1000])
+def test_planned_for_other_counts_of_multiprocessors(sms):
+    binding.set_sm_budget(sms)
+    try:
+        for fmt in FMTS:
+            run_gemm(fmt, [300, 1, 77], 264, 1152, gather=some_rows)
+            run_gemm(fmt, [3, 0, 1], 136, 3584)
+        run_lora(mixed(300, 3), 3, 40, 520, 264)
+        run_lora(mixed(30, 9), 9, 16, 520, 264)
+    finally:
+        binding.set_sm_budget(0)
+
+
+def test_offsets_past_32_bits():
+    """Outputs and inputs of more than 2^31 elements: the rows at their ends."""
+    N = 4096
+    S = (1 << 31) // N + 3000
+    x = torch.randn(S, 8, generator=ref.gen(1)).to(torch.bfloat16).to(DEV)
+    w = torch.randn(2, N, 8, generator=ref.gen(2)).to(torch.bfloat16).to(DEV)
+    off = torch.tensor([0, S - 700, S], dtype=torch.int32, device=DEV)
+    out = sgq.grouped_gemm(x, w, off, fmt="none")
+    for lo, hi, g in ((S - 900, S - 700, 0), (S - 700, S, 1)):
+        want = x[lo:hi].double() @ w[g].double().T
+        mag = x[lo:hi].double().abs() @ w[g].double().abs().T
+        ref.check(out[lo:hi].cpu(), want.cpu(), (8 * 2.0 ** -22 * mag).cpu() + ref.rounding(want.cpu(), torch.bfloat16))
+    slots = torch.randint(S - 2000, S, (64, 3), generator=ref.gen(3)).to(torch.int32)
+    got = sgq.combine_rows(out, slots.to(DEV))
+    low = S - 2000
+    res, tol = ref.combine(out[low:].cpu(), slots - low, None, torch.bfloat16)
+    ref.check(got.cpu(), res, tol)
+    # lora_add on the same rows, some of the last ones with an adapter
+    ids = torch.full((S,), -1, dtype=torch.int32)
+    ids[-300:] = torch.randint(-1, 2, (300,), generator=ref.gen(4)).to(torch.int32)
+    a = torch.randn(2, 16, 8, generator=ref.gen(5)).to(torch.bfloat16)
+    b = torch.randn(2, N, 16, generator=ref.gen(6)).to(torch.bfloat16)
+    o, r, s = sgq.group_rows(ids.to(DEV), 2)
+    before = out[-400:].cpu()
+    sgq.lora_add(x, a.to(DEV), b.to(DEV), out, o, rows=r, slots=s)
+    o2, r2, s2 = ref.group_rows(ids[-400:].view(-1, 1), 2)
+    res, tol = ref.lora(x[-400:].cpu(), a, b, before, o2, r2, s2.view(-1), None, 400)
+    ref.check(out[-400:].cpu(), res, tol)
+
+
+def test_empty_calls():
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    b = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    assert sgq.grouped_gemm(b(3, 64), b(2, 32, 64), i(3), fmt="none", rows=i(0)).shape == (0, 32)
+    assert sgq.grouped_gemm(b(0, 64), b(2, 32, 64), i(3), fmt="none").shape == (0, 32)
+    assert sgq.combine_rows(b(3, 64), i(0, 2)).shape == (0, 64)
+    y = b(4, 32)
+    assert (sgq.lora_add(b(4, 64), b(2, 8, 64), b(2, 32, 8), y, i(3), rows=i(0), slots=i(4) - 1) == 1).all()
+    assert sgq.lora_add(b(0, 64), b(2, 8, 64), b(2, 32, 8), b(0, 32), i(3)).shape == (0, 32)
+    o, r, s = sgq.group_rows(i(0, 3), 5)
+    assert (o == 0).all() and r.shape == (0,) and s.shape == (0, 3)
 
 
 # ------------------------------------------------------------------ combine_rows

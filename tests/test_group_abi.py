@@ -29,12 +29,13 @@ def _text():
 
 def test_exports_and_constants(sgq_lib):
     names = re.findall(r"^(?:int|int64_t)\s+(\w+)\(", _text(), flags=re.M)
-    assert {"group_rows", "grouped_gemm", "combine_rows", "lora_add", "sgq_lora_workspace_bytes"} <= set(names)
+    assert {"group_rows", "grouped_gemm", "combine_rows", "lora_add", "sgq_lora_workspace_bytes", "sgq_wait_timeouts"} == set(names)
     for n in names:
         assert hasattr(sgq_lib, n), n
     value = lambda n: int(re.search(rf"#define {n}\s+(\d+)", _text()).group(1))  # noqa: E731
     assert value("SGQ_MAX_GROUPS") == sgq.MAX_GROUPS
     assert value("SGQ_MAX_RANK") == sgq.MAX_RANK
+    assert "#define SGQ_MAX_ROWS 0x7FFF0000" in _text()
     assert value("SGQ_FMT_16BIT") == sgq.GEMM_FORMATS["none"]
     assert {k: v for k, v in sgq.GEMM_FORMATS.items() if k != "none"} == sgq.FORMATS
 
@@ -82,6 +83,7 @@ def test_grouped_gemm_refusals(L):
     assert gemm(L, flags=1) == INVALID
     assert gemm(L, S=-1) == INVALID
     assert gemm(L, S=1 << 31, X=1 << 31) == INVALID
+    assert gemm(L, S=0x7FFF0001, X=0x7FFF0001) == INVALID
     assert gemm(L, X=1 << 31, r=P(5)) == INVALID
     assert gemm(L, G=0) == INVALID
     assert gemm(L, G=1025) == UNSUPPORTED
@@ -121,6 +123,7 @@ def test_combine_refusals(L):
     assert comb(L, N=0) == INVALID
     assert comb(L, N=12) == UNSUPPORTED
     assert comb(L, N=131072 + 8) == UNSUPPORTED
+    assert comb(L, T=1 << 24, k=1, N=131072, out=P(8)) == UNSUPPORTED     # 2^32 CTAs
     for kw in ("y", "s", "out"):
         assert comb(L, **{kw: None}) == INVALID, kw
     assert comb(L, y=P(0, 8)) == MISALIGNED
@@ -163,6 +166,7 @@ def test_lora_refusals(L):
     for S, R in ((1, 8), (77, 40), (1 << 30, 128)):
         assert sgq.lora_workspace_bytes(S, R) == S * (4 * R + 16)      # what lora_add allocates
     assert L.sgq_lora_workspace_bytes(-1, 8) == 0
+    assert L.sgq_wait_timeouts(None) == INVALID
 
 
 def i32(*shape):
