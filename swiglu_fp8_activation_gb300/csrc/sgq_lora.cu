@@ -54,13 +54,13 @@ __device__ __forceinline__ int64_t token_of(const LoraArgs& l, int s) {
     return t >= 0 && t < l.T && l.slots[t] == s ? t : -1;
 }
 
-// Barrier `ID` of THREADS threads of the block; true when `ok` is in all of them.
-template <int ID, int THREADS>
-__device__ __forceinline__ bool all_agree(bool ok) {
+// Barrier `id` of THREADS threads of the block; true when `ok` is in all of them.
+template <int THREADS>
+__device__ __forceinline__ bool all_agree(int id, bool ok) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"((uint32_t)ok), "n"(ID), "n"(THREADS)
+                 : "r"((uint32_t)ok), "r"(id), "n"(THREADS)
                  : "memory");
     return r != 0;
 }
@@ -378,12 +378,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(full_b + 8 * i, 1);
             tc::bar_init(acc + 8 * i, 1);
-            tc::bar_init(acc_empty + 8 * i, 8);
+            tc::bar_init(acc_empty + 8 * i, 4);
         }
         tc::bar_init(full_v, 1);
         for (int i = 0; i < C::kYBufs; ++i) {
             tc::bar_init(y_full + 8 * i, kLoaders + kLoaders / 32);
-            tc::bar_init(y_empty + 8 * i, 8);
+            tc::bar_init(y_empty + 8 * i, 4);
         }
         tc::fence_barrier_init();
         *stop = 0;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             ok = tc::bar_wait(y_empty + 8 * buf, ((i / C::kYBufs) & 1) ^ 1, stop);
             int* tk = tokens + buf * kM;
             if (ok) tk[u] = t;
-            if (!all_agree<1, kLoaders>(ok)) break;
+            if (!all_agree<kLoaders>(1, ok)) break;
             if (lane == 0) tc::bar_arrive(y_full + 8 * buf);             // the tokens; the copies arrive by themselves
             uint8_t* to = smem + C::kYAt + buf * C::kY + piece * 16;
             const int n = walk.n0 + piece * 8;
@@ -499,29 +499,34 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             __syncwarp();
         }
     } else {
-        // -------------------------------------- sums: 64 columns of slot c a thread
-        const int quarter = warp & 3, c = quarter * 32 + lane, first_n = (warp >> 2) * (NT / 2), piece = tid & 15;
-        bool ok = true;
+        // ------------------------------- sums: the 128 columns of slot c a thread.
+        // Warps 0-3 take the even tiles and 4-7 the odd ones, so that the waits
+        // and barriers of one overlap the other's work (all eight on each tile:
+        // 54 us for 8192 rows of 8192 and rank 64).
+        const int quarter = warp & 3, group = warp >> 2, u = tid & 127, c = u, piece = u & 15;
         float f = 0.0f;
+        int seen = -1;
         pdl_wait();
         for (uint32_t i = 0; walk.next(); ++i) {
+            if ((i & 1) != (uint32_t)group) continue;
             const uint32_t buf = i & 1, y_buf = i % C::kYBufs;
             uint8_t* y = smem + C::kYAt + y_buf * C::kY;
             const int* tk = tokens + y_buf * kM;
-            if (walk.fresh) {
+            if (walk.q != seen) {
+                seen = walk.q;
                 f = l.scaling ? l.scaling[walk.g] : 1.0f;
                 if (DT == DT_F16 && c < walk.m)
                     f *= *reinterpret_cast<const float*>(static_cast<const uint8_t*>(l.v) +
                                                          (int64_t)(walk.s0 + c) * lora_row_bytes(R) + 4 * R);
             }
-            ok = tc::bar_wait(y_full + 8 * y_buf, (i / C::kYBufs) & 1, stop) && tc::bar_wait(acc + 8 * buf, (i >> 1) & 1, stop);
-            if (!all_agree<2, 256>(ok)) break;
+            const bool ok = tc::bar_wait(y_full + 8 * y_buf, (i / C::kYBufs) & 1, stop) && tc::bar_wait(acc + 8 * buf, (i >> 1) & 1, stop);
+            if (!all_agree<128>(2 + group, ok)) break;
             tc::fence_after();
-            uint4* row = reinterpret_cast<uint4*>(y + c * C::kPitch + 2 * first_n);
+            uint4* row = reinterpret_cast<uint4*>(y + c * C::kPitch);
 #pragma unroll
-            for (int h = 0; h < NT / 2 / 32; ++h) {
+            for (int h = 0; h < NT / 32; ++h) {
                 uint32_t v[32];
-                tc::tmem_load32(tmem + ((uint32_t)quarter << 21) + buf * NT + first_n + 32 * h, v);
+                tc::tmem_load32(tmem + ((uint32_t)quarter << 21) + buf * NT + 32 * h, v);
                 tc::tmem_load_wait(v);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -534,12 +539,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 }
             }
             tc::fence_before();
-            asm volatile("bar.sync 2, 256;" ::: "memory");               // the tile's rows are done
+            asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");     // the tile's rows are done
             if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
             const int n = walk.n0 + piece * 8;
 #pragma unroll
-            for (int j = 0; j < kM / 16; ++j) {
-                const int r = (tid >> 4) + 16 * j, t = tk[r];
+            for (int j = 0; j < kM / 8; ++j) {
+                const int r = (u >> 4) + 8 * j, t = tk[r];
                 if (t >= 0 && n < l.N)
                     st16_if(l.y + (int64_t)t * l.N + n, *reinterpret_cast<const uint4*>(y + r * C::kPitch + piece * 16), true);
             }
