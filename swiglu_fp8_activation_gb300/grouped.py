@@ -120,11 +120,11 @@ def group_rows(ids: torch.Tensor, groups: int, *, offsets_out: torch.Tensor | No
         with _there(stream, ids):
             return group_rows(ids, groups, offsets_out=offsets_out, rows_out=rows_out, slots_out=slots_out)
     if offsets_out is None:
-        offsets_out = ids.new_empty((groups + 1,), dtype=torch.int32)
+        offsets_out = torch.empty((groups + 1,), dtype=torch.int32, device=ids.device)
     if rows_out is None:
-        rows_out = ids.new_empty((T * k,), dtype=torch.int32)
+        rows_out = torch.empty((T * k,), dtype=torch.int32, device=ids.device)
     if slots_out is None:
-        slots_out = ids.new_empty(shape, dtype=torch.int32)
+        slots_out = torch.empty(shape, dtype=torch.int32, device=ids.device)
     st = _lib().group_rows(ids.element_size(), T, k, groups, ids.data_ptr(), offsets_out.data_ptr(), rows_out.data_ptr(),
                            slots_out.data_ptr(), at)
     if st:
@@ -191,7 +191,7 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt
         with _there(stream, x):
             return grouped_gemm(x, w, offsets, fmt=fmt, x_scale=x_scale, w_scale=w_scale, rows=rows, out=out, out_dtype=odt)
     if out is None:
-        out = x.new_empty((S, N), dtype=odt)
+        out = torch.empty((S, N), dtype=odt, device=x.device)
     st = _lib().grouped_gemm(GEMM_FORMATS[fmt], F_FP16 if odt == torch.float16 else 0, S, groups, N, K, X, x.data_ptr(),
                              _at(x_scale), w.data_ptr(), _at(w_scale), offsets.data_ptr(), _at(rows), out.data_ptr(), at)
     if st:
@@ -222,7 +222,7 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
         with _there(stream, y):
             return combine_rows(y, slots, weights, out=out)
     if out is None:
-        out = y.new_empty((T, N))
+        out = torch.empty((T, N), dtype=dt, device=y.device)
     st = _lib().combine_rows(F_FP16 if dt == torch.float16 else 0, T, k, S, N, y.data_ptr(), slots.data_ptr(), _at(weights),
                              out.data_ptr(), at)
     if st:
@@ -283,7 +283,7 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
         with _there(stream, x):
             return lora_add(x, a, b, y, offsets, rows=rows, slots=slots, scaling=scaling, workspace=workspace)
     if workspace is None:
-        workspace = x.new_empty((S * (4 * R + 16),), dtype=torch.uint8)      # lora_workspace_bytes(S, R)
+        workspace = torch.empty((S * (4 * R + 16),), dtype=torch.uint8, device=x.device)      # lora_workspace_bytes(S, R)
     st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, x.data_ptr(), a.data_ptr(), b.data_ptr(),
                       _at(scaling), offsets.data_ptr(), _at(rows), _at(slots), y.data_ptr(), workspace.data_ptr(), at)
     if st:
