@@ -111,12 +111,16 @@ cudaError_t ctas_per_sm(const void* kernel, int device, int threads, int smem, i
 
 cudaError_t ensure_dynamic_smem(const void* kernel, int device, int bytes) {
     if (device < 0 || device >= 64) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    std::lock_guard<std::mutex> lock(smem_mu);
-    int& granted = smem_granted[device][kernel];
-    if (granted >= bytes) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) granted = bytes;
-    return e;
+    try {
+        std::lock_guard<std::mutex> lock(smem_mu);
+        int& granted = smem_granted[device][kernel];
+        if (granted >= bytes) return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) granted = bytes;
+        return e;
+    } catch (...) {                  // no exception leaves a C entry point
+        return cudaErrorMemoryAllocation;
+    }
 }
 
 namespace {

@@ -17,18 +17,21 @@ namespace {
 
 constexpr int kThreads = 64;
 
-// PIECE 16-byte reads, side by side, of data that is read once.
+// PIECES 16-byte reads, side by side, of data that is read once. (Not by the
+// read-only path: the kernel before may still write y when this one starts.)
 template <int PIECES>
 __device__ __forceinline__ void load_once(const void* p, uint4 (&v)[PIECES]) {
     if (PIECES == 2)
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[PIECES - 1].x), "=r"(v[PIECES - 1].y),
                        "=r"(v[PIECES - 1].z), "=r"(v[PIECES - 1].w)
-                     : "l"(p));
+                     : "l"(p)
+                     : "memory");
     else
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w)
-                     : "l"(p));
+                     : "l"(p)
+                     : "memory");
 }
 
 template <int DT, int PIECES, int AHEAD>

@@ -714,11 +714,27 @@ cudaError_t pick(const Device& dev, GemmParams& p, cudaStream_t stream) {
     while (p.split < kMaxCluster && few * p.split * 2 <= dev.sms && p.chunks >= (p.split == 1 ? 24 : 16 * p.split))
         p.split *= 2;
     if (p.split > 1) return run<FMT, 32, false, true>(dev, p, stream);
-    const int64_t mean = ((int64_t)p.a.S + p.a.groups - 1) / p.a.groups;
-    if (mean <= 24) return run<FMT, 32>(dev, p, stream);
-    if (mean <= 64) return run<FMT, 64>(dev, p, stream);
-    if (FMT == FMT_B128 || mean <= 128 || p.n_tiles < 2) return run<FMT, 128>(dev, p, stream);
-    return run<FMT, FMT == FMT_B128 ? 128 : FMT == FMT_MX ? 224 : 256, FMT != FMT_B128>(dev, p, stream);
+    // Else tiles about as wide as a group has slots on average, unless they are
+    // fewer than three fifths of the multiprocessors: then narrower ones, which
+    // read the weights more often but from more CTAs. 1000 MXFP8 rows of 4 groups,
+    // N = 1024, K = 2048: pairs (64 CTAs) 12.2 us, 128 slots (64) 9.7, 64 (128) 8.3;
+    // 4096 rows of 16 groups, N = K = 2048: pairs (512) 28.3, 128 slots (512) 31.1,
+    // 64 (1024) 40.8; 999 per-token rows of 7 groups, N = 1544: pairs (98) 14.2, 128
+    // slots (182) 14.7.
+    constexpr int kPair = FMT == FMT_B128 ? 128 : FMT == FMT_MX ? 224 : 256;
+    const int64_t groups = p.a.S < p.a.groups ? p.a.S : p.a.groups, mean = (p.a.S + groups - 1) / groups;
+    auto ctas = [&](int level) {
+        const int bn = level == 3 ? kPair : 32 << level;
+        return groups * ((mean + bn - 1) / bn) * (level == 3 ? (p.n_tiles + 1) / 2 * 2 : p.n_tiles);
+    };
+    int level = mean <= 24 ? 0 : mean <= 64 ? 1 : FMT == FMT_B128 || mean <= 128 || p.n_tiles < 2 ? 2 : 3;
+    while (level > 0 && 5 * ctas(level) < 3 * (int64_t)dev.sms) --level;
+    switch (level) {
+        case 0: return run<FMT, 32>(dev, p, stream);
+        case 1: return run<FMT, 64>(dev, p, stream);
+        case 2: return run<FMT, 128>(dev, p, stream);
+        default: return run<FMT, kPair, FMT != FMT_B128>(dev, p, stream);
+    }
 }
 
 }  // namespace

@@ -3,6 +3,7 @@ plain 64-bit forms (group_ref.py, with the tolerances derived there): every
 format and type, ragged and empty groups, odd widths, rows out of range,
 offsets out of order, guard bands around every output, other streams, graph
 replay, and an expert layer run end to end."""
+import contextlib
 import math
 
 import pytest
@@ -21,6 +22,15 @@ GUARD = 4096
 def no_wait_ran_out():
     yield
     assert sgq.wait_timeouts() == 0
+
+
+@contextlib.contextmanager
+def planned_for(sms):
+    binding.set_sm_budget(sms)
+    try:
+        yield
+    finally:
+        binding.set_sm_budget(0)
 
 
 def guarded(shape, dtype):
@@ -199,12 +209,30 @@ def test_grouped_gemm_many_rows(fmt):
 @pytest.mark.parametrize("gather", [None, some_rows, wild_rows], ids=["rows in order", "gathered", "rows outside"])
 @pytest.mark.parametrize("fmt", FMTS)
 def test_grouped_gemm_large_groups(fmt, sizes, N, units, gather):
-    run_gemm(fmt, sizes, N, units * ref.UNIT[fmt] if fmt != "none" else units * 24, gather=gather, lead=2, tail=5)
+    """Planned for two multiprocessors, so that the widest tiles (pairs of CTAs, but
+    for 1x128) run, each CTA many of them; then for the device's own count."""
+    for sms in (2, 0):
+        with planned_for(sms):
+            run_gemm(fmt, sizes, N, units * ref.UNIT[fmt] if fmt != "none" else units * 24, gather=gather, lead=2, tail=5)
 
 
-def test_grouped_gemm_large_groups_long_products():
-    for fmt in FMTS:
-        run_gemm(fmt, [290, 31], 384, 6144, gather=some_rows)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_gemm_large_groups_long_products(fmt):
+    for sms in (2, 0):
+        with planned_for(sms):
+            run_gemm(fmt, [290, 31], 384, 6144, gather=some_rows)
+
+
+@pytest.mark.parametrize("mean", [20, 50, 100, 200])
+@pytest.mark.parametrize("gather", [None, some_rows], ids=["rows in order", "gathered"])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_gemm_many_tiles_a_cta(fmt, gather, mean):
+    """Every width of tile, three CTAs (or one pair) walking over all of them."""
+    sizes = [mean, 0, mean // 3, 2 * mean + 1, 1, mean + 7]
+    with planned_for(3):
+        run_gemm(fmt, sizes, 392, 11 * ref.UNIT[fmt] if fmt != "none" else 264, gather=gather, tail=3)
+        if fmt != "block128":
+            run_gemm(fmt, sizes, 128, 2 * ref.UNIT[fmt], gather=gather, dtype=torch.float16)
 
 
 def test_grouped_gemm_padding_of_w_scale_is_not_read_into_the_result():
@@ -264,15 +292,13 @@ def test_grouped_gemm_scales_at_any_address():
 
 @pytest.mark.parametrize("sms", [1, 7, 64, 1000])
 def test_planned_for_other_counts_of_multiprocessors(sms):
-    binding.set_sm_budget(sms)
-    try:
+    with planned_for(sms):
         for fmt in FMTS:
             run_gemm(fmt, [300, 1, 77], 264, 1152, gather=some_rows)
             run_gemm(fmt, [3, 0, 1], 136, 3584)
         run_lora(mixed(300, 3), 3, 40, 520, 264)
+        run_lora(mixed(700, 3), 3, 104, 264, 1032, torch.float16)
         run_lora(mixed(30, 9), 9, 16, 520, 264)
-    finally:
-        binding.set_sm_budget(0)
 
 
 def test_offsets_past_32_bits():
