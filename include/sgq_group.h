@@ -149,7 +149,8 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
  * Rows of y that belong to no slot are left as they are. rows must come with
  * slots (both from group_rows with k = 1): a slot s whose token t does not
  * hold slots[t] = s, or whose t is outside [0, T), is passed over, so no row
- * of y is updated twice whatever rows holds. Two launches on the stream.
+ * of y is updated twice whatever rows holds. One launch on the stream where the
+ * slots are few for the adapters (no workspace), two else.
  *
  * Arguments:
  *   flags         SGQ_F_FP16: x, a, b and y are fp16, not bf16 (others rejected)
@@ -165,16 +166,17 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
  *   offsets       [groups + 1] int32, read
  *   rows, slots   [S] and [T] int32, read, or both NULL
  *   y             [T, N], read and written
- *   workspace     sgq_lora_workspace_bytes(S, R) bytes, written (16-byte
- *                 aligned); calls that may run at the same time (other
- *                 streams, graphs) need workspaces of their own
+ *   workspace     sgq_lora_workspace_bytes(S, groups, R) bytes, written
+ *                 (16-byte aligned; may be NULL where that is 0); calls that
+ *                 may run at the same time (other streams, graphs) need
+ *                 workspaces of their own
  */
 int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, int64_t K, int64_t N,
              const void* x, const void* a, const void* b, const float* scaling, const int32_t* offsets,
              const int32_t* rows, const int32_t* slots, void* y, void* workspace, sgq_stream_t stream);
 
-/* Bytes of lora_add's workspace; 0 where S or R is outside its range. */
-int64_t sgq_lora_workspace_bytes(int64_t S, int64_t R);
+/* Bytes of lora_add's workspace; 0 where it needs none, or an argument is outside its range. */
+int64_t sgq_lora_workspace_bytes(int64_t S, int64_t groups, int64_t R);
 
 /*
  * Launches of grouped_gemm and lora_add on the current device, since the

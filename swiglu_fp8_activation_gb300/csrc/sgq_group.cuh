@@ -59,7 +59,7 @@ struct LoraArgs {
     const int32_t* rows;   // or null
     const int32_t* slots;  // null exactly when rows is
     uint16_t* y;
-    void* v;               // workspace, S rows of lora_row_bytes(R)
+    void* v;               // workspace, S rows of lora_row_bytes(R); null with lora_few
     int64_t T;
     int S, groups, R, K, N;
 };
@@ -75,6 +75,12 @@ bool encode_tiles512(CUtensorMap* m, const void* base, int64_t tiles);
 // Bytes of a row of lora_add's workspace: two parts of R 16-bit values, then
 // the row's factor (fp32) and 12 bytes of zeros.
 __host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }
+
+// Whether lora_add runs its form for few slots an adapter (one launch, no
+// workspace): slots an adapter (on average) x rank up to 128. K = N = 4096, this
+// form and the tensor cores' in a graph: rank 16, 2 slots an adapter 9.6 and 21.6
+// us, 8 slots 13.5 and 22.8, 16 slots 25.9 and 20.7; rank 64, 4 slots 19.3 and 14.8.
+constexpr bool lora_few(int64_t S, int64_t groups, int64_t R) { return S * R <= 128 * groups; }
 
 cudaError_t launch_group_rows(const Device& dev, const GroupRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream);

@@ -117,9 +117,9 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
                                    static_cast<cudaStream_t>(stream)));
 }
 
-int64_t sgq_lora_workspace_bytes(int64_t S, int64_t R) {
-    if (S < 0 || S > kMaxRows || R < 1 || R > SGQ_MAX_RANK) return 0;
-    return S * lora_row_bytes((int)R);
+int64_t sgq_lora_workspace_bytes(int64_t S, int64_t groups, int64_t R) {
+    if (S < 0 || S > kMaxRows || groups < 1 || groups > SGQ_MAX_GROUPS || R < 1 || R > SGQ_MAX_RANK) return 0;
+    return lora_few(S, groups, R) ? 0 : S * lora_row_bytes((int)R);
 }
 
 int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, int64_t K, int64_t N, const void* x,
@@ -132,11 +132,12 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
         return SGQ_ERR_UNSUPPORTED;
     if (S == 0 || T == 0) return SGQ_OK;
     if (!rows != !slots || (!rows && S != T)) return SGQ_ERR_INVALID_ARG;
-    if (!x || !a || !b || !offsets || !y || !workspace) return SGQ_ERR_INVALID_ARG;
+    const int64_t ws_bytes = sgq_lora_workspace_bytes(S, groups, R);
+    if (!x || !a || !b || !offsets || !y || (ws_bytes > 0 && !workspace)) return SGQ_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(workspace, 16) ||
         !aligned(scaling, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4))
         return SGQ_ERR_MISALIGNED;
-    const Span out[] = {{y, (size_t)(T * N) * 2}, {workspace, (size_t)sgq_lora_workspace_bytes(S, R)}};
+    const Span out[] = {{y, (size_t)(T * N) * 2}, {workspace, (size_t)ws_bytes}};
     const Span in[] = {{x, (size_t)(T * K) * 2}, {a, (size_t)(groups * R * K) * 2}, {b, (size_t)(groups * N * R) * 2},
                        {scaling, (size_t)groups * 4}, {offsets, (size_t)(groups + 1) * 4}, {rows, (size_t)S * 4},
                        {slots, (size_t)T * 4}};

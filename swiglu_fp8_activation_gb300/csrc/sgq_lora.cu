@@ -1,8 +1,9 @@
 // sgq_lora.cu -- low-rank adapters of many requests, added to a shared
 // projection's output (include/sgq_group.h, lora_add).
 //
-// Two launches, both on the tensor cores (tcgen05) with the slots as the M
-// side, so that a thread owns one slot's row of the result:
+// One launch in plain fp32 for few slots an adapter (below). Else two launches,
+// both on the tensor cores (tcgen05) with the slots as the M side, so that a
+// thread owns one slot's row of the result:
 //
 //   shrink   v = x . a^T, tiles of 128 slots x the whole rank. Bound by the
 //            reading of x (prefill) or of a (decode), so the length of x is
@@ -563,149 +564,133 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
 //
 // A decode batch: one or a few slots an adapter, so that the tensor cores'
 // tiles of 128 slots would be empty and their latency most of the time. Plain
-// fp32 arithmetic instead, v in fp32 in the workspace. A CTA takes up to 8
-// slots of one adapter and each value of a or b once for all of them.
+// fp32 arithmetic instead, in one launch: a cluster of 8 CTAs takes up to 8
+// slots of one adapter, each CTA an eighth of the ranks (every value of a is read
+// once for all slots), then, v having gone round through distributed shared
+// memory, an eighth of the columns of y. As two launches with v in the
+// workspace, 64 rows of 32 adapters (rank 16, K = N = 4096) took 8.0 us in a
+// graph, against 9.6, but 19.8 as a call from Python, against 14.
 
 constexpr int kFew = 8;              // slots a tile
+constexpr int kFewCtas = 8;          // of a cluster
 constexpr int kFewThreads = 256;
-// Slots an adapter (on average) x rank up to which this form runs. K = N = 4096,
-// this form and the tensor cores': rank 16, 16 slots 16.7 and 22.4 us; rank 64,
-// 8 slots 17.2 and 15, 16 slots 21.5 and 15.7; rank 128, 16 slots 25.3 and 14.4.
-constexpr int64_t kFewWork = 256;
-constexpr int kFewRanks = 2;         // ranks a CTA of the shrink takes: 4 warps each, a quarter of K
 
 template <int DT>
-__global__ void __launch_bounds__(kFewThreads) lora_few_shrink_kernel(const LoraArgs l) {
-    extern __shared__ int few_smem[];
-    int* lo = few_smem;
-    int* first = lo + table_ints(l.groups);
-    __shared__ float sums[kFewRanks * 4][kFew];
-    __shared__ int part[kFewThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    pdl_trigger();
-    scan_groups(l.offsets, l.groups, l.S, kFew, lo, first, part);
-    const int blocks = (l.R + kFewRanks - 1) / kFewRanks;
-    int g, s0, m;
-    if (!find_tile(lo, first, l.groups, kFew, blockIdx.x / (uint32_t)blocks, g, s0, m)) return;
-    const int r0 = (int)(blockIdx.x % (uint32_t)blocks) * kFewRanks, r = r0 + warp / 4, slice = warp & 3;   // R is even
-    const int64_t mine = lane < m ? token_of(l, s0 + lane) : -1;
-    const uint16_t* x[kFew];
-#pragma unroll
-    for (int i = 0; i < kFew; ++i) {
-        const int64_t t = __shfl_sync(0xFFFFFFFFu, mine, i);
-        x[i] = t >= 0 ? l.x + t * l.K : nullptr;
-    }
-    const uint16_t* a = l.a + ((int64_t)g * l.R + r) * l.K;
-    float sum[kFew] = {};
-    // chunks of 8 values: lane, 32 + lane, .. of this warp's slice
-    const int chunks = l.K / 8, per = (chunks + 3) / 4, from = slice * per, to = min(chunks, from + per);
-#pragma unroll 4
-    for (int c = from + lane; c < to; c += 32) {
-        float fa[8];
-        load8<DT>(*reinterpret_cast<const uint4*>(a + 8 * c), fa);
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-            if (x[i]) {
-                float fx[8];
-                load8<DT>(*reinterpret_cast<const uint4*>(x[i] + 8 * c), fx);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[i] = fmaf(fa[j], fx[j], sum[i]);
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kFew; ++i) {
-        float v = sum[i];
-#pragma unroll
-        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-        if (lane == 0) sums[warp][i] = v;
-    }
-    __syncthreads();
-    if (tid < kFewRanks * kFew) {
-        const int i = tid % kFew, k = tid / kFew;
-        if (i < m)
-            static_cast<float*>(l.v)[(int64_t)(s0 + i) * l.R + r0 + k] =
-                (sums[4 * k][i] + sums[4 * k + 1][i]) + (sums[4 * k + 2][i] + sums[4 * k + 3][i]);
-    }
-}
-
-// A CTA: up to 8 slots x 512 columns, two columns a thread.
-template <int DT>
-__global__ void __launch_bounds__(kFewThreads) lora_few_expand_kernel(const LoraArgs l) {
+__global__ void __launch_bounds__(kFewThreads) lora_few_kernel(const LoraArgs l) {
     extern __shared__ int few_smem[];
     int* lo = few_smem;
     int* first = lo + table_ints(l.groups);
     __shared__ __align__(16) float v[kFew][kMaxRank];
+    __shared__ float sums[kFewThreads / 32][kFew];
     __shared__ int part[kFewThreads / 32];
-    const int tid = threadIdx.x;
-    // (what may be read before the wait: see lora_expand_kernel)
-    scan_groups(l.offsets, l.groups, l.S, kFew, lo, first, part);
-    const int blocks = (l.N + 2 * kFewThreads - 1) / (2 * kFewThreads);
-    int g, s0, m;
-    if (!find_tile(lo, first, l.groups, kFew, blockIdx.x / (uint32_t)blocks, g, s0, m)) {
-        pdl_wait();
-        pdl_trigger();
-        return;
-    }
-    const int n = ((int)(blockIdx.x % (uint32_t)blocks) * kFewThreads + tid) * 2;
-    const bool in = n < l.N;                             // N is even
-    const int64_t mine = (tid & 31) < m ? token_of(l, s0 + (tid & 31)) : -1;
-    int64_t t[kFew];
-    uint32_t old[kFew];
-#pragma unroll
-    for (int i = 0; i < kFew; ++i) t[i] = __shfl_sync(0xFFFFFFFFu, mine, i);
-#pragma unroll
-    for (int i = 0; i < kFew; ++i)
-        if (t[i] >= 0 && in) old[i] = *reinterpret_cast<const uint32_t*>(l.y + t[i] * l.N + n);
-    const float scale = l.scaling ? l.scaling[g] : 1.0f;
-    const uint16_t* b = l.b + ((int64_t)g * l.N + (in ? n : 0)) * l.R;
-    uint4 b0 = *reinterpret_cast<const uint4*>(b), b1 = *reinterpret_cast<const uint4*>(b + l.R);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster_rank();
+    cluster_arrive_relaxed();
     pdl_wait();
     pdl_trigger();
-    for (int i = tid; i < m * l.R; i += kFewThreads) v[i / l.R][i % l.R] = static_cast<const float*>(l.v)[(int64_t)s0 * l.R + i];
-    __syncthreads();
-    float acc[kFew][2] = {};
-    for (int r = 0; r < l.R; r += 8) {
-        float f0[8], f1[8];
-        load8<DT>(b0, f0);
-        load8<DT>(b1, f1);
-        if (r + 8 < l.R) {
-            b0 = *reinterpret_cast<const uint4*>(b + r + 8);
-            b1 = *reinterpret_cast<const uint4*>(b + l.R + r + 8);
+    scan_groups(l.offsets, l.groups, l.S, kFew, lo, first, part);
+    cluster_wait();                  // every CTA of the cluster runs: its shared memory may be written
+    int g, s0, m;
+    if (!find_tile(lo, first, l.groups, kFew, blockIdx.x / kFewCtas, g, s0, m)) return;     // the whole cluster
+    const int64_t mine = lane < m ? token_of(l, s0 + lane) : -1;
+    int64_t t[kFew];
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) t[i] = __shfl_sync(0xFFFFFFFFu, mine, i);
+
+    // this CTA's columns, two a thread at a time; the first ones' values are read ahead
+    const int columns = (l.N / 2 + kFewCtas - 1) / kFewCtas * 2, n_to = min(l.N, (rank + 1) * columns);
+    int n = rank * columns + 2 * tid;
+    uint32_t old[kFew];
+    uint4 b0 = {}, b1 = {};
+    auto read = [&]() {
+        if (n >= n_to) return;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+            if (t[i] >= 0) old[i] = *reinterpret_cast<const uint32_t*>(l.y + t[i] * l.N + n);
+        const uint16_t* b = l.b + ((int64_t)g * l.N + n) * l.R;
+        b0 = *reinterpret_cast<const uint4*>(b);
+        b1 = *reinterpret_cast<const uint4*>(b + l.R);
+    };
+    read();
+
+    // v of two ranks at a time, four warps each, a quarter of K a warp
+    for (int r0 = 2 * rank; r0 < l.R; r0 += 2 * kFewCtas) {
+        const uint16_t* a = l.a + ((int64_t)g * l.R + r0 + warp / 4) * l.K;
+        float sum[kFew] = {};
+        const int chunks = l.K / 8, per = (chunks + 3) / 4, from = (warp & 3) * per, to = min(chunks, from + per);
+#pragma unroll 4
+        for (int c = from + lane; c < to; c += 32) {
+            float fa[8];
+            load8<DT>(*reinterpret_cast<const uint4*>(a + 8 * c), fa);
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                if (t[i] >= 0) {
+                    float fx[8];
+                    load8<DT>(*reinterpret_cast<const uint4*>(l.x + t[i] * l.K + 8 * c), fx);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[i] = fmaf(fa[j], fx[j], sum[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], d);
+            if (lane == 0) sums[warp][i] = sum[i];
+        }
+        __syncthreads();
+        if (tid < 2 * kFew * kFewCtas) {
+            const int i = tid % kFew, k = tid / kFew % 2;
+            st_cluster4(&v[i][r0 + k], (uint32_t)(tid / (2 * kFew)),
+                        (sums[4 * k][i] + sums[4 * k + 1][i]) + (sums[4 * k + 2][i] + sums[4 * k + 3][i]));
+        }
+        __syncthreads();
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+
+    const float scale = l.scaling ? l.scaling[g] : 1.0f;
+    while (n < n_to) {
+        const uint16_t* b = l.b + ((int64_t)g * l.N + n) * l.R;
+        float acc[kFew][2] = {};
+        for (int r = 0; r < l.R; r += 8) {
+            float f0[8], f1[8];
+            load8<DT>(b0, f0);
+            load8<DT>(b1, f1);
+            if (r + 8 < l.R) {
+                b0 = *reinterpret_cast<const uint4*>(b + r + 8);
+                b1 = *reinterpret_cast<const uint4*>(b + l.R + r + 8);
+            }
+#pragma unroll
+            for (int i = 0; i < kFew; ++i)
+                if (i < m) {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(&v[i][r + j]);
+                        acc[i][0] = fmaf(w.x, f0[j], fmaf(w.y, f0[j + 1], fmaf(w.z, f0[j + 2], fmaf(w.w, f0[j + 3], acc[i][0]))));
+                        acc[i][1] = fmaf(w.x, f1[j], fmaf(w.y, f1[j + 1], fmaf(w.z, f1[j + 2], fmaf(w.w, f1[j + 3], acc[i][1]))));
+                    }
+                }
         }
 #pragma unroll
         for (int i = 0; i < kFew; ++i)
-            if (i < m) {
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const float4 w = *reinterpret_cast<const float4*>(&v[i][r + j]);
-                    acc[i][0] = fmaf(w.x, f0[j], fmaf(w.y, f0[j + 1], fmaf(w.z, f0[j + 2], fmaf(w.w, f0[j + 3], acc[i][0]))));
-                    acc[i][1] = fmaf(w.x, f1[j], fmaf(w.y, f1[j + 1], fmaf(w.z, f1[j + 2], fmaf(w.w, f1[j + 3], acc[i][1]))));
-                }
+            if (t[i] >= 0) {
+                const float2 was = DT == DT_BF16 ? make_float2(__uint_as_float(old[i] << 16), __uint_as_float(old[i] & 0xFFFF0000u))
+                                                 : f16x2_to_f32x2(old[i]);
+                *reinterpret_cast<uint32_t*>(l.y + t[i] * l.N + n) =
+                    pack2<DT>(fmaf(scale, acc[i][0], was.x), fmaf(scale, acc[i][1], was.y));
             }
+        n += 2 * kFewThreads;
+        read();
     }
-#pragma unroll
-    for (int i = 0; i < kFew; ++i)
-        if (t[i] >= 0 && in) {
-            const float2 was = DT == DT_BF16 ? make_float2(__uint_as_float(old[i] << 16), __uint_as_float(old[i] & 0xFFFF0000u))
-                                             : f16x2_to_f32x2(old[i]);
-            *reinterpret_cast<uint32_t*>(l.y + t[i] * l.N + n) =
-                pack2<DT>(fmaf(scale, acc[i][0], was.x), fmaf(scale, acc[i][1], was.y));
-        }
 }
 
 template <int DT>
 cudaError_t run_few(const Device& dev, const LoraArgs& l, cudaStream_t stream) {
     const int64_t tiles = (int64_t)l.S / kFew + (l.S < l.groups ? l.S : l.groups);   // at most
-    const int64_t shrink = tiles * ((l.R + kFewRanks - 1) / kFewRanks);
-    const int64_t expand = tiles * ((l.N + 2 * kFewThreads - 1) / (2 * kFewThreads));
-    if (shrink > 0x7FFFFFFF || expand > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const int smem = 2 * 4 * table_ints(l.groups);
-    const cudaError_t e =
-        launch_grid(lora_few_shrink_kernel<DT>, dim3((unsigned)shrink), kFewThreads, smem, 1, dev.id, l, stream);
-    if (e != cudaSuccess) return e;
-    return launch_grid(lora_few_expand_kernel<DT>, dim3((unsigned)expand), kFewThreads, smem, 1, dev.id, l, stream);
+    if (tiles > 0x7FFFFFFF / kFewCtas) return cudaErrorInvalidConfiguration;
+    return launch_grid(lora_few_kernel<DT>, dim3((unsigned)(tiles * kFewCtas)), kFewThreads, 2 * 4 * table_ints(l.groups),
+                       kFewCtas, dev.id, l, stream);
 }
 
 template <int DT, int BEHIND>
@@ -730,7 +715,7 @@ cudaError_t expand(const Device& dev, ExpandParams& p, int64_t tiles, cudaStream
 
 template <int DT>
 cudaError_t run(const Device& dev, const LoraArgs& l, cudaStream_t stream) {
-    if ((int64_t)l.S * l.R <= kFewWork * l.groups) return run_few<DT>(dev, l, stream);
+    if (lora_few(l.S, l.groups, l.R)) return run_few<DT>(dev, l, stream);
     ShrinkParams p;
     p.l = l;
     p.kbytes = 2 * l.K;

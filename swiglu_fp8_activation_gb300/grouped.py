@@ -39,7 +39,7 @@ def _lib() -> C.CDLL:
         L.sgq_wait_timeouts.restype = C.c_int
         L.sgq_wait_timeouts.argtypes = [C.POINTER(C.c_uint32)]
         L.sgq_lora_workspace_bytes.restype = i64
-        L.sgq_lora_workspace_bytes.argtypes = [i64, i64]
+        L.sgq_lora_workspace_bytes.argtypes = [i64, i64, i64]
         _bound = L
     return L
 
@@ -238,24 +238,24 @@ def wait_timeouts() -> int:
     return n.value
 
 
-def lora_workspace_bytes(S: int, R: int) -> int:
-    """Bytes of lora_add's workspace for S slots and rank R (0 out of range)."""
-    return _lib().sgq_lora_workspace_bytes(int(S), int(R))
+def lora_workspace_bytes(S: int, groups: int, R: int) -> int:
+    """Bytes of lora_add's workspace (0 where it needs none, or out of range)."""
+    return _lib().sgq_lora_workspace_bytes(int(S), int(groups), int(R))
 
 
 def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, offsets: torch.Tensor, *,
              rows: torch.Tensor | None = None, slots: torch.Tensor | None = None,
              scaling: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The low-rank adapters of many requests, added in place to a shared
-    projection's output (two kernel launches): for slot s of adapter g with
+    projection's output (one kernel launch, or two): for slot s of adapter g with
     t = rows[s], y[t] += scaling[g] * (x[t] @ a[g].T) @ b[g].T, in fp32.
 
     x [T, K], a [groups, R, K], b [groups, N, R] and y [T, N]: all bfloat16 or
     all float16. offsets, rows, slots: group_rows of the requests' adapters
     ([T] ids, -1 for none); rows and slots both None where the rows of x
     already are in adapter order (slot s is row s). scaling [groups] float32 or
-    None (ones). workspace: uint8 [lora_workspace_bytes(S, R)] or None
-    (allocated). Rows without an
+    None (ones). workspace: uint8 [lora_workspace_bytes(S, groups, R)]
+    or None (allocated where one is needed). Rows without an
     adapter stay as they are. Returns y.
     """
     T, K = _dims(x, 2, "x")
@@ -276,16 +276,17 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
         _need(slots, (T, 1) if slots.dim() == 2 else (T,), torch.int32, "slots")
     if scaling is not None:
         _need(scaling, (groups,), torch.float32, "scaling")
+    room = 0 if S * R <= 128 * groups else S * (4 * R + 16)      # lora_workspace_bytes(S, groups, R)
     if workspace is not None:
-        _need(workspace, (S * (4 * R + 16),), torch.uint8, "workspace")
+        _need(workspace, (room,), torch.uint8, "workspace")
     at = _here(stream, "lora_add", x, a, b, y, offsets, rows, slots, scaling, workspace)
     if at is None:
         with _there(stream, x):
             return lora_add(x, a, b, y, offsets, rows=rows, slots=slots, scaling=scaling, workspace=workspace)
-    if workspace is None:
-        workspace = torch.empty((S * (4 * R + 16),), dtype=torch.uint8, device=x.device)      # lora_workspace_bytes(S, R)
+    if workspace is None and room:
+        workspace = torch.empty((room,), dtype=torch.uint8, device=x.device)
     st = _lib().lora_add(F_FP16 if dt == torch.float16 else 0, T, S, groups, R, K, N, x.data_ptr(), a.data_ptr(), b.data_ptr(),
-                      _at(scaling), offsets.data_ptr(), _at(rows), _at(slots), y.data_ptr(), workspace.data_ptr(), at)
+                      _at(scaling), offsets.data_ptr(), _at(rows), _at(slots), y.data_ptr(), _at(workspace), at)
     if st:
         _check(st, "lora_add")
     return y

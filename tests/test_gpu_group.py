@@ -391,7 +391,7 @@ def run_lora(ids, G, R, K, N, dtype=torch.bfloat16, scaled=True, seed=0, sorted_
     res, tol = ref.lora(x, a, b, y, offsets, rows, slots, scaling, T)
     out, untouched = guarded((T, N), dtype)
     out.copy_(y)
-    ws, ws_untouched = guarded((sgq.lora_workspace_bytes(T, R),), torch.uint8)
+    ws, ws_untouched = guarded((sgq.lora_workspace_bytes(T, G, R),), torch.uint8)
     dx, da, db, doff, drows, dslots, dc = cuda(x, a, b, offsets, rows, slots, scaling)
     got = sgq.lora_add(dx, da, db, out, doff, rows=drows, slots=dslots, scaling=dc, workspace=ws)
     assert got is out
@@ -417,8 +417,10 @@ def test_lora_ranks(R, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("R", [8, 24, 56, 128])
 def test_lora_ranks_few_slots_an_adapter(R, dtype):
-    run_lora(mixed(90, 20), 20, R, 520, 1032, dtype)
-    run_lora([3] * 40 + mixed(20, 16), 16, R, 136, 520, dtype)      # 40 slots of one, few on average
+    G = 90 * R // 128 + 1                                           # few enough slots an adapter
+    run_lora(mixed(90, G), G, R, 520, 1032, dtype)
+    run_lora([3] * 40 + mixed(20, 6), 60, R, 136, 520, dtype)       # 40 slots of one, few on average
+    run_lora(mixed(5, 6), 6, R, 4104, 8200, dtype)
 
 
 @pytest.mark.parametrize("T,G,K,N", [(1, 1, 8, 8), (1, 5, 1024, 2048), (2, 2, 4096, 72), (64, 32, 512, 512), (65, 64, 136, 1032), (333, 3, 1000, 264),

@@ -133,7 +133,7 @@ def test_combine_refusals(L):
     assert comb(L, out=P(0, 16 * 64 * 2 - 16)) == INVALID
 
 
-def lora(L, flags=0, T=8, S=8, G=2, R=16, K=64, N=128, x=P(0), a=P(1), b=P(2), c=P(3), off=P(4), r=P(5), s=P(6), y=P(7), ws=P(8)):
+def lora(L, flags=0, T=64, S=64, G=2, R=16, K=64, N=128, x=P(0), a=P(1), b=P(2), c=P(3), off=P(4), r=P(5), s=P(6), y=P(7), ws=P(8)):
     return refused(L.lora_add(flags, T, S, G, R, K, N, x, a, b, c, off, r, s, y, ws, None))
 
 
@@ -161,11 +161,13 @@ def test_lora_refusals(L):
         assert lora(L, y=P(i)) == INVALID, i
         assert lora(L, ws=P(i)) == INVALID, i
     assert lora(L, ws=P(7)) == INVALID
-    assert L.sgq_lora_workspace_bytes(8, 16) == 8 * (16 * 4 + 16)
-    assert L.sgq_lora_workspace_bytes(8, 200) == 0
-    for S, R in ((1, 8), (77, 40), (1 << 30, 128)):
-        assert sgq.lora_workspace_bytes(S, R) == S * (4 * R + 16)      # what lora_add allocates
-    assert L.sgq_lora_workspace_bytes(-1, 8) == 0
+    assert L.sgq_lora_workspace_bytes(64, 2, 16) == 64 * (16 * 4 + 16)
+    assert L.sgq_lora_workspace_bytes(64, 2, 200) == 0
+    assert L.sgq_lora_workspace_bytes(-1, 2, 8) == 0
+    assert L.sgq_lora_workspace_bytes(64, 0, 8) == 0
+    for S, G, R in ((1, 1, 8), (77, 4, 40), (64, 32, 16), (8, 1, 16), (9, 1, 16), (1 << 30, 1024, 128)):
+        # what the Python lora_add allocates
+        assert sgq.lora_workspace_bytes(S, G, R) == (0 if S * R <= 128 * G else S * (4 * R + 16))
     assert L.sgq_wait_timeouts(None) == INVALID
 
 
@@ -217,7 +219,7 @@ def test_python_refusals():
     no(sgq.lora_add, *args, rows=i32(4))                                        # rows without slots
     no(sgq.lora_add, *args, rows=i32(4), slots=i32(3))
     no(sgq.lora_add, *args, scaling=torch.zeros(3))
-    no(sgq.lora_add, *args, workspace=u8(4 * 8 * 4))
+    no(sgq.lora_add, *args, workspace=u8(7))
     no(sgq.lora_add, args[0], args[1], bf(2, 8, 32), args[3], off)              # b transposed
     no(sgq.lora_add, args[0], args[1].half(), args[2], args[3], off)
     no(sgq.lora_add, *args)                                                     # on the CPU
