@@ -24,6 +24,18 @@
 //         asynchronous copies into the swizzled layout. (TMA's four-row gather
 //         took 76 cycles an instruction of 512 bytes: 32768 MXFP8 rows of N =
 //         4096, K = 6144 ran in 3687 us with it.)
+// Large groups run on pairs of CTAs (cta_group::2): 256 channels by 224 or 256
+// slots, each CTA holding its 128 channels and half of the slots' rows, which
+// halves what it fetches and reads of them. Where tiles are very few, the CTAs of
+// a cluster share the K of one and sum the parts through distributed shared
+// memory. pick() below has the rule, with both sides measured.
+//
+// What bounds it: the weights' bytes for small groups (64 x 8 MXFP8 rows of 64
+// experts, N = K = 4096: 143 us, 7.7 TB/s), the tensor cores for large ones (32768
+// rows, N = 4096, K = 6144, in order: MXFP8 529 us, 3115 TFLOP/s, per-token 496; 8192
+// bf16 rows, N = K = 8192: 586 us, 1876 TFLOP/s), the epilogue's sums with 1x128
+// scales (985 us for those 32768 rows).
+//
 // Two accumulators in tensor memory let the epilogue of one tile run under
 // the products of the next. With 1x128 scales, which fp32 holds and no block
 // scale of the tensor core can, every chunk is its own accumulator (two pairs)
@@ -43,11 +55,12 @@ namespace sgq {
 namespace {
 
 constexpr int kGatherThreads = 128;
-constexpr int kM = 128;            // channels a tile
+constexpr int kM = 128;              // channels a tile
 constexpr int kScaleThreads = 64;
 constexpr int kTurn = 32 * 64;       // bytes in which an epilogue warp turns 32 slots x 32 channels
 constexpr int kTurnPitch = 80;       // ... with 1x128 scales in rows of 64 + 16 bytes, free of bank conflicts
-constexpr int kScaleBufs = 4;      // chunks whose scales tensor memory holds
+constexpr int kScaleBufs = 4;        // chunks whose scales tensor memory holds: copies and products of one
+                                     // thread run in order, and a place is written again 4 chunks later
 
 struct alignas(128) GemmParams {
     CUtensorMap mw;                // w as bytes [groups][N][K], box 128 x 128 rows

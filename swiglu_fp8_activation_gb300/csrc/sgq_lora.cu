@@ -13,6 +13,9 @@
 //   expand   y += c (v . b^T), tiles of 128 slots x 128 columns. Bound
 //            by reading and writing y.
 //
+// 8192 rows of 8 adapters, rank 64, K = 4096, N = 8192: 73 us, 20 and 53 (347 MB,
+// 51 us at the copy bandwidth).
+//
 // v is kept to about 16 bits and more between them: a row of the workspace
 // holds v as two 16-bit parts, hi = round(v) and lo = round(v - hi), and the
 // expand product runs over both, so that rounding v costs 2^-17 of it and not
