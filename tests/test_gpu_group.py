@@ -581,3 +581,64 @@ def test_expert_layer_in_a_graph_and_two_streams():
     torch.cuda.synchronize()
     for m, r in zip(layers, outs):
         m.check(r)
+
+
+def test_many_calls_on_several_streams():
+    """Calls of every form at once on four streams, each equal, bit for bit, to the same call alone."""
+    calls = []                                   # (name, function that makes its outputs)
+
+    def gemm(fmt, sizes, N, K, gather, seed):
+        off = sizes_to_offsets(sizes)
+        S, G = sum(sizes), len(sizes)
+        x, xs, w, ws = ref.operands(fmt, S, G, N, K, seed)
+        dx, dxs, dw, doff = cuda(x, xs, w, off)
+        dws = None if ws is None else (ref.swizzled(ws) if fmt == "mxfp8" else ws).to(DEV)
+        rows = some_rows(S, S).to(DEV) if gather else None
+        calls.append((f"{fmt} {sizes}", lambda: sgq.grouped_gemm(dx, dw, doff, fmt=fmt, x_scale=dxs, w_scale=dws, rows=rows)))
+
+    for i, fmt in enumerate(FMTS):
+        gemm(fmt, [1, 0, 2], 264, 4096, True, i)                  # a cluster a tile
+        gemm(fmt, [9, 17, 3, 0, 30] * 8, 1024, 512, i % 2 == 0, i)       # narrow tiles
+        gemm(fmt, [1500, 900], 2048, 512, i % 2 == 1, i)                 # pairs of CTAs, or the widest tiles
+    for T, G, R, N in ((40, 20, 16, 1032), (900, 3, 64, 2048), (500, 2, 128, 520)):
+        r = ref.gen(T)
+        x, y = torch.randn(T, 512, generator=r).to(torch.bfloat16).to(DEV), torch.randn(T, N, generator=r).to(torch.bfloat16).to(DEV)
+        a, b = torch.randn(G, R, 512, generator=r).to(torch.bfloat16).to(DEV), torch.randn(G, N, R, generator=r).to(torch.bfloat16).to(DEV)
+        o, rows, slots = sgq.group_rows(torch.tensor(mixed(T, G), dtype=torch.int32, device=DEV), G)
+        calls.append((f"lora {T}", lambda x=x, a=a, b=b, y=y, o=o, rows=rows, slots=slots:
+                      sgq.lora_add(x, a, b, y.clone(), o, rows=rows, slots=slots)))
+    ids = torch.randint(-1, 200, (9000, 4), generator=ref.gen(5)).to(torch.int32).to(DEV)
+    calls.append(("group_rows", lambda: sgq.group_rows(ids, 200)[1]))
+    torch.cuda.synchronize()
+    alone = []
+    for _, f in calls:
+        alone.append(f())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for turn in range(6):
+        got = []
+        for i in range(4 * len(calls)):
+            name, f = calls[(i * 5 + turn) % len(calls)]
+            with torch.cuda.stream(streams[i % 4]):
+                got.append(((i * 5 + turn) % len(calls), f()))
+        torch.cuda.synchronize()
+        for k, t in got:
+            assert torch.equal(t.view(torch.uint8), alone[k].view(torch.uint8)), calls[k][0]
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(seed):
+    """Shapes, formats, indices and plans drawn at random."""
+    import random
+    r = random.Random(1000 + seed)
+    sms = r.choice((0, 0, 1, 3, 20))
+    with planned_for(sms):
+        fmt = r.choice(FMTS)
+        unit = ref.UNIT[fmt]
+        sizes = [r.choice((0, 1, r.randint(0, 40), r.randint(0, 400))) for _ in range(r.randint(1, 9))]
+        run_gemm(fmt, sizes, 8 * r.randint(1, 80), unit * r.randint(1, max(1, 2600 // unit)), seed=seed,
+                 gather=r.choice((None, some_rows, wild_rows)), lead=r.choice((0, 3)), tail=r.choice((0, 50)),
+                 dtype=r.choice((torch.bfloat16, torch.float16)))
+        T, G = r.choice((1, r.randint(1, 40), r.randint(1, 900))), r.randint(1, 40)
+        run_lora(mixed(T, G, seed, r.choice((0.0, 0.5))), G, 8 * r.randint(1, 16), 8 * r.randint(1, 200), 8 * r.randint(1, 200),
+                 r.choice((torch.bfloat16, torch.float16)), scaled=r.random() < 0.7, seed=seed)
