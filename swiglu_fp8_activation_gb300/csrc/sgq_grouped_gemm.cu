@@ -16,8 +16,9 @@
 //   0     copies: the weights' tile by TMA, their scales as 512-byte tiles
 //         (MXFP8), the slots' rows as a box where they follow one another
 //   1     the products (one thread), four instructions of 32 bytes of K a chunk
-//   2, 3  the slots' scales (MXFP8 and 1x128): row-major in memory, written
-//         into the operand's layout in shared memory
+//         (with 1x128 scales warp 3 issues half of them)
+//   2, 3  the slots' scales (MXFP8, and 1x128 in warp 2): row-major in memory,
+//         written into the operand's layout in shared memory
 //   4-7   the epilogue, one quarter of the channels each (with 1x128 scales
 //         4-11, one quarter of the slots and half of the channels each)
 //   last 4  with row indices: the slots' rows, gathered in 16-byte
@@ -34,7 +35,7 @@
 // experts, N = K = 4096: 143 us, 7.7 TB/s), the tensor cores for large ones (32768
 // rows, N = 4096, K = 6144, in order: MXFP8 529 us, 3115 TFLOP/s, per-token 496; 8192
 // bf16 rows, N = K = 8192: 586 us, 1876 TFLOP/s), the epilogue's sums with 1x128
-// scales (985 us for those 32768 rows).
+// scales (827 us for those 32768 rows).
 //
 // Two accumulators in tensor memory let the epilogue of one tile run under
 // the products of the next. With 1x128 scales, which fp32 holds and no block
@@ -56,7 +57,6 @@ namespace {
 
 constexpr int kGatherThreads = 128;
 constexpr int kM = 128;              // channels a tile
-constexpr int kScaleThreads = 64;
 constexpr int kTurn = 32 * 64;       // bytes in which an epilogue warp turns 32 slots x 32 channels
 constexpr int kTurnPitch = 80;       // ... with 1x128 scales in rows of 64 + 16 bytes, free of bank conflicts
 constexpr int kScaleBufs = 4;        // chunks whose scales tensor memory holds: copies and products of one
@@ -72,6 +72,8 @@ struct alignas(128) GemmParams {
     int kbytes;                    // bytes of a row
     int f16;                       // out (and 16-bit operands) are fp16
     int split;                     // CTAs of a cluster that share a tile's K (1: none)
+    int across;                    // tiles of channels (a pair's: 256) beside one another
+    int step_q, step_r;            // from one of a CTA's tiles to its next: tiles of slots, and of channels
     int xs_align;                  // 16, 4 or 1: alignment of every 4-byte (4 chunks: 16-byte) piece of x_scale
 };
 
@@ -85,6 +87,7 @@ struct Cfg {
     static constexpr int kSx = kMx ? 512 * kHalves : 0;           // slots' scales of a chunk
     static constexpr int kStage = kW + kX + kSw + kSx;
     static constexpr int kEpiWarps = kB128 ? 8 : 4;
+    static constexpr int kScaleThreads = kB128 ? 32 : 64;         // warp 2, and 3 where it issues no products
     // fp32 scales of the slots: for each quarter of the channels, or for each accumulator
     static constexpr int kXbuf = FMT == FMT_PT || kB128 ? 4 * 4 * BN : 0;
     static constexpr int kTurnBytes = kB128 ? 32 * kTurnPitch : kTurn;
@@ -106,27 +109,36 @@ struct Cfg {
     static_assert(kNeed <= 512 && kStages >= 3, "tile too large");
 };
 
-// The tiles of one CTA in order: slots [s0, s0 + m) of group g, channels from n0 on.
+// The tiles of one CTA in order: slots [s0, s0 + m) of group g, channels from
+// n0 on. The q-th tile of slots and the r-th of the channels' are stepped
+// without divisions, which every role of the CTA would wait for at every tile
+// (1x128, 16384 rows, N = 4096, K = 1536: 156 us with 64-bit divisions, 141 without).
 struct Walk {
     const int* lo;
     const int* first;
-    int n_tiles, bn, ctas, rank;     // tiles of `ctas` x 128 channels, this CTA's being the rank-th 128
-    int64_t tile, end;
+    const GemmParams& p;
+    int bn, ctas, rank;              // tiles of `ctas` x 128 channels, this CTA's being the rank-th 128
+    int q, r, end;
     int g, s0, m, n0;
 
-    __device__ Walk(const int* lo_, const int* first_, int G, int n_tiles_, int bn_, int ctas_)
-        : lo(lo_), first(first_), n_tiles((n_tiles_ + ctas_ - 1) / ctas_), bn(bn_), ctas(ctas_), rank((int)(blockIdx.x % ctas_)),
-          tile(blockIdx.x / ctas_), end((int64_t)first_[G] * n_tiles), g(0) {}
+    __device__ Walk(const int* lo_, const int* first_, const GemmParams& p_, int bn_, int ctas_, uint32_t from)
+        : lo(lo_), first(first_), p(p_), bn(bn_), ctas(ctas_), rank((int)(blockIdx.x % ctas_)), q((int)(from / (uint32_t)p_.across)),
+          r((int)(from % (uint32_t)p_.across)), end(first_[p_.a.groups]), g(0) {}
     __device__ bool next() {
-        if (tile >= end) return false;
-        const int q = (int)(tile / n_tiles);
+        if (q >= end) return false;
         while (first[g + 1] <= q) ++g;
         s0 = lo[g] + (q - first[g]) * bn;
         m = min(bn, lo[g + 1] - s0);
-        n0 = ((int)(tile % n_tiles) * ctas + rank) * kM;
-        tile += gridDim.x / ctas;
+        n0 = (r * ctas + rank) * kM;
+        q += p.step_q;
+        r += p.step_r;
+        if (r >= p.across) {
+            r -= p.across;
+            ++q;
+        }
         return true;
     }
+    __device__ void stop() { end = 0; }
 };
 
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
@@ -146,7 +158,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
     uint8_t* turns = reinterpret_cast<uint8_t*>(xbuf) + C::kXbuf;         // [epilogue warps][32 slots][32 channels]
     float* parts = reinterpret_cast<float*>(turns + C::kEpiWarps * C::kTurnBytes);   // [split][BN / split][128 channels]
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(parts) + C::kParts);
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 6);
     int* part = reinterpret_cast<int*>(misc + 4);                        // 24 ints
     volatile uint32_t* stop = misc + 1;
     const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kStages;
@@ -161,15 +173,16 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             // the copies' thread and the warps that write scales or rows (in a pair, of both CTAs)
-            const int writers = (C::kMx ? kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0);
+            const int writers = (C::kMx ? C::kScaleThreads / 32 : 0) + (gather ? kGatherThreads / 32 : 0);
             tc::bar_init(full + 8 * i, 1 + (PAIR ? 2 : 1) * writers);
             tc::bar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < C::kAccs; ++i) {
-            tc::bar_init(acc_full + 8 * i, 1 + (C::kB128 ? kScaleThreads / 32 : 0));
+            tc::bar_init(acc_full + 8 * i, 1 + (C::kB128 ? C::kScaleThreads / 32 : 0));
             tc::bar_init(acc_empty + 8 * i, (PAIR ? 2 : 1) * C::kEpiWarps);
         }
         tc::bar_init(done, 1);
+        tc::bar_init(done + 8, 1);
         tc::fence_barrier_init();
         *stop = 0;
         tc::prefetch_map(&p.mw);
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
     // start only now that this CTA has its own
     pdl_trigger();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
-    Walk walk(lo, first, a.groups, p.n_tiles, BN, PAIR ? 2 : 1);
+    Walk walk(lo, first, p, BN, PAIR ? 2 : 1, blockIdx.x / (SPLIT ? (uint32_t)p.split : PAIR ? 2 : 1));
     // Where few tiles would leave multiprocessors idle, the CTAs of a cluster
     // share one: each takes a piece of K (a multiple of 4 chunks), and each sums
     // the pieces, in order, for some of the slots.
@@ -200,11 +213,10 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
     if (SPLIT) {
         part_no = (int)(blockIdx.x % (uint32_t)p.split);
         share = BN / p.split;
-        walk.tile = blockIdx.x / (uint32_t)p.split;                      // and no second one
         const int per = ((chunks + p.split - 1) / p.split + 3) & ~3;
         k_from = min(chunks, part_no * per);
         k_to = min(chunks, k_from + per);
-        if (k_from == k_to) walk.tile = walk.end;
+        if (k_from == k_to) walk.stop();
     }
     // In a pair the first CTA issues the products: what makes a stage full, and
     // an accumulator free, arrives at its barriers, and the products' ends at both CTAs'.
@@ -257,13 +269,71 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                 never = 0;
             }
         }
+    } else if (C::kB128 && (warp == 1 || warp == 3)) {
+        // ------------------------------------- products with 1x128 scales
+        // Two chunks fill a pair of accumulators. Warp 1 issues for the even pairs
+        // and warp 3 for the odd ones: the issuing thread is held while its
+        // products run, and what it does between (three waits, the votes, the
+        // descriptors) runs under the other's products (32768 rows, N = 4096, K =
+        // 6144: 972 us with warp 1 alone, 833 with both).
+        const int mine = warp >> 1;
+        const uint64_t base = tc::desc_sw128(tiles_at);
+        const uint32_t idesc = (1u << 4) | ((kM >> 3) << 17) | ((kM >> 4) << 24);
+        const uint32_t d = tmem + mine * C::kAccWidth, acc_bars = 8 * mine;
+        int st = 0;
+        uint32_t ph = 0, use = 0;
+        bool ok = true;
+        auto products = [&](uint32_t to) {                               // of the next stage
+            ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(full + 8 * st, ph, stop));
+            if (!ok) return;
+            tc::fence_after();
+            if (tc::elect()) {
+                const uint64_t dw = base + (uint32_t)(st * ((C::kW + C::kX) >> 4)), dx = dw + (C::kW >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc::mma_f8(to, dx + 2 * k, dw + 2 * k, idesc, k > 0);
+                tc::commit(empty + 8 * st);
+            }
+            __syncwarp();
+        };
+        auto step = [&]() {
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        };
+        while (ok && walk.next()) {
+            for (int kc = k_from; kc < k_to; kc += 2, ++use) {
+                const bool two = kc + 1 < k_to;
+                if ((use & 1) == (uint32_t)mine) {
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_empty + acc_bars, ((use >> 1) & 1) ^ 1, stop));
+                    if (ok) products(d);
+                    step();
+                    if (ok && two) {
+                        products(d + kM);
+                    }
+                    if (two) step();
+                    if (!ok) break;
+                    if (tc::elect()) tc::commit(acc_full + acc_bars);
+                    __syncwarp();
+                } else {
+                    step();
+                    if (two) step();
+                }
+            }
+        }
+        if (!ok) {
+            uint32_t never = 0;
+            if (tc::elect()) tc::commit(done + 8 * mine);
+            __syncwarp();
+            tc::bar_wait(done + 8 * mine, 0, &never, 1 << 27);
+        }
     } else if (warp == 1) {
         // -------------------------------------------------------- products
         int st = 0, use = 0;
         uint32_t ph = 0, chunk_no = 0;
         bool ok = true, ready = false;
         while (ok && leader && walk.next()) {
-            const uint32_t n = C::kB128 ? kM : (uint32_t)columns(walk.m);
+            const uint32_t n = (uint32_t)columns(walk.m);
             constexpr int kRows = PAIR ? 2 * kM : kM;
             uint32_t idesc;
             if (C::kMx) idesc = ((n >> 3) << 17) | (1u << 23) | ((kRows >> 7) << 27);
@@ -275,12 +345,12 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                 const int buf = use % C::kAccs;
                 if (!ready) {
                     ok = true;
-                    if (C::kB128 ? (kc & 1) == 0 : kc == k_from) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
+                    if (kc == k_from) ok = tc::bar_wait<PAIR>(acc_empty + 8 * buf, ((use / C::kAccs) & 1) ^ 1, stop);
                     ok = __all_sync(0xFFFFFFFFu, ok && tc::bar_wait<PAIR>(full + 8 * st, ph, stop));
                     if (!ok) break;
                 }
                 tc::fence_after();
-                const bool done_acc = kc == k_to - 1 || (C::kB128 && (kc & 1));
+                const bool done_acc = kc == k_to - 1;
                 const int next_st = st + 1 == kStages ? 0 : st + 1;
                 const uint32_t next_ph = ph ^ (next_st == 0);
                 // whether the next chunk can follow at once: asked for now, so that
@@ -291,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                 if (tc::elect()) {
                     const uint32_t w_at = tiles_at + st * (C::kW + C::kX);
                     const uint64_t dw = tc::desc_sw128(w_at), dx = tc::desc_sw128(w_at + C::kW);
-                    const uint32_t d = tmem + buf * C::kAccWidth + (C::kB128 ? (kc & 1) * kM : 0);
+                    const uint32_t d = tmem + buf * C::kAccWidth;
                     const uint32_t sw = tmem + C::kAccCols + (chunk_no % kScaleBufs) * 4 * (1 + C::kHalves), sx = sw + 4;
                     if (C::kMx) {
                         const uint32_t s_at = scales_at + st * (C::kSw + C::kSx);
@@ -303,11 +373,10 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                     const int steps = kc == chunks - 1 ? last_steps : 4;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t add = k > 0 || (!C::kB128 && kc > k_from);
+                        const uint32_t add = k > 0 || kc > k_from;
                         if (k >= steps) break;
                         if (C::kMx) tc::mma_mx8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc | (k << 4) | (k << 29), sw, sx, add);
                         else if (FMT == FMT_16BIT) tc::mma_f16<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
-                        else if (C::kB128) tc::mma_f8<PAIR>(d, dx + 2 * k, dw + 2 * k, idesc, add);
                         else tc::mma_f8<PAIR>(d, dw + 2 * k, dx + 2 * k, idesc, add);
                     }
                     tc::commit<PAIR>(empty + 8 * st);
@@ -328,7 +397,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
     } else if (warp < 4) {
         // ------------------------------------------------- scales of the slots
         if (C::kMx || C::kB128) {
-            constexpr int kRows = (BN + kScaleThreads - 1) / kScaleThreads;
+            constexpr int kScaleThreads = C::kScaleThreads, kRows = (BN + kScaleThreads - 1) / kScaleThreads;
             const int u = tid - 64;
             int st = 0, use = 0;
             uint32_t ph = 0;
@@ -660,8 +729,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        Walk one(lo, first, a.groups, p.n_tiles, BN, 1);
-        one.tile = blockIdx.x / (uint32_t)p.split;
+        Walk one(lo, first, p, BN, 1, blockIdx.x / (uint32_t)p.split);
         if (one.next()) {
             const int per = ((chunks + p.split - 1) / p.split + 3) & ~3, active = (chunks + per - 1) / per;
             const int mine = min(share, one.m - part_no * share);
@@ -712,6 +780,9 @@ cudaError_t run(const Device& dev, GemmParams& p, cudaStream_t stream) {
     const int64_t most = most_tiles(a, BN, (p.n_tiles + kCtas - 1) / kCtas);
     const int64_t room = dev.sms >= kCtas ? dev.sms / kCtas : 1, tiles = SPLIT || most < room ? most : room;
     const int cluster = SPLIT ? p.split : kCtas;
+    p.across = (p.n_tiles + kCtas - 1) / kCtas;
+    p.step_q = (int)(tiles / p.across);              // with SPLIT all the tiles there may be: a cluster has one
+    p.step_r = (int)(tiles % p.across);
     return launch_grid(grouped_gemm_kernel<FMT, BN, PAIR, SPLIT>, dim3((unsigned)(tiles * cluster)),
                        C::kThreads + (a.rows ? kGatherThreads : 0), C::kSmem, cluster, dev.id, p, stream);
 }
