@@ -141,6 +141,15 @@ struct Walk {
     __device__ void stop() { end = 0; }
 };
 
+// a0 += v0 f, a1 += v1 f, in one instruction (32768 rows, N = 4096, K = 6144 with
+// 1x128 scales: 775 us, 827 in two).
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float f) {
+    asm("{\n\t.reg .b64 a, v, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
+        "fma.rn.f32x2 a, v, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "r"(v0), "r"(v1), "f"(f));
+}
+
 __device__ uint32_t g_gave_up;     // launches in which a wait ran out of time
 
 template <int FMT, int BN, bool PAIR, bool SPLIT>
@@ -642,8 +651,8 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                             tc::tmem_load_wait(cur);
                             if (j < 7 && (j != 3 || two)) tc::tmem_load16(at + (j + 1) / 4 * kM + (j + 1) % 4 * 16, nxt);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                acc[j % 4 * 16 + i] = fmaf(__uint_as_float(cur[i]), j < 4 ? f0 : f1, acc[j % 4 * 16 + i]);
+                            for (int i = 0; i < 16; i += 2)
+                                fma2(acc[j % 4 * 16 + i], acc[j % 4 * 16 + i + 1], cur[i], cur[i + 1], j < 4 ? f0 : f1);
                         }
                     }
                     tc::fence_before();
