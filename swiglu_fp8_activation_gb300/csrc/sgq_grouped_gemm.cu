@@ -35,7 +35,7 @@
 // experts, N = K = 4096: 143 us, 7.7 TB/s), the tensor cores for large ones (32768
 // rows, N = 4096, K = 6144, in order: MXFP8 529 us, 3115 TFLOP/s, per-token 496; 8192
 // bf16 rows, N = K = 8192: 586 us, 1876 TFLOP/s), the epilogue's sums with 1x128
-// scales (827 us for those 32768 rows).
+// scales (711 us for those 32768 rows).
 //
 // Two accumulators in tensor memory let the epilogue of one tile run under
 // the products of the next. With 1x128 scales, which fp32 holds and no block
@@ -629,14 +629,19 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                 float acc[64];
 #pragma unroll
                 for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-                bool ready = false;
                 for (int kc = k_from; kc < k_to; kc += 2, ++use) {
                     const int buf = use & 1;
-                    if (!ready) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc_full + 8 * buf, (use >> 1) & 1, stop));
                     if (!ok) break;
                     tc::fence_after();
                     const uint32_t at = tmem + lanes + buf * C::kAccWidth + first;
-                    const bool next_ready = tc::bar_test(acc_full + 8 * (buf ^ 1), ((use + 1) >> 1) & 1);
+                    // the pair is free once the last of it is in registers, before that is summed
+                    // (arriving behind the sums: 135 us for 120, 16384 rows, N = 4096, K = 1536; 761 for 711, 32768 rows, K = 6144)
+                    auto release = [&]() {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
+                    };
                     if (busy) {
                         // 16 columns at a time, the next 16 on their way
                         uint32_t v[2][16];
@@ -649,16 +654,15 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
                             uint32_t(&nxt)[16] = v[(j & 1) ^ 1];
                             if (j == 4 && !two) break;
                             tc::tmem_load_wait(cur);
+                            if (j == (two ? 7 : 3)) release();
                             if (j < 7 && (j != 3 || two)) tc::tmem_load16(at + (j + 1) / 4 * kM + (j + 1) % 4 * 16, nxt);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2)
                                 fma2(acc[j % 4 * 16 + i], acc[j % 4 * 16 + i + 1], cur[i], cur[i + 1], j < 4 ? f0 : f1);
                         }
+                    } else {
+                        release();
                     }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::bar_arrive(acc_empty + 8 * buf);
-                    ready = kc + 2 < k_to && __all_sync(0xFFFFFFFFu, next_ready);
                 }
                 if (!ok) break;
                 if (SPLIT) {
