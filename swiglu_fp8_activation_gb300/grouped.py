@@ -6,7 +6,8 @@ requests beside a shared projection.
 Argument marshalling only, as in `binding`: checks, output allocation, the
 call. Every tensor of a call has to be on one CUDA device; the call runs on
 that device and on `stream` (default: its current stream), and what it
-allocates belongs to that stream.
+allocates belongs to that stream. Like the rest of the library these are for
+inference: autograd records none of them, lora_add's update of y included.
 """
 from __future__ import annotations
 
