@@ -83,6 +83,26 @@ def test_group_rows_skewed(T, k, what):
         assert torch.equal(a.cpu(), b)
 
 
+@pytest.mark.parametrize("n", [8192, 8193, 16384, 16385, 262144, 262145])
+@pytest.mark.parametrize("G", [40, 200, 1000])
+def test_group_rows_at_the_steps_of_its_plan(n, G):
+    """Where the number of CTAs changes, and where a lane's ids no longer stay in registers; replayed from a graph."""
+    ids = torch.randint(-1, G, (n,), generator=ref.gen(n + G)).to(torch.int32)
+    order = torch.argsort(torch.where(ids < 0, G, ids), stable=True)
+    kept = int((ids >= 0).sum())
+    rows = torch.where(torch.arange(n) < kept, order, -1).to(torch.int32)
+    slots = torch.empty(n, dtype=torch.int32)
+    slots[order] = torch.where(torch.arange(n) < kept, torch.arange(n), -1).to(torch.int32)
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), torch.bincount(ids[ids >= 0], minlength=G).cumsum(0)]).to(torch.int32)
+    dids = ids.to(DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, r, s = sgq.group_rows(dids, G)
+    graph.replay()
+    for got, want in ((o, offsets), (r, rows), (s, slots)):
+        assert torch.equal(got.cpu(), want)
+
+
 def test_group_rows_of_a_vector():
     ids = torch.tensor([2, -1, 0, 2], dtype=torch.int64, device=DEV)
     o, r, s = sgq.group_rows(ids, 3)
