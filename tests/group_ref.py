@@ -167,3 +167,47 @@ def check(got, ref, tol, what=""):
         at = bad.nonzero()[0].tolist()
         i = tuple(at)
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {at}: {got[i]} for {ref[i]} (may be {tol[i]} off)")
+
+
+# ------------------------------------------------------------------ precision of long sums
+#
+# The bound above grows with K for each element and cannot tell fp32 sums from
+# sums kept in 11 bits once K is some thousands. Over many elements the sums
+# can be told apart by how often the one rounding at the end goes the other
+# way: a value whose error before it is d crosses a boundary, one of which lies
+# in every step of the type, with probability |d| / step.
+#
+# d of fp32 sums: M = sqrt(sum of terms^2) is the size of the running sum of K
+# terms of random sign. Each product loses at most a unit of 2^-23 M, with a
+# random sign, together sqrt(K / 3) 2^-23 M; the accumulator, cut once an
+# instruction of 16 products at least, loses half a unit each time in one
+# direction, K / 16 2^-24 times the mean 2/3 M. Up to K = 8192 these are 2^-17.3
+# and 2^-15.6 of M; 4 sqrt(K) 2^-23 M, 2^-14.5 there, is more than twice both.
+
+def step(value, dtype):
+    """The distance of `dtype`'s values at `value` (64 bits)."""
+    f = torch.finfo(dtype)
+    return f.eps * torch.exp2(torch.floor(torch.log2(value.abs().clamp(min=f.tiny))))
+
+
+def spread(fmt, x, xs, w, ws, offsets, rows, S):
+    """sqrt of the sum of the squared terms of every result of grouped_gemm; rows inside x."""
+    G, N, K = w.shape
+    out = torch.zeros(S, N, dtype=torch.float64)
+    xv = values(fmt, x, xs)
+    for g, (a, b) in enumerate(ranges(offsets, S)):
+        if a < b:
+            xr = xv[torch.arange(a, b) if rows is None else rows[a:b].long()]
+            out[a:b] = ((xr ** 2) @ (values(fmt, w[g], None if ws is None else ws[g], N) ** 2).T).sqrt()
+    return out
+
+
+def misrounded(got, res):
+    """The share of `got` that is not the 64-bit result rounded to its type."""
+    return float((got != res.to(got.dtype)).double().mean())
+
+
+def misrounded_limit(res, size, K, dtype):
+    """What fp32 sums leave of it: the mean chance, and four standard deviations of a count of as many."""
+    p = (4 * K ** 0.5 * 2.0 ** -23 * size / step(res, dtype)).clamp(max=1).mean()
+    return float(p + 4 * (p / res.numel()).sqrt() + 1 / res.numel())
