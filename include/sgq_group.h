@@ -146,6 +146,10 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
  *   v       = x[t] . a[g]^T                                  (fp32, not rounded)
  *   y[t]    = y[t] + scaling[g] * (v . b[g]^T)               (fp32, rounded once)
  *
+ * (v is multiplied in 16-bit parts that together hold its 24 bits; with fp16
+ * rows and a workspace, the last of them may lack up to 2^-39 of the row's
+ * largest |v|.)
+ *
  * Rows of y that belong to no slot are left as they are. rows must come with
  * slots (both from group_rows with k = 1): a slot s whose token t does not
  * hold slots[t] = s, or whose t is outside [0, T), is passed over, so no row

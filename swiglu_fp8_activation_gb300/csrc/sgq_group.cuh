@@ -72,8 +72,8 @@ bool encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* d
 // `tiles` pieces of 512 bytes, one below the other, box one piece, no swizzle.
 bool encode_tiles512(CUtensorMap* m, const void* base, int64_t tiles);
 
-// Bytes of a row of lora_add's workspace: two parts of R 16-bit values, then
-// the row's factor (fp32) and 12 bytes of zeros.
+// Bytes of a row of lora_add's workspace: R values of v, then the row's
+// factor (fp16 rows), all fp32, and 12 bytes over.
 __host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }
 
 // Whether lora_add runs its form for few slots an adapter (one launch, no

@@ -13,14 +13,17 @@
 //   expand   y += c (v . b^T), tiles of 128 slots x 128 columns. Bound
 //            by reading and writing y.
 //
-// 8192 rows of 8 adapters, rank 64, K = 4096, N = 8192: 73 us, 20 and 53 (347 MB,
-// 51 us at the copy bandwidth).
+// 8192 rows of 8 adapters, rank 64, K = 4096, N = 8192: 77 us, 20 and 57 (347 MB,
+// 51 us at the copy bandwidth); rank 128: 97 us.
 //
-// v is kept to about 16 bits and more between them: a row of the workspace
-// holds v as two 16-bit parts, hi = round(v) and lo = round(v - hi), and the
-// expand product runs over both, so that rounding v costs 2^-17 of it and not
-// 2^-9. fp16 rows are first scaled by a power of two to below 2 (the row's
-// factor stands behind them), so that no v leaves the type's range.
+// v is fp32 between them, in rows of the workspace. The tensor cores multiply
+// 16-bit values, so expand splits each v into three, h = round(v), m = round(v -
+// h) and l = round(v - h - m), and its product runs over all of them: three
+// parts of 8 bits and a sign each hold the 24 bits of v, three of 11 more than
+// them. (Two parts of bf16 lose up to 2^-18 of v; made by shrink, they took 73.5 us.)
+// fp16 rows are scaled by a power of two first, so that their largest |v| lies in
+// [2^14, 2^15): what is left behind l is then at most 2^-39 of it, nothing for the |v|
+// from 2^-16 of it up. The row's factor stands behind it.
 #include "sgq_group.cuh"
 #include "sgq_ragged.cuh"
 #include "sgq_tc.cuh"
@@ -34,7 +37,9 @@ constexpr int kMaxStages = 8;
 constexpr int kShrinkThreads = 256;  // warp 0 copies of a, 1 products, 4-7 rows of x, then the result
 constexpr int kGather = 128;
 constexpr int kLoaders = 128;
-constexpr int kExpandThreads = 288 + kLoaders;   // warps 0-7 the sums, 8 copies and products, 9-12 loads of y
+constexpr int kSplitters = 256;
+constexpr int kExpandThreads = 288 + kLoaders + kSplitters;   // warps 0-7 the sums, 8 copies and products, 9-12 loads of y, 13-20 v
+constexpr int kParts = 3;            // 16-bit parts of v
 
 __device__ uint32_t g_gave_up;       // launches in which a wait ran out of time
 
@@ -46,7 +51,6 @@ struct alignas(128) ShrinkParams {
 
 struct alignas(128) ExpandParams {
     CUtensorMap mb;                  // b as bytes [groups][N][R], box 128 x 128 rows
-    CUtensorMap mv;                  // workspace rows, box 128 x 128 rows
     LoraArgs l;
     int n_tiles;
 };
@@ -282,8 +286,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
                     const float4 f = sum4(tid, r);
                     top = fmaxf(top, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
                 }
-                // 2^e with top / 2^e in [1, 2), e held to where both powers are normal
-                const int e = min(max((int)(__float_as_uint(top) >> 23), 27), 227);
+                // 2^e with top / 2^e in [2^14, 2^15), e held to where both powers are normal
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 14, 27), 227);
                 factors[tid] = __uint_as_float((uint32_t)e << 23);
             }
             __syncthreads();
@@ -291,24 +295,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_kernel(const __
         const int pieces = R / 8;
         for (int i = tid; i < mine * pieces; i += kShrinkThreads) {
             const int c = i / pieces, r = (i - c * pieces) * 8;
-            const float factor = DT == DT_F16 ? factors[c] : 1.0f;
-            const float down = DT == DT_F16 ? __uint_as_float((254u << 23) - __float_as_uint(factor)) : 1.0f;   // 1 / factor
             uint8_t* row = static_cast<uint8_t*>(l.v) + (int64_t)(s0 + rank * share + c) * lora_row_bytes(R);
-            uint32_t hi[4], low[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 f = sum4(c, r + 4 * h);
-                const float v[4] = {f.x * down, f.y * down, f.z * down, f.w * down};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float a0 = round_io<DT>(v[2 * j]), a1 = round_io<DT>(v[2 * j + 1]);
-                    hi[2 * h + j] = pack2<DT>(a0, a1);
-                    low[2 * h + j] = pack2<DT>(v[2 * j] - a0, v[2 * j + 1] - a1);
-                }
-            }
-            *reinterpret_cast<uint4*>(row + 2 * r) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(row + 2 * R + 2 * r) = make_uint4(low[0], low[1], low[2], low[3]);
-            if (r == 0) *reinterpret_cast<float4*>(row + 4 * R) = make_float4(factor, 0.0f, 0.0f, 0.0f);
+            *reinterpret_cast<float4*>(row + 4 * r) = sum4(c, r);
+            *reinterpret_cast<float4*>(row + 4 * r + 16) = sum4(c, r + 4);
+            if (DT == DT_F16 && r == 0) *reinterpret_cast<float*>(row + 4 * R) = factors[c];
         }
     }
     tc::fence_before();
@@ -326,11 +316,13 @@ struct ExpandCfg {
     static constexpr int kNT = 128, kPitch = 2 * kNT + 16;
     static constexpr int kB = kNT * kChunk, kV = kM * kChunk, kY = kM * kPitch;
     static constexpr int kBufs = VC == 1 ? 2 : 1;                    // of b: the next tile's under this one's
-    static constexpr int kYBufs = VC == 1 ? 4 : 3;                   // of y: loads two or three tiles ahead
-    static constexpr int kYAt = kBufs * VC * kB + 2 * VC * kV;
+    static constexpr int kYBufs = VC == 1 ? 4 : 2;                   // of y: loads one or three tiles ahead
+    static constexpr int kVAt = kBufs * VC * kB;                     // [kParts][VC]
+    static constexpr int kYAt = kVAt + kParts * VC * kV;
     static constexpr int kTokensAt = kYAt + kYBufs * kY;
     static constexpr int kTablesAt = kTokensAt + kYBufs * 4 * kM;
-    static int smem(int groups) { return 1024 + kTablesAt + 2 * 4 * table_ints(groups) + 256; }
+    static int smem(int groups) { return kTablesAt + 2 * 4 * table_ints(groups) + 256; }
+    static_assert(kTablesAt + 2 * 4 * table_ints(kMaxGroups) + 256 <= kMaxDynamicSmem, "tile too large");
 };
 
 // The tiles of one CTA: a piece of their list, in which the columns' tiles of
@@ -365,18 +357,17 @@ template <int DT, int VC>
 __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __grid_constant__ ExpandParams p) {
     using C = ExpandCfg<VC>;
     constexpr int NT = C::kNT;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];        // the swizzle counts in pieces of 1024
     const LoraArgs& l = p.l;
     int* tokens = reinterpret_cast<int*>(smem + C::kTokensAt);           // [kYBufs][128]
     int* lo = reinterpret_cast<int*>(smem + C::kTablesAt);
     int* first = lo + table_ints(l.groups);
     uint64_t* bars = reinterpret_cast<uint64_t*>(first + table_ints(l.groups));
-    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 15);
+    uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 16);
     int* part = reinterpret_cast<int*>(misc + 4);
     volatile uint32_t* stop = misc + 1;
     const uint32_t full_b = tc::smem_addr(bars), full_v = full_b + 16, acc = full_v + 8, acc_empty = acc + 16;
-    const uint32_t y_full = acc_empty + 16, y_empty = y_full + 32;
+    const uint32_t y_full = acc_empty + 16, y_empty = y_full + 32, v_empty = y_empty + 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), R = l.R;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -384,7 +375,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             tc::bar_init(acc + 8 * i, 1);
             tc::bar_init(acc_empty + 8 * i, 4);
         }
-        tc::bar_init(full_v, 1);
+        tc::bar_init(full_v, kSplitters / 32);
+        tc::bar_init(v_empty, 1);
         for (int i = 0; i < C::kYBufs; ++i) {
             tc::bar_init(y_full + 8 * i, kLoaders + kLoaders / 32);
             tc::bar_init(y_empty + 8 * i, 4);
@@ -392,7 +384,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         tc::fence_barrier_init();
         *stop = 0;
         tc::prefetch_map(&p.mb);
-        tc::prefetch_map(&p.mv);
     }
     // The shrink launch before this one lets it start after it has waited for
     // everything before itself, and writes the workspace alone: all but the
@@ -404,7 +395,69 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
     tc::fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, misc[0], 0);
     ExpandWalk walk(lo, first, l.groups, p.n_tiles, NT);
-    if (warp > 8) {
+    if (warp >= 9 + kLoaders / 32) {
+        // ------------------------------------- v: fp32 rows -> three 16-bit parts
+        // thread u takes pieces u, u + 256, ... of 8 values of the tile's rows; an odd
+        // last piece is filled up with zeros (a product takes 16 values). Eight warps,
+        // so that at rank 64 all of it is read before the parts are free (four: 78.4 us
+        // for 77.1, 8192 rows of 8 adapters, K = 4096, N = 8192; rank 128 100 for 97).
+        const int u = tid - 288 - kLoaders, pieces = (R / 8 + 1) & ~1, all = kM * pieces;
+        bool ok = true;
+        uint32_t vs = 0;                                                 // sets of slots so far
+        pdl_wait();
+        pdl_trigger();
+        while (ok && walk.next()) {
+            if (!walk.fresh) continue;
+            bool free = vs == 0;
+            for (int j0 = 0; j0 < all; j0 += 4 * kSplitters) {
+                float v[4][8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int j = j0 + q * kSplitters + u, c = j / pieces, r = (j - c * pieces) * 8;
+                    const bool in = j < all && c < walk.m && r < R;
+                    const uint8_t* row = static_cast<const uint8_t*>(l.v) + (int64_t)(walk.s0 + (in ? c : 0)) * lora_row_bytes(R);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 f = in ? __ldcg(reinterpret_cast<const float4*>(row + 4 * r) + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        v[q][4 * h] = f.x, v[q][4 * h + 1] = f.y, v[q][4 * h + 2] = f.z, v[q][4 * h + 3] = f.w;
+                    }
+                    if (DT == DT_F16) {
+                        const float factor = in ? __ldcg(reinterpret_cast<const float*>(row + 4 * R)) : 1.0f;
+                        const float down = __uint_as_float((254u << 23) - __float_as_uint(factor));       // 1 / factor
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[q][k] *= down;
+                    }
+                }
+                if (!free) {         // the products are done with the parts of the set before
+                    ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(v_empty, (vs - 1) & 1, stop));
+                    if (!ok) break;
+                    free = true;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int j = j0 + q * kSplitters + u, c = j / pieces, piece = j - c * pieces;
+                    if (j >= all) break;
+                    uint8_t* to = smem + C::kVAt + (piece >> 3) * C::kV + c * kChunk + (((piece ^ c) & 7) << 4);
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const float a0 = round_io<DT>(v[q][k]), a1 = round_io<DT>(v[q][k + 1]);
+                            o[k / 2] = pack2<DT>(a0, a1);
+                            v[q][k] -= a0;
+                            v[q][k + 1] -= a1;
+                        }
+                        *reinterpret_cast<uint4*>(to + h * VC * C::kV) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (ok && lane == 0) tc::bar_arrive(full_v);
+            ++vs;
+        }
+    } else if (warp > 8) {
         // ------------------------------------------------------- loads of y
         const int u = tid - 288, piece = u & 15;
         bool ok = true;
@@ -430,8 +483,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         pdl_wait();
         pdl_trigger();
     } else if (warp == 8) {
-        // ------------------------------------------ copies of b and v, products
-        const uint32_t at = tc::smem_addr(smem), v_at = at + C::kBufs * VC * C::kB;
+        // ------------------------------------------------ copies of b, products
+        const uint32_t at = tc::smem_addr(smem), v_at = at + C::kVAt;
         auto load_b = [&](const ExpandWalk& w, uint32_t i) {             // tile i's rows of b into buffer i % kBufs
             if (tc::elect()) {
                 const uint32_t bar = full_b + 8 * (i % C::kBufs), to = at + (i % C::kBufs) * VC * C::kB;
@@ -447,21 +500,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
         pdl_wait();
         pdl_trigger();
         bool ok = true;
-        uint32_t vs = 0;                                                 // loads of v so far
+        uint32_t vs = 0;                                                 // sets of slots so far
         for (uint32_t i = 0; ok && walk.next(); ++i) {
             const uint32_t buf = i & 1;
-            // the product before is done with v and with the other buffer of b
+            // the product before is done with the other buffer of b
             if (i > 0) ok = __all_sync(0xFFFFFFFFu, tc::bar_wait(acc + 8 * (buf ^ 1), ((i - 1) >> 1) & 1, stop));
             if (!ok) break;
             if (walk.fresh) {
-                if (tc::elect()) {
-                    tc::bar_arrive_expect(full_v, 2 * VC * C::kV);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int c = 0; c < VC; ++c)
-                            tc::load_2d(v_at + (h * VC + c) * C::kV, &p.mv, full_v, h * 2 * R + c * kChunk, walk.s0);
-                }
+                if (i > 0 && tc::elect()) tc::bar_arrive(v_empty);       // and with the other slots' v
                 __syncwarp();
                 ++vs;
             }
@@ -479,8 +525,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
             if (!ok) {
                 // gave up: wait (a while) for the copies in flight
                 uint32_t never = 0;
-                tc::bar_wait(full_v, (vs - 1) & 1, &never, 1 << 27);
-                never = 0;
                 tc::bar_wait(full_b + 8 * (i % C::kBufs), (i / C::kBufs) & 1, &never, 1 << 27);
                 never = 0;
                 if (more) tc::bar_wait(full_b + 8 * ((i + 1) % C::kBufs), ((i + 1) / C::kBufs) & 1, &never, 1 << 27);
@@ -491,7 +535,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
                 const uint32_t idesc = idesc_f16(DT, NT), b_at = at + (i % C::kBufs) * VC * C::kB;
                 const int steps = (R + 15) / 16;                         // of 16 values
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < kParts; ++h)
 #pragma unroll
                     for (int k = 0; k < 4 * VC; ++k) {
                         if (k >= steps) break;
@@ -708,8 +752,7 @@ cudaError_t expand(const Device& dev, ExpandParams& p, int64_t tiles, cudaStream
     using C = ExpandCfg<VC>;
     const LoraArgs& l = p.l;
     const cuuint64_t bd[3] = {(cuuint64_t)(2 * l.R), (cuuint64_t)l.N, (cuuint64_t)l.groups};
-    const cuuint64_t vd[2] = {(cuuint64_t)lora_row_bytes(l.R), (cuuint64_t)l.S};
-    if (!encode_rows(&p.mb, l.b, 3, bd, C::kNT) || !encode_rows(&p.mv, l.v, 2, vd, kM)) return cudaErrorInvalidValue;
+    if (!encode_rows(&p.mb, l.b, 3, bd, C::kNT)) return cudaErrorInvalidValue;
     p.n_tiles = (l.N + C::kNT - 1) / C::kNT;
     const int64_t most = tiles * p.n_tiles, room = dev.sms > 0 ? dev.sms : 1;
     return launch_grid(lora_expand_kernel<DT, VC>, dim3((unsigned)(most < room ? most : room)), kExpandThreads,

@@ -211,3 +211,33 @@ def misrounded_limit(res, size, K, dtype):
     """What fp32 sums leave of it: the mean chance, and four standard deviations of a count of as many."""
     p = (4 * K ** 0.5 * 2.0 ** -23 * size / step(res, dtype)).clamp(max=1).mean()
     return float(p + 4 * (p / res.numel()).sqrt() + 1 / res.numel())
+
+
+# ------------------------------------------------------------------ adapters whose v takes all of fp32
+
+def exact_lora(T, R, N, K, dtype, seed):
+    """x, a, b of one adapter for which every v takes 23 bits and every sum on
+    the way is exact in fp32, and the 64-bit result (of y = 0): v of a pair of
+    ranks differ in their last bits alone, and b takes the difference.
+
+    x holds three digits of 7 bits, 2^8 apart, so that v = d0 + 2^-8 e1 d1 +
+    2^-16 e2 d2 with e of 0 and 1 from a; all terms are multiples of 2^-16 and
+    all sums below 2^7. The last two ranks have the largest |v|, 2^12 times the
+    others', and nothing of it reaches y."""
+    r = gen(seed)
+    x = torch.zeros(T, K, dtype=torch.float64)
+    at = torch.randperm(K, generator=r)[:3]
+    x[:, at[0]] = torch.randint(64, 96, (T,), generator=r).double()
+    x[:, at[1]] = torch.randint(64, 128, (T,), generator=r).double() * 2.0 ** -8
+    x[:, at[2]] = (2 * torch.randint(32, 64, (T,), generator=r) + 1).double() * 2.0 ** -16
+    a = torch.zeros(R, K, dtype=torch.float64)
+    a[:, at[0]] = 1
+    a[:, at[1]] = torch.randint(0, 2, (R // 2,), generator=r).double().repeat_interleave(2)
+    a[0::2, at[2]] = 1                                   # of a pair, the second lacks the last digit
+    a[-2:] *= 2.0 ** 12
+    sign = torch.randint(-1, 2, (N, R // 2), generator=r).double()
+    sign[:, -1] = 0
+    b = torch.stack([sign, -sign], -1).view(N, R)
+    res = (x @ a.T) @ b.T
+    x, a, b = (t.to(dtype) for t in (x, a[None], b[None]))
+    return x, a, b, res

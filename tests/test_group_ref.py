@@ -1,5 +1,5 @@
 """The checks of the ragged-group operators' precision (group_ref.py) on the
-CPU: results whose sums are kept in too few bits fail them."""
+CPU: results whose sums or factors are kept in too few bits fail them."""
 import pytest
 import torch
 
@@ -33,3 +33,19 @@ def test_sums_in_few_bits_are_found(fmt, K):
     # eight parts of K, each rounded to 16 bits before they are added
     parts = [held(p, 11) for p in ((xv[:, i * K // 8:(i + 1) * K // 8] @ wv[:, i * K // 8:(i + 1) * K // 8].T) for i in range(8))]
     assert ref.misrounded(sum(parts).to(torch.bfloat16), res) > limit
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R", [8, 24, 64, 72, 128])
+def test_factors_in_few_bits_are_found(R, dtype):
+    x, a, b, res = ref.exact_lora(20, R, 136, 64, dtype, R)
+    xv, av, bv = x.double(), a[0].double(), b[0].double()
+    v = xv @ av.T
+    assert torch.equal(v @ bv.T, res) and torch.equal(v, v.float().double())
+    assert float(v[:, :-2].abs().max()) < 128 and float(res.abs().max()) > 0
+    want = res.to(dtype)
+    digits = torch.finfo(dtype).bits - (8 if dtype == torch.bfloat16 else 5)      # significant bits of the type
+    one = held(v, digits)
+    two = one + held(v - one, digits)
+    for few in (one, two) if dtype == torch.bfloat16 else (one,):
+        assert float(((few @ bv.T).to(dtype) != want).double().mean()) > 0.2
