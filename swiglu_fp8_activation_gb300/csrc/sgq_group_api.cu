@@ -168,7 +168,10 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
 int sgq_wait_timeouts(uint32_t* count) {
     if (!count) return SGQ_ERR_INVALID_ARG;
     uint32_t gemm = 0, lora = 0;
-    cudaError_t e = gemm_gave_up(&gemm);
+    // the copies of the counts wait for the default stream alone, which streams
+    // made not to block it do not wait for either
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = gemm_gave_up(&gemm);
     if (e == cudaSuccess) e = lora_gave_up(&lora);
     if (e == cudaSuccess) *count = gemm + lora;
     return launched(e);
