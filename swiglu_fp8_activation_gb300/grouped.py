@@ -277,7 +277,7 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
         _need(slots, (T, 1) if slots.dim() == 2 else (T,), torch.int32, "slots")
     if scaling is not None:
         _need(scaling, (groups,), torch.float32, "scaling")
-    room = 0 if S * R <= 128 * groups else S * (4 * R + 16)      # lora_workspace_bytes(S, groups, R)
+    room = _lib().sgq_lora_workspace_bytes(S, groups, R)
     if workspace is not None:
         _need(workspace, (room,), torch.uint8, "workspace")
     at = _here(stream, "lora_add", x, a, b, y, offsets, rows, slots, scaling, workspace)
