@@ -153,8 +153,9 @@ int combine_rows(uint32_t flags, int64_t T, int64_t k, int64_t S, int64_t N, con
  * Rows of y that belong to no slot are left as they are. rows must come with
  * slots (both from group_rows with k = 1): a slot s whose token t does not
  * hold slots[t] = s, or whose t is outside [0, T), is passed over, so no row
- * of y is updated twice whatever rows holds. One launch on the stream where the
- * slots are few for the adapters (no workspace), two else.
+ * of y is updated twice whatever rows holds. One launch on the stream, without a
+ * workspace, where the slots are few for the adapters (S up to 512, S * R up to
+ * 8192 and 128 * groups), two else: the two add in different orders.
  *
  * Arguments:
  *   flags         SGQ_F_FP16: x, a, b and y are fp16, not bf16 (others rejected)

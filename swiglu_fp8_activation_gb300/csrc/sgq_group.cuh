@@ -80,7 +80,16 @@ __host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }
 // workspace): slots an adapter (on average) x rank up to 128. K = N = 4096, this
 // form and the tensor cores' in a graph: rank 16, 2 slots an adapter 9.6 and 21.6
 // us, 8 slots 13.5 and 22.8, 16 slots 25.9 and 20.7; rank 64, 4 slots 19.3 and 14.8.
-constexpr bool lora_few(int64_t S, int64_t groups, int64_t R) { return S * R <= 128 * groups; }
+// The host does not know how many adapters are in use, and where it is one or a few
+// of many the slots are not few: up to 512 slots, and 8192 slots x rank, the worse
+// of the two mistakes is the smaller one. 1024 adapters, one in use and all: rank 16,
+// 256 slots 21.7 and 30.9 us, 40.6 and 94.4; 512 slots 41.6 and 30.9, 82.5 and 167; 1024
+// slots 79.5 and 32.3, 147 and 244; 8192 slots 499 and 59.6, 545 and 384. Rank 64, 128 slots
+// 41.1 and 34.0, 64.2 and 67.8; 256 slots 46.8 and 33.9, 112 and 125; 512 slots 87.2 and
+// 34.0, 186 and 199.
+constexpr bool lora_few(int64_t S, int64_t groups, int64_t R) {
+    return S <= 512 && S * R <= (groups < 64 ? 128 * groups : 8192);
+}
 
 cudaError_t launch_group_rows(const Device& dev, const GroupRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_grouped_gemm(int fmt, int dt, const Device& dev, const GroupGemmArgs& a, cudaStream_t stream);

@@ -248,3 +248,14 @@ def test_plain_swizzle_matches_the_oracle():
     import oracle
     codes = torch.randint(0, 255, (1, 200, 7), generator=ref.gen(1)).to(torch.uint8)
     np.testing.assert_array_equal(ref.swizzled(codes)[0].numpy(), oracle.scale_layout("mxfp8", codes[0].numpy(), "swizzled"))
+
+
+def test_lora_form_is_bounded_in_slots():
+    """However many adapters are loaded, many slots take the tensor cores' form, with its workspace."""
+    room = lambda S, R: S * (4 * R + 16)  # noqa: E731
+    for R, most in ((8, 512), (16, 512), (24, 341), (64, 128), (128, 64)):
+        assert sgq.lora_workspace_bytes(most, 1024, R) == 0
+        assert sgq.lora_workspace_bytes(most + 1, 1024, R) == room(most + 1, R)
+        assert sgq.lora_workspace_bytes(8192, 1024, R) == room(8192, R)
+    assert sgq.lora_workspace_bytes(512, 64, 16) == 0
+    assert sgq.lora_workspace_bytes(512, 63, 16) == room(512, 16)
