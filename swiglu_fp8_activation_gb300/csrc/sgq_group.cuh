@@ -78,8 +78,9 @@ __host__ __device__ constexpr int lora_row_bytes(int R) { return 4 * R + 16; }
 
 // Whether lora_add runs its form for few slots an adapter (one launch, no
 // workspace): slots an adapter (on average) x rank up to 128. K = N = 4096, this
-// form and the tensor cores' in a graph: rank 16, 2 slots an adapter 9.6 and 21.6
-// us, 8 slots 13.5 and 22.8, 16 slots 25.9 and 20.7; rank 64, 4 slots 19.3 and 14.8.
+// form and the tensor cores' in a graph: rank 16, 2 slots an adapter 8.0 and 21.8
+// us, 8 slots 13.9 and 21.8, 16 slots 25.9 and 21.8; rank 64, 2 slots 20.6 and 25.9, 4 slots
+// 28.9 and 25.9 (32 adapters, the same number of slots each).
 // The host does not know how many adapters are in use, and where it is one or a few
 // of many the slots are not few: up to 512 slots, and 8192 slots x rank, the worse
 // of the two mistakes is the smaller one. 1024 adapters, one in use and all: rank 16,

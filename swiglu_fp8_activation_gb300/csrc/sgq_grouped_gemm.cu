@@ -31,8 +31,8 @@
 // a cluster share the K of one and sum the parts through distributed shared
 // memory. pick() below has the rule, with both sides measured.
 //
-// What bounds it: the weights' bytes for small groups (64 x 8 MXFP8 rows of 64
-// experts, N = K = 4096: 143 us, 7.7 TB/s), the tensor cores for large ones (32768
+// What bounds it: the weights' bytes for small groups (64 x 8 MXFP8 rows, 54 of 64
+// experts in use, N = K = 4096: 935 MB in 143 us, 6.5 TB/s), the tensor cores for large ones (32768
 // rows, N = 4096, K = 6144, in order: MXFP8 529 us, 3115 TFLOP/s, per-token 496; 8192
 // bf16 rows, N = K = 8192: 586 us, 1876 TFLOP/s), the epilogue's sums with 1x128
 // scales (711 us for those 32768 rows).
@@ -142,7 +142,7 @@ struct Walk {
 };
 
 // a0 += v0 f, a1 += v1 f, in one instruction (32768 rows, N = 4096, K = 6144 with
-// 1x128 scales: 775 us, 827 in two).
+// 1x128 scales: 761 us, 827 in two).
 __device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t v1, float f) {
     asm("{\n\t.reg .b64 a, v, f;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
         "fma.rn.f32x2 a, v, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, SPLIT>::kThreads + kGatherT
         // and warp 3 for the odd ones: the issuing thread is held while its
         // products run, and what it does between (three waits, the votes, the
         // descriptors) runs under the other's products (32768 rows, N = 4096, K =
-        // 6144: 972 us with warp 1 alone, 833 with both).
+        // 6144: 972 us with warp 1 alone and a division a tile, 827 with both and none).
         const int mine = warp >> 1;
         const uint64_t base = tc::desc_sw128(tiles_at);
         const uint32_t idesc = (1u << 4) | ((kM >> 3) << 17) | ((kM >> 4) << 24);

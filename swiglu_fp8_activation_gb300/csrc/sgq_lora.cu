@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const __
 // once for all slots), then, v having gone round through distributed shared
 // memory, an eighth of the columns of y. As two launches with v in the
 // workspace, 64 rows of 32 adapters (rank 16, K = N = 4096) took 8.0 us in a
-// graph, against 9.6, but 19.8 as a call from Python, against 14.
+// graph, against 9.4, but 19.8 as a call from Python, against 9.9.
 
 constexpr int kFew = 8;              // slots a tile
 constexpr int kFewCtas = 8;          // of a cluster

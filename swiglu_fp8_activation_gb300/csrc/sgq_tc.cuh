@@ -11,11 +11,10 @@ namespace tc {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// One lane of a converged warp. The tensor-core, commit and bulk-copy
-// instructions take warp-uniform operands: under this choice of a lane, in
-// control flow that the whole warp runs, the compiler keeps them in uniform
-// registers. Under `lane == 0` it built a loop around each of them (104 cycles
-// an instruction; a chunk of four products cost 740 cycles whatever its size).
+// One lane of a converged warp, for the tensor-core, commit and bulk-copy
+// instructions, in control flow that the whole warp runs. Measured against
+// `lane == 0`, under which each of them took 104 cycles and a chunk of four
+// products 740 whatever its size: grouped_gemm 1107 us for 699.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
