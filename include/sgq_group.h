@@ -31,9 +31,18 @@
  * synchronisation, CUDA-graph capture allowed, programmatic dependent launch
  * (every kernel here waits for the kernel before it before it reads or
  * writes any tensor). Outputs may not overlap inputs or each other except
- * where stated. Every result is the same on every run: no float atomics.
+ * where stated. Every result is the same on every run: no float atomics. (The
+ * order of grouped_gemm's and lora_add's sums follows the call's sizes and the
+ * count of multiprocessors, which sgq_set_sm_budget replaces; so may its last bit.)
  * Non-finite FP8 codes, scales or 16-bit values give non-finite or
  * unspecified results in the rows that they enter, and in no others.
+ *
+ * State kept between calls, beside sgq.h's: for group_rows, whether the device
+ * runs clusters of 16 CTAs; and a count that sgq_wait_timeouts returns. Every
+ * wait inside grouped_gemm and lora_add is limited to some seconds. A launch in
+ * which one runs out (the device made no progress, or was held by others for that
+ * long) ends and leaves its outputs unspecified; its call has returned SGQ_OK
+ * by then, and sgq_wait_timeouts is where it shows.
  */
 #ifndef SGQ_GROUP_H
 #define SGQ_GROUP_H
@@ -82,8 +91,14 @@ int group_rows(int id_bytes, int64_t T, int64_t k, int64_t groups, const void* i
  *   per-token  out[s][n] = xs[r] * ws[g][n] * sum_k x[r][k] w[g][n][k]
  *   16-bit     out[s][n] = sum_k x[r][k] w[g][n][k]
  *
- * summed in fp32 and rounded once. A row index outside [0, x_rows) stands for
+ * summed in fp32 and rounded once. The scales enter in fp32: MXFP8's with every
+ * term, exactly; 1x128's as xs * ws; per-token's one after the other, xs first. What leaves
+ * fp32's range on the way is 0 or infinite (or NaN: the sum of both infinities).
+ * A row index outside [0, x_rows) stands for
  * a row of zeros. Slots of no group keep what out held.
+ *
+ * The width of the tiles is chosen for S / groups slots a group, those of no
+ * group among them, and has no influence on which slots are computed.
  *
  * Arguments:
  *   fmt           sgq_format_t or SGQ_FMT_16BIT
@@ -185,9 +200,8 @@ int64_t sgq_lora_workspace_bytes(int64_t S, int64_t groups, int64_t R);
 
 /*
  * Launches of grouped_gemm and lora_add on the current device, since the
- * library was loaded, in which a wait inside the kernel ran out of time (some
- * seconds: the device was not making progress). Such a launch ends and leaves
- * its outputs unspecified. A diagnosis: it waits for the device, and may not be
+ * library was loaded, in which a wait inside the kernel ran out of time (see
+ * above). A diagnosis: it waits for the device, all streams of it, and may not be
  * called during graph capture. NULL returns SGQ_ERR_INVALID_ARG.
  */
 int sgq_wait_timeouts(uint32_t* count);

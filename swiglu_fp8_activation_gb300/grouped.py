@@ -159,7 +159,7 @@ def grouped_gemm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, fmt
     offsets [groups+1] int32; rows [S] int32 or None (slot s reads x[s], S = X).
     A row index outside x reads zeros. Returns out [S, N] (bfloat16, float16 by
     out_dtype or `out`, x's type with "none"); slots of no group keep what out
-    held.
+    held. Waits inside the kernel are limited: see wait_timeouts.
     """
     if fmt not in GEMM_FORMATS:
         raise SgqError(f"unknown format {fmt!r}")
@@ -233,7 +233,9 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
 
 def wait_timeouts() -> int:
     """Launches of grouped_gemm and lora_add on the current device in which a
-    wait inside the kernel ran out of time (waits for the device)."""
+    wait inside the kernel ran out of time (some seconds without progress). Such
+    a launch ends, its call having returned, and leaves its outputs unspecified:
+    this count is where it shows. Waits for the device; not during graph capture."""
     n = C.c_uint32(0)
     _check(_lib().sgq_wait_timeouts(C.byref(n)), "sgq_wait_timeouts")
     return n.value
@@ -257,7 +259,8 @@ def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, y: torch.Tensor,
     already are in adapter order (slot s is row s). scaling [groups] float32 or
     None (ones). workspace: uint8 [lora_workspace_bytes(S, groups, R)]
     or None (allocated where one is needed). Rows without an
-    adapter stay as they are. Returns y.
+    adapter stay as they are. Returns y. Waits inside the kernels are limited:
+    see wait_timeouts.
     """
     T, K = _dims(x, 2, "x")
     groups, R, _ = _dims(a, 3, "a")
