@@ -88,25 +88,29 @@ std::unordered_map<OccKey, int, OccHash> occ_seen;
 
 cudaError_t ctas_per_sm(const void* kernel, int device, int threads, int smem, int* out) {
     const OccKey key{kernel, device, threads, smem};
-    {
-        std::lock_guard<std::mutex> lock(occ_mu);
-        const auto it = occ_seen.find(key);
-        if (it != occ_seen.end()) {
-            *out = it->second;
-            return cudaSuccess;
+    try {
+        {
+            std::lock_guard<std::mutex> lock(occ_mu);
+            const auto it = occ_seen.find(key);
+            if (it != occ_seen.end()) {
+                *out = it->second;
+                return cudaSuccess;
+            }
         }
-    }
-    if (smem > 40 * 1024) {
-        const cudaError_t e = ensure_dynamic_smem(kernel, device, smem);
+        if (smem > 40 * 1024) {
+            const cudaError_t e = ensure_dynamic_smem(kernel, device, smem);
+            if (e != cudaSuccess) return e;
+        }
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, (size_t)smem);
         if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lock(occ_mu);
+        occ_seen[key] = n;
+        *out = n;
+        return cudaSuccess;
+    } catch (...) {                  // no exception leaves a C entry point
+        return cudaErrorMemoryAllocation;
     }
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, (size_t)smem);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(occ_mu);
-    occ_seen[key] = n;
-    *out = n;
-    return cudaSuccess;
 }
 
 cudaError_t ensure_dynamic_smem(const void* kernel, int device, int bytes) {
