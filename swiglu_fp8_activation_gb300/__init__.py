@@ -22,6 +22,10 @@ experts' matrix products, on rows of the three FP8 formats or 16-bit ones),
 `combine_rows` (each token's weighted sum) and `lora_add` (the low-rank
 adapters of many requests beside a shared projection).
 
+What stands between the projections of an attention layer: `rope` (rotary
+positions), `cache_write` and `cache_read` (rows of a paged key-value cache, 16-bit or
+FP8 with a scale a row) and `paged_attention` (one new token a sequence).
+
 Formats: MXFP8 (E4M3 + one E8M0 scale per 1x32 block), 1x128 block FP8 with
 fp32 scales, and per-token FP8 with an [M,1] fp32 scale.
 
@@ -38,4 +42,8 @@ from .binding import (  # noqa: F401
 from .grouped import (  # noqa: F401
     GEMM_FORMATS, MAX_GROUPS, MAX_RANK, combine_rows, gemm_scale_shapes, group_rows, grouped_gemm, lora_add,
     lora_workspace_bytes, wait_timeouts,
+)
+from .cache import (  # noqa: F401
+    CACHE_FORMATS, MAX_HEAD, MAX_HEADS, MAX_PAGE, MAX_SEQUENCES, ROPE_LAYOUTS, attention_workspace_bytes, cache_read, cache_write,
+    paged_attention, rope, rope_frequencies, rope_turns,
 )

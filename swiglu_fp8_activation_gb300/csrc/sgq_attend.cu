@@ -1,0 +1,12 @@
+// sgq_attend.cu -- the kernels of paged_attention by the cache's format and the
+// 16-bit type beside it, one translation unit each.
+#include "sgq_attend.cuh"
+
+namespace sgq {
+
+cudaError_t launch_attend(int fmt, int dt, const Device& dev, const AttendArgs& a, cudaStream_t stream) {
+    if (fmt == FMT_PT) return dt == DT_F16 ? attend::launch_fp8_f16(dev, a, stream) : attend::launch_fp8_bf16(dev, a, stream);
+    return dt == DT_F16 ? attend::launch_f16(dev, a, stream) : attend::launch_bf16(dev, a, stream);
+}
+
+}  // namespace sgq

@@ -1,0 +1,10 @@
+// sgq_attend_fp8_bf16.cu -- paged_attention's kernels for E4M3 rows beside bf16 queries.
+#include "sgq_attend.cuh"
+
+namespace sgq {
+
+cudaError_t attend::launch_fp8_bf16(const Device& dev, const AttendArgs& a, cudaStream_t stream) {
+    return launch_kind<FP8_BF16>(dev, a, stream);
+}
+
+}  // namespace sgq

@@ -1,0 +1,121 @@
+// sgq_cache.cuh -- arguments and host-side launchers of the paged cache's
+// kernels (rope, cache_write, cache_read, paged_attention).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sgq_group.cuh"
+
+namespace sgq {
+
+constexpr int kMaxHead = 256;
+constexpr int kMaxHeads = 1024;
+constexpr int kMaxPage = 65536;
+
+// n / d for 0 <= n < 2^31 by one multiplication: with 2^(s-1) < d <= 2^s and
+// m = floor(2^(31+s) / d) + 1, n m / 2^(31+s) lies above n / d by less than 1 / d.
+struct Div {
+    uint32_t m;
+    int s;
+    uint32_t d;
+};
+
+inline Div make_div(uint32_t d) {
+    int s = 0;
+    while ((uint64_t(1) << s) < d) ++s;
+    return {(uint32_t)((uint64_t(1) << (31 + s)) / d + 1), 31 + s, d};
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.m) >> d.s); }
+
+struct Heads {
+    uint16_t* p;
+    int64_t ts, hs;      // strides of tokens and heads, in elements
+    int n;
+};
+
+struct CacheArgs {
+    uint8_t* k;
+    uint8_t* v;
+    float* ks;           // null with 16-bit rows
+    float* vs;
+    int64_t pages;
+    int64_t ps, hs, ts;  // strides of pages, heads and tokens, in bytes
+    int heads;
+    int D;
+    Div page;            // tokens a page
+};
+
+struct RopeArgs {
+    const uint64_t* freqs;
+    const void* positions;
+    float factor;
+    int half;            // pairs, R / 2; 0 for no rotation
+    int wide;            // 64-bit positions
+    int inverse;
+};
+
+struct WriteArgs {
+    RopeArgs rope;
+    Heads q, qo, k, v;   // q.n heads are rotated, k.n rotated and written, v.n (equal to k.n) written
+    CacheArgs c;
+    const void* slots;
+    int wide;            // 64-bit slots
+    int64_t T;
+    int tpc;             // tokens a CTA
+    int D;
+};
+
+struct ReadArgs {
+    CacheArgs c;
+    const void* slots;
+    int wide;
+    int64_t S;
+    uint16_t* k;         // either may be null
+    uint16_t* v;
+};
+
+struct AttendArgs {
+    CacheArgs c;
+    Heads q;
+    const int32_t* table;
+    const int32_t* lengths;
+    const float* sinks;  // or null
+    uint16_t* out;
+    float* lse;          // or null
+    void* ws;
+    int64_t width;       // pages a sequence
+    float scale;
+    int window;          // 0 for none
+    int B;
+    int group;           // heads of q a head of the cache
+    int limit;           // width * page size: the longest sequence
+    int chunks;          // column chunks a head of the cache
+    int items;           // heads * chunks a sequence
+    int joined;          // whether a second launch joins what several CTAs have computed
+};
+
+// Most CTAs that one paged_attention runs, for which its workspace has room.
+constexpr int kAttendCtas = 512;
+constexpr int kAttendTile = 64;      // tokens a CTA takes at a time
+
+// Columns (heads of q) a CTA takes at once.
+constexpr int attend_columns(int group) { return group <= 8 ? 8 : 16; }
+constexpr int attend_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
+__host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }
+
+// The item that CTA c of paged_attention has begun and not ended, and the last CTA that
+// has some of it; first is c, or -1 where there is none. The workspace begins with them.
+struct Shared {
+    int b, j, first, last;
+};
+
+__host__ __device__ constexpr int attend_header_bytes() { return kAttendCtas * (int)sizeof(Shared); }
+
+cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& dev, const WriteArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read(int fmt, int dt, const Device& dev, const ReadArgs& a, cudaStream_t stream);
+cudaError_t launch_attend(int fmt, int dt, const Device& dev, const AttendArgs& a, cudaStream_t stream);
+
+}  // namespace sgq
