@@ -7,14 +7,15 @@
 // have computed of one sequence.
 //
 // Shares. An item is a sequence and a head of the cache (a chunk of its group of
-// q heads, where there are more than a CTA's columns); its tiles are 64 tokens
-// each. All items' tiles stand in one row, and CTA c of G takes those from
-// total c / G to total (c + 1) / G. The lengths are summed on the device, so a
+// q heads, where there are more than a CTA's columns); its tiles are 64 tokens,
+// 128 of E4M3 rows. All items' tiles stand in one row, and CTA c of G takes those from
+// c total / G on, total / G of them, rounded up or down. The lengths are summed on the device, so a
 // captured graph follows them.
 //
-// Inside a CTA each of four warps takes 16 tokens of every tile and runs by itself:
-// its own asynchronous copies, several tiles ahead and across the items' borders, its own
-// running maximum and sums. The warps meet where an item ends, to add up.
+// Inside a CTA each of four groups of warps takes a quarter of every tile's tokens, and each warp of a
+// group 8 columns of them. A group runs by itself: its own asynchronous copies, several tiles
+// ahead and across the items' borders; a warp has its own running maximum and sums. All warps meet where an
+// item ends, to add up.
 //
 // Products, transposed so that a small group wastes little of a tile: the tokens are
 // the 16 rows of S = K q^T, the heads its 8 columns. p comes out of S with a
@@ -36,29 +37,43 @@
 namespace sgq {
 namespace attend {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;                        // tokens a warp takes at a time
+constexpr int kParts = 4;                        // of a tile's tokens, a group of warps each
 constexpr float kNone = -3.0e38f;                // below every logit
-constexpr float kRoom = 8.0f;                    // log2 of what p may exceed 1 by
+constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
 
 // Kinds of rows and queries.
 enum Kind : int { BF16 = 0, F16 = 1, FP8_BF16 = 2, FP8_F16 = 3 };
 
-template <int KIND, int DP, int NT>
+// CG: groups of 8 columns, a warp of each group of warps for each.
+template <int KIND, int DP, int CG>
 struct Shape {
     static constexpr bool fp8 = KIND >= FP8_BF16;
+#ifndef ATT_H
+#define ATT_H 2
+#endif
+#ifndef ATT_C16
+#define ATT_C16 2
+#endif
+#ifndef ATT_C8
+#define ATT_C8 2
+#endif
+    static constexpr int warps = kParts * CG, threads = warps * 32;
+    static constexpr int halves = fp8 ? ATT_H : 1;               // 16 tokens each, of those that a warp takes at a time
+    static constexpr int rows = 16 * halves;
+    static constexpr uint32_t full = rows == 32 ? 0xFFFFFFFFu : 0xFFFFu;         // the mask of rows that are all there
+    static constexpr int tokens = kParts * rows;                 // of a tile
     static constexpr int elem = fp8 ? 1 : 2;
     static constexpr int pieces = DP * elem / 16;                // 16-byte pieces of a row
     static constexpr int stride = DP * elem + 16;                // of rows in shared memory: 8 rows' pieces meet no bank twice
-    static constexpr int slot = 2 * kRows * stride + (fp8 ? 2 * kRows * 4 : 0);
-    static constexpr int budget = 104 * 1024;                    // two CTAs a multiprocessor
-    static constexpr int fit = budget / (slot * kWarps);
+    static constexpr int slot = 2 * rows * stride + (fp8 ? 2 * rows * 4 : 0);
+    static constexpr int ctas = DP == 256 ? (CG == 1 ? 2 : 1) : CG == 1 ? (fp8 ? ATT_C8 : ATT_C16) : CG == 2 ? 2 : 1;   // a multiprocessor
+    static constexpr int fit = (227 * 1024 / ctas - 4096) / (slot * kParts);
     static constexpr int stages = fit < 2 ? 2 : fit > 8 ? 8 : fit;
-    static constexpr int smem = stages * slot * kWarps;
+    static constexpr int smem = stages * slot * kParts;
     static constexpr int parts = KIND == FP8_BF16 ? 1 : 2;       // 16-bit parts of p
-    static constexpr int ctas = smem <= 110 * 1024 ? 2 : 1;      // a multiprocessor
-    static_assert(8 * (DP + 4) * 4 <= slot, "an item's sums of 8 columns pass through a slot");
+    static constexpr int line = (DP + 4) * 4;                    // bytes of a column's sums: 4 lanes' columns meet no bank twice
+    static constexpr int at_once = slot / (8 * line) < CG ? slot / (8 * line) : CG;      // groups of columns whose sums pass through a slot
+    static_assert(at_once >= 1 && CG % at_once == 0 && smem <= 227 * 1024 - 2048, "");
 };
 
 template <bool BF>
@@ -129,9 +144,11 @@ __device__ __forceinline__ float scale_log(float s) {
     return (float)max(-100, min(100, e));
 }
 
-// Walks over the tiles of a CTA's share.
+// Walks over the tiles of a CTA's share, tiles of TOKENS each.
+template <int TOKENS>
 struct Walk {
-    int b, j;            // sequence, item of it
+    int b, j;            // sequence, item of it: chunk `chunk` of the cache's head `head`
+    int head, chunk;
     int tile, tiles;     // of the item
     int lo, n;           // tokens [lo, n) are not masked
     int start;           // first token of the first tile
@@ -140,16 +157,10 @@ struct Walk {
         b = seq;
         n = min(max(length, 0), a.limit);
         lo = a.window > 0 && n > a.window ? n - a.window : 0;
-        start = lo / kAttendTile * kAttendTile;
-        tiles = max(1, (n - start + kAttendTile - 1) / kAttendTile);
+        start = lo / TOKENS * TOKENS;
+        tiles = max(1, (n - start + TOKENS - 1) / TOKENS);
     }
 };
-
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int length) {
-    Walk w;
-    w.enter(a, 0, length);
-    return w.tiles;
-}
 
 // An item's result: sums of columns rel. to the reference m (log2), and their total.
 __device__ __forceinline__ void finish(const AttendArgs& a, int b, int head, float m, float l, float& inv, float& lse) {
@@ -165,362 +176,431 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int b, int head, flo
     lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <int KIND, int DP, int NT>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
-    using S = Shape<KIND, DP, NT>;
+template <int KIND, int DP, int CG>
+__global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, CG>::ctas) attend_kernel(const AttendArgs a) {
+    using S = Shape<KIND, DP, CG>;
     constexpr bool kF8 = S::fp8, kBf = KIND == BF16;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
-    constexpr int kSteps = DP / 16, kCols = NT * 8;
+    constexpr int kSteps = DP / 16, kCols = CG * 8, kThreads = S::threads;
     extern __shared__ __align__(16) uint8_t stages[];
-    __shared__ long long sum_part[kWarps];
-    __shared__ long long share_at;
-    __shared__ int share_b;
-    __shared__ float s_m[kWarps][kCols], s_l[kWarps][kCols];
+    __shared__ int sum_part[S::warps];
+    __shared__ int share_b, share_n, share_off;
+    __shared__ float s_m[kParts][kCols], s_l[kParts][kCols];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int part = warp % kParts, cg = warp / kParts;          // of the tile's tokens, of the columns
+    // the warps of a part of the tokens, who share its copies
+    auto group_sync = [&]() {
+        if (CG == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + part), "n"(CG * 32) : "memory");
+    };
 
     pdl_wait();
     pdl_trigger();
 
     // The CTA's share of all tiles, and where it begins: each thread sums the tiles of a run of sequences.
+    using W = Walk<S::tokens>;
+    auto tiles_of = [&](int length) {
+        W w;
+        w.enter(a, 0, length);
+        return w.tiles * a.items;
+    };
     const int run = (a.B + kThreads - 1) / kThreads, b_from = min((int)threadIdx.x * run, a.B), b_to = min(b_from + run, a.B);
-    long long mine = 0;
-    for (int b = b_from; b < b_to; ++b) mine += tiles_of(a, a.lengths[b]);
-    long long before = mine;
+    int mine = 0;
+    for (int b = b_from; b < b_to; ++b) mine += tiles_of(a.lengths[b]);
+    int before = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
         if (lane >= d) before += o;
     }
     if (lane == 31) sum_part[warp] = before;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < S::warps; ++w) {
         if (w < warp) before += sum_part[w];
         total += sum_part[w];
     }
     before -= mine;
-    total *= a.items;
-    // no CTA between two that share an item is without a tile: with fewer tiles than CTAs the last ones have none
-    const long long G = min((long long)gridDim.x, total), me = min((long long)blockIdx.x, G);
-    const long long from = total * me / G, to = total * min(me + 1, G) / G;
-    if (from >= before * a.items && from < (before + mine) * a.items) {
-        long long at = before * a.items;
+    // With fewer tiles than CTAs the last ones have none: no CTA between two that share an item is without a tile.
+    const int G = min((int)gridDim.x, total), me = (int)blockIdx.x;
+    const int each = total / G, more = total - each * G;         // the first `more` CTAs take one tile more
+    const int from = me * each + min(me, more), count = me >= G ? 0 : each + (me < more ? 1 : 0);
+    if (count > 0 && from >= before && from < before + mine) {
+        int at = before;
         for (int b = b_from; b < b_to; ++b) {
-            const long long next = at + (long long)tiles_of(a, a.lengths[b]) * a.items;
+            const int n = a.lengths[b], next = at + tiles_of(n);
             if (from < next) {
                 share_b = b;
-                share_at = at;
+                share_n = n;
+                share_off = from - at;
                 break;
             }
             at = next;
         }
     }
     __syncthreads();
-    if (from >= to) {
+    if (count == 0) {
         if (a.joined && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
         return;
     }
 
-    Walk ld;
-    ld.enter(a, share_b, a.lengths[share_b]);
-    {
-        const long long off = from - share_at;
-        ld.j = (int)(off / ld.tiles);
-        ld.tile = (int)(off - (long long)ld.j * ld.tiles);
-    }
-    Walk cu = ld;
-    long long left = to - from;                                  // tiles to copy
+    W ld;
+    ld.enter(a, share_b, share_n);
+    ld.j = share_off / ld.tiles;
+    ld.tile = share_off - ld.j * ld.tiles;
+    ld.head = ld.j / a.chunks;
+    ld.chunk = ld.j - ld.head * a.chunks;
+    W cu = ld;
+    int left = count;                                            // tiles to copy
     int next_n = ld.b + 1 < a.B ? a.lengths[ld.b + 1] : 0;
 
-    auto advance = [&](Walk& w, bool ahead) {
+    auto advance = [&](W& w, bool ahead) {
         if (++w.tile < w.tiles) return;
         w.tile = 0;
+        if (++w.chunk == a.chunks) {
+            w.chunk = 0;
+            ++w.head;
+        }
         if (++w.j < a.items) return;
-        w.j = 0;
+        w.j = w.head = 0;
         if (w.b + 1 >= a.B) return;                              // behind the last: not used
         w.enter(a, w.b + 1, ahead ? next_n : a.lengths[w.b + 1]);
         if (ahead) next_n = w.b + 1 < a.B ? a.lengths[w.b + 1] : 0;
     };
 
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(stages) + warp * S::stages * S::slot;
-    __shared__ uint32_t s_mask[kWarps][S::stages];
-    auto page_of = [&](const Walk& w) {                          // of the lane's token of w's tile; -1 where it is masked
-        const int t = w.start + w.tile * kAttendTile + warp * kRows + (lane & 15);
+    // Copying. Where pages are whole multiples of 16 tokens, 16 tokens have one page and lie
+    // a stride apart; else each lane finds its own token's row.
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(stages) + part * S::stages * S::slot;
+    __shared__ uint32_t s_mask[kParts][S::stages];
+    const bool even = (a.c.page.d & 15) == 0;
+    const int64_t v_from_k = a.c.v - a.c.k;
+    constexpr int kRowsAt = 32 / S::pieces > 0 ? 32 / S::pieces : 1;              // rows that 32 lanes copy at once
+    const int lane_row = kRowsAt > 1 ? lane / S::pieces : 0, piece = lane % S::pieces;
+    const bool used = piece * 16 < a.c.D * S::elem;              // columns from D on are filled with zeros
+    const uint32_t lane_to = lane_row * S::stride + piece * 16;
+    const int64_t lane_from = lane_row * a.c.ts + (used ? piece * 16 : 0), row_step = kRowsAt * a.c.ts;
+    // the lane's token of w's tile (of 16 tokens both halves of a warp have the same)
+    auto token_of = [&](const W& w) { return w.start + w.tile * S::tokens + part * S::rows + (lane & (S::rows - 1)); };
+    auto page_of = [&](const W& w) {                             // of the lane's token; -1 where it is masked
+        const int t = token_of(w);
         if (t < w.lo || t >= w.n) return -1;
         return a.table[w.b * a.width + quotient(t, a.c.page)];
     };
-    // Copies w's tile into a slot; pid: page_of(w), asked for a tile before.
-    auto copy = [&](const Walk& w, int slot, int pid) {
+    // Copies w's tile into a slot, the group's warps each their share; pid: page_of(w), asked for a tile before.
+    auto copy = [&](const W& w, int slot, int pid) {
         const uint32_t at = base + slot * S::slot;
-        const int t = w.start + w.tile * kAttendTile + warp * kRows + (lane & 15);
-        const int head = w.j / a.chunks;
+        const int t = token_of(w);
         const bool there = pid >= 0 && pid < a.c.pages;
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & 0xFFFFu;
-        const int place = there ? t - (int)(quotient(t, a.c.page) * a.c.page.d) : 0;
-        const int64_t page = there ? pid : 0;
-        const int64_t off = page * a.c.ps + (int64_t)head * a.c.hs + place * a.c.ts;
-        if (lane == 0) s_mask[warp][slot] = mask;
-        constexpr int kRowsAt = 32 / S::pieces > 0 ? 32 / S::pieces : 1;      // rows that 32 lanes copy at once
-        const int used = a.c.D * S::elem / 16;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & S::full;
+        if (lane == 0 && cg == 0) s_mask[part][slot] = mask;
+        const int place = t - (int)(quotient(t, a.c.page) * a.c.page.d);
+        constexpr int kTurns = 16 / kRowsAt;                     // of 16 tokens
+        if (even) {
+            // a token of the 16 that is there has their page
+            const int h0 = S::rows == 32 ? lane & 16 : 0;
+            const uint32_t some0 = (mask >> h0) & 0xFFFFu;
+            const int p = __shfl_sync(0xFFFFFFFFu, pid, h0 + (some0 ? __ffs(some0) - 1 : 0)), first = __shfl_sync(0xFFFFFFFFu, place, h0);
+            const int64_t off = (int64_t)(some0 ? p : 0) * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)first * a.c.ts;
 #pragma unroll
-        for (int i = 0; i < kRows * S::pieces / 32; ++i) {
-            const int row = i * 32 / S::pieces + (kRowsAt > 1 ? lane / S::pieces : 0);
-            const int piece = lane % S::pieces;
-            const uint32_t lo = __shfl_sync(0xFFFFFFFFu, (uint32_t)off, row), hi = __shfl_sync(0xFFFFFFFFu, (uint32_t)(off >> 32), row);
-            const int64_t o = (int64_t)(((uint64_t)hi << 32) | lo) + piece * 16;
-            const bool ok = ((mask >> row) & 1) && piece < used;
-            const uint32_t to_k = at + row * S::stride + piece * 16;
-            copy16(to_k, a.c.k + (ok ? o : 0), ok);
-            copy16(to_k + kRows * S::stride, a.c.v + (ok ? o : 0), ok);
-        }
-        if (kF8) {
-            const int64_t row = (page * a.c.heads + head) * a.c.page.d + place;
-            copy4(at + 2 * kRows * S::stride + lane * 4, (lane < 16 ? a.c.ks : a.c.vs) + row, there);
-        }
-    };
-
-    // q of the current item as the right operand of S, and the factors of its columns.
-    uint32_t qf[kSteps][NT][2];
-    float factor[NT][2];
-    auto load_q = [&](const Walk& w) {
-        constexpr float kLog2e = 1.44269504088896340736f;
-        const int head = w.j / a.chunks, first = (w.j - head * a.chunks) * kCols;
+            for (int h = 0; h < S::halves; ++h) {
+                const uint32_t some = (mask >> (16 * h)) & 0xFFFFu;
+                const uint8_t* k = a.c.k + ((S::halves > 1 ? __shfl_sync(0xFFFFFFFFu, off, 16 * h) : off) + lane_from + cg * row_step);
+                uint32_t to = at + h * 16 * S::stride + lane_to + cg * kRowsAt * S::stride;
+                if (some == 0xFFFFu) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = first + nt * 8 + g;
-            const bool there = col < a.group;
-            const uint16_t* q = a.q.p + (int64_t)w.b * a.q.ts + (int64_t)(there ? head * a.group + col : 0) * a.q.hs;
-            float top = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                // the columns that this lane's pieces of k meet
-                const int d0 = kF8 ? (kk >> 2) * 64 + c * 16 + (kk & 3) * 4 : kk * 16 + c * 2, d1 = kF8 ? d0 + 2 : d0 + 8;
-                const uint32_t* p = reinterpret_cast<const uint32_t*>(q);
-                qf[kk][nt][0] = there && d0 < a.c.D ? p[d0 >> 1] : 0u;
-                qf[kk][nt][1] = there && d1 < a.c.D ? p[d1 >> 1] : 0u;
-                if (KIND == FP8_BF16) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][nt][i] << 16)), fabsf(__uint_as_float(qf[kk][nt][i] & 0xFFFF0000u))));
+                    for (int i = 0; i < kTurns; i += CG) {
+                        if (kTurns % CG == 0 || i + cg < kTurns) {
+                            copy16(to, k, used);
+                            copy16(to + S::rows * S::stride, k + v_from_k, used);
+                        }
+                        k += CG * row_step;
+                        to += CG * kRowsAt * S::stride;
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = cg; i < kTurns; i += CG) {
+                        const bool ok = used && ((some >> (i * kRowsAt + lane_row)) & 1);
+                        copy16(to, ok ? k : a.c.k, ok);
+                        copy16(to + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
+                        k += CG * row_step;
+                        to += CG * kRowsAt * S::stride;
+                    }
                 }
             }
-            float up = 1.0f;
-            if (KIND == FP8_BF16) {      // bf16 -> fp16 by a power of two a head, its largest value in [1, 2)
-                top = group_max<4>(top);
-                const int e = max(-120, min(120, (int)(__float_as_uint(top) >> 23) - 127));
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                for (int kk = 0; kk < kSteps; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t v = qf[kk][nt][i];
-                        qf[kk][nt][i] = f32x2_to_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
-                    }
+        } else {
+            const int64_t off = there ? (int64_t)pid * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)place * a.c.ts : 0;
+            uint32_t to = at + lane_to + cg * kRowsAt * S::stride;
+#pragma unroll 4
+            for (int i = cg; i < S::rows / kRowsAt; i += CG) {
+                const int row = i * kRowsAt + lane_row;
+                const bool ok = used && ((mask >> row) & 1);
+                const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + (used ? piece * 16 : 0);
+                copy16(to, ok ? k : a.c.k, ok);
+                copy16(to + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
+                to += CG * kRowsAt * S::stride;
             }
-            // column 2c (+ 1)'s factor is held by the lanes of row 2c (+ 1)
-            factor[nt][0] = __shfl_sync(0xFFFFFFFFu, up, c * 8) * (a.scale * kLog2e);
-            factor[nt][1] = __shfl_sync(0xFFFFFFFFu, up, c * 8 + 4) * (a.scale * kLog2e);
+        }
+        if (kF8 && cg == CG - 1 && lane < S::rows) {
+            const int64_t row = there ? ((int64_t)pid * a.c.heads + w.head) * a.c.page.d + place : 0;
+            const uint32_t to = at + 2 * S::rows * S::stride + lane * 4;
+            copy4(to, a.c.ks + row, there);
+            copy4(to + S::rows * 4, a.c.vs + row, there);
         }
     };
 
-    float o[kSteps][NT][4], ref[NT][2], sum[NT][2];
-    auto clear = [&]() {
+    // q of the current item as the right operand of S, and the factors of its columns: asked for, then made ready.
+    uint32_t qf[kSteps][2];
+    float factor[2];
+    auto ask_q = [&](const W& w) {
+        const int col = w.chunk * kCols + cg * 8 + g;
+        const bool there = col < a.group;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q.p + (int64_t)w.b * a.q.ts + (int64_t)(there ? w.head * a.group + col : 0) * a.q.hs);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            ref[nt][0] = ref[nt][1] = kNone;
-            sum[nt][0] = sum[nt][1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+        for (int kk = 0; kk < kSteps; ++kk) {
+            // the columns that this lane's pieces of k meet
+            const int d0 = kF8 ? (kk >> 2) * 64 + c * 16 + (kk & 3) * 4 : kk * 16 + c * 2, d1 = kF8 ? d0 + 2 : d0 + 8;
+            qf[kk][0] = there && d0 < a.c.D ? q[d0 >> 1] : 0u;
+            qf[kk][1] = there && d1 < a.c.D ? q[d1 >> 1] : 0u;
         }
+    };
+    auto ready_q = [&]() {
+        constexpr float kLog2e = 1.44269504088896340736f;
+        float up = 1.0f;
+        if (KIND == FP8_BF16) {      // bf16 -> fp16 by a power of two a head, its largest value in [1, 2)
+            float top = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][i] << 16)), fabsf(__uint_as_float(qf[kk][i] & 0xFFFF0000u))));
+            top = group_max<4>(top);
+            const int e = max(-120, min(120, (int)(__float_as_uint(top) >> 23) - 127));
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t v = qf[kk][i];
+                    qf[kk][i] = f32x2_to_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
+                }
+        }
+        // column 2c (+ 1)'s factor is held by the lanes of row 2c (+ 1)
+        factor[0] = __shfl_sync(0xFFFFFFFFu, up, c * 8) * (a.scale * kLog2e);
+        factor[1] = __shfl_sync(0xFFFFFFFFu, up, c * 8 + 4) * (a.scale * kLog2e);
+    };
+
+    float o[kSteps][4], ref[2], sum[2];
+    auto clear = [&]() {
+        ref[0] = ref[1] = kNone;
+        sum[0] = sum[1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     };
 
     auto tile = [&](int slot) {
-        const uint32_t at = base + slot * S::slot, vt = at + kRows * S::stride, sc = vt + kRows * S::stride;
-        const uint32_t mask = s_mask[warp][slot];
-        float x[NT][4] = {}, x2[NT][4] = {};         // two chains of products
+        constexpr int H = S::halves;
+        const uint32_t at = base + slot * S::slot, vt = at + S::rows * S::stride, sc = vt + S::rows * S::stride;
+        const uint32_t mask = s_mask[part][slot];
+        float x[H][4];
         if (!kF8) {
+            float x2[4] = {};                        // two chains of products
             const uint32_t from = at + (lane & 15) * S::stride + (lane >> 4) * 16;
+            x[0][0] = x[0][1] = x[0][2] = x[0][3] = 0.0f;
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
                 uint32_t k[4];
                 ldmatrix4(k, from + kk * 32);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<kBf>(kk & 1 ? x2[nt] : x[nt], k, qf[kk][nt][0], qf[kk][nt][1]);
+                mma<kBf>(kk & 1 ? x2 : x[0], k, qf[kk][0], qf[kk][1]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[0][i] = (x[0][i] + x2[i]) * factor[i & 1];
         } else {
 #pragma unroll
-            for (int blk = 0; blk < DP / 64; ++blk) {
-                const uint4 p = lds16(at + g * S::stride + blk * 64 + c * 16), q = lds16(at + (g + 8) * S::stride + blk * 64 + c * 16);
-                const uint32_t up[4] = {p.x, p.y, p.z, p.w}, dn[4] = {q.x, q.y, q.z, q.w};
+            for (int h = 0; h < H; ++h) {
+                float x2[4] = {};
+                x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.0f;
+                const float k0 = lds_f32(sc + (h * 16 + g) * 4), k1 = lds_f32(sc + (h * 16 + g + 8) * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t k[4];
-                    widen(up[i], k[0], k[2]);
-                    widen(dn[i], k[1], k[3]);
+                for (int blk = 0; blk < DP / 64; ++blk) {
+                    const uint32_t from = at + (h * 16 + g) * S::stride + blk * 64 + c * 16;
+                    const uint4 p = lds16(from), q = lds16(from + 8 * S::stride);
+                    const uint32_t up[4] = {p.x, p.y, p.z, p.w}, dn[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma<false>(i & 1 ? x2[nt] : x[nt], k, qf[blk * 4 + i][nt][0], qf[blk * 4 + i][nt][1]);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t k[4];
+                        widen(up[i], k[0], k[2]);
+                        widen(dn[i], k[1], k[3]);
+                        mma<false>(i & 1 ? x2 : x[h], k, qf[blk * 4 + i][0], qf[blk * 4 + i][1]);
+                    }
                 }
-            }
-        }
-        float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f}, lg[2] = {0.0f, 0.0f};
-        if (kF8) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                ks[r] = lds_f32(sc + (g + 8 * r) * 4);
-                vs[r] = lds_f32(sc + (kRows + g + 8 * r) * 4);
-                lg[r] = scale_log(vs[r]);
+                for (int i = 0; i < 4; ++i) x[h][i] = (x[h][i] + x2[i]) * (factor[i & 1] * (i < 2 ? k0 : k1));
             }
         }
+        if (mask != S::full) {
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!((mask >> (h * 16 + g + 8 * (i >> 1))) & 1)) x[h][i] = -INFINITY;
+        }
+        // p, and w = p times the row's v scale. Where one is out of bounds (or no number) the reference moves.
+        float vs[H][2], w[H][4], s0 = 0.0f, s1 = 0.0f;
         bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < H; ++h) {
+            vs[h][0] = kF8 ? lds_f32(sc + (S::rows + h * 16 + g) * 4) : 1.0f;
+            vs[h][1] = kF8 ? lds_f32(sc + (S::rows + h * 16 + g + 8) * 4) : 1.0f;
+        }
+        auto weigh = [&]() {
+            s0 = s1 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = i & 1, r = i >> 1;
-                float v = (x[nt][i] + x2[nt][i]) * factor[nt][col];
-                if (kF8) v *= ks[r];
-                if (!((mask >> (g + 8 * r)) & 1)) v = -INFINITY;
-                x[nt][i] = v;
-                over |= (kF8 ? v + lg[r] : v) > ref[nt][col] + kRoom;
+            for (int h = 0; h < H; ++h) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[h][i] = ex2_approx(x[h][i] - ref[i & 1]);
+                s0 += w[h][0] + w[h][2];
+                s1 += w[h][1] + w[h][3];
+                if (kF8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[h][i] *= vs[h][i >> 1];
+                }
             }
+        };
+        weigh();
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) over |= !(w[h][i] <= kMost);
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int col = 0; col < 2; ++col) {
+                float top = ref[col];
 #pragma unroll
-                for (int col = 0; col < 2; ++col) {
-                    float top = fmaxf(x[nt][col] + lg[0], x[nt][2 + col] + lg[1]);
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    top = fmaxf(top, ref[nt][col]);
-                    const float f = ex2_approx(ref[nt][col] - top);
-                    ref[nt][col] = top;
-                    sum[nt][col] *= f;
+                    for (int r = 0; r < 2; ++r) top = fmaxf(top, kF8 ? x[h][2 * r + col] + scale_log(vs[h][r]) : x[h][2 * r + col]);
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        o[i][nt][col] *= f;
-                        o[i][nt][2 + col] *= f;
-                    }
+                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                const float f = ex2_approx(ref[col] - top);
+                ref[col] = top;
+                sum[col] *= f;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    o[i][col] *= f;
+                    o[i][2 + col] *= f;
                 }
+            }
+            weigh();
         }
-        uint32_t p[S::parts][NT][2];
+        sum[0] += s0;
+        sum[1] += s1;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < H; ++h) {
+            uint32_t p[S::parts][2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float w0 = ex2_approx(x[nt][2 * r] - ref[nt][0]), w1 = ex2_approx(x[nt][2 * r + 1] - ref[nt][1]);
-                sum[nt][0] += w0;
-                sum[nt][1] += w1;
-                if (kF8) {
-                    w0 *= vs[r];
-                    w1 *= vs[r];
-                }
+                const float w0 = w[h][2 * r], w1 = w[h][2 * r + 1];
                 const uint32_t hi = kBf ? f32x2_to_bf16x2(w0, w1) : f32x2_to_f16x2(w0, w1);
-                p[0][nt][r] = transposed(hi);
+                p[0][r] = transposed(hi);
                 if (S::parts == 2) {
                     const float2 back = kBf ? make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)) : f16x2_to_f32x2(hi);
-                    p[S::parts - 1][nt][r] = transposed(kBf ? f32x2_to_bf16x2(w0 - back.x, w1 - back.y) : f32x2_to_f16x2(w0 - back.x, w1 - back.y));
+                    p[S::parts - 1][r] = transposed(kBf ? f32x2_to_bf16x2(w0 - back.x, w1 - back.y) : f32x2_to_f16x2(w0 - back.x, w1 - back.y));
                 }
             }
-        if (!kF8) {
-            // 8 x 8 pieces of V^T: tokens 0-7 by columns 0-7, columns 8-15, then tokens 8-15
-            const uint32_t from = vt + ((lane & 7) + (lane >> 4) * 8) * S::stride + ((lane >> 3) & 1) * 16;
+            if (!kF8) {
+                // 8 x 8 pieces of V^T: tokens 0-7 by columns 0-7, columns 8-15, then tokens 8-15
+                const uint32_t from = vt + ((lane & 7) + (lane >> 4) * 8) * S::stride + ((lane >> 3) & 1) * 16;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                uint32_t v[4];
-                ldmatrix4t(v, from + i * 32);
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t v[4];
+                    ldmatrix4t(v, from + i * 32);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < S::parts; ++e) mma<kBf>(o[i][nt], v, p[e][nt][0], p[e][nt][1]);
-            }
-        } else {
-            constexpr int kWords = DP >= 128 ? 4 : 2;            // 4 codes of a token each
-#pragma unroll
-            for (int blk = 0; blk < (DP + 127) / 128; ++blk) {
-                uint32_t v[4][4];                                // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t from = vt + (2 * c + (t & 1) + (t >> 1) * 8) * S::stride + blk * 128 + g * kWords * 4;
-                    if (kWords == 4) {
-                        const uint4 q = lds16(from);
-                        v[t][0] = q.x, v[t][1] = q.y, v[t][2] = q.z, v[t][3] = q.w;
-                    } else {
-                        const uint2 q = lds8(from);
-                        v[t][0] = q.x, v[t][1] = q.y;
-                    }
+                    for (int e = 0; e < S::parts; ++e) mma<kBf>(o[i], v, p[e][0], p[e][1]);
                 }
+            } else {
+                constexpr int kWords = DP >= 128 ? 4 : 2;        // 4 codes of a token each
 #pragma unroll
-                for (int w = 0; w < kWords; ++w)
+                for (int blk = 0; blk < (DP + 127) / 128; ++blk) {
+                    uint32_t v[4][4];                            // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {                // columns 4 w + 2 e, + 1 of the lane's
-                        uint32_t m[4];
-                        widen(__byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140), m[0], m[1]);
-                        widen(__byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140), m[2], m[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int part = 0; part < S::parts; ++part)
-                                mma<false>(o[blk * 8 + 2 * w + e][nt], m, p[part][nt][0], p[part][nt][1]);
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t from = vt + (h * 16 + 2 * c + (t & 1) + (t >> 1) * 8) * S::stride + blk * 128 + g * kWords * 4;
+                        if (kWords == 4) {
+                            const uint4 q = lds16(from);
+                            v[t][0] = q.x, v[t][1] = q.y, v[t][2] = q.z, v[t][3] = q.w;
+                        } else {
+                            const uint2 q = lds8(from);
+                            v[t][0] = q.x, v[t][1] = q.y;
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {            // columns 4 i + 2 e, + 1 of the lane's
+                            uint32_t m[4];
+                            widen(__byte_perm(v[0][i], v[1][i], e ? 0x7362 : 0x5140), m[0], m[1]);
+                            widen(__byte_perm(v[2][i], v[3][i], e ? 0x7362 : 0x5140), m[2], m[3]);
+#pragma unroll
+                            for (int n = 0; n < S::parts; ++n) mma<false>(o[blk * 8 + 2 * i + e], m, p[n][0], p[n][1]);
+                        }
+                }
             }
         }
     };
 
     // Adds up what the warps have of the item at w and writes it: the result, or this CTA's part of it.
-    auto flush = [&](const Walk& w, int slot, bool begun_here, bool ends_here) {
-        const int head = w.j / a.chunks, first = (w.j - head * a.chunks) * kCols;
+    auto flush = [&](const W& w, int slot, bool begun_here, bool ends_here) {
         const bool whole = begun_here && ends_here;
-        float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attend_header_bytes()) +
-                      (size_t)(2 * blockIdx.x + (begun_here ? 1 : 0)) * attend_part(kCols, DP);
+        float* to_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attend_header_bytes()) +
+                         (size_t)(2 * blockIdx.x + (begun_here ? 1 : 0)) * attend_part(kCols, DP);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int col = 0; col < 2; ++col) {
+            float l = sum[col];
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
-                float l = sum[nt][col];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-                if (g == 0) {
-                    s_m[warp][nt * 8 + 2 * c + col] = ref[nt][col];
-                    s_l[warp][nt * 8 + 2 * c + col] = l;
-                }
+            for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            if (g == 0) {
+                s_m[part][cg * 8 + 2 * c + col] = ref[col];
+                s_l[part][cg * 8 + 2 * c + col] = l;
             }
-        const uint32_t own = base + slot * S::slot;
-        constexpr int kLine = (DP + 4) * 4;                      // bytes of a column: 4 lanes' columns meet no bank twice
+        }
+        group_sync();
+        constexpr int kEach = kThreads / (8 * S::at_once);       // threads a column, 4 values at a time
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            __syncwarp();
+        for (int round = 0; round < CG / S::at_once; ++round) {
+            if (cg / S::at_once == round) {
+                const uint32_t own = base + slot * S::slot + (cg % S::at_once) * 8 * S::line;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+                for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = 2 * c + (e & 1), r = e >> 1;
-                    constexpr int kEach = DP >= 128 ? 16 : 8;    // columns of V side by side in a lane (FP8)
-                    const int d = kF8 ? (i >> 3) * 128 + g * kEach + 2 * (i & 7) + r : i * 16 + g + 8 * r;
-                    sts_f32(own + col * kLine + d * 4, o[i][nt][e]);
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        const int col = 2 * c + (e & 1), r = e >> 1;
+                        constexpr int kSide = DP >= 128 ? 16 : 8;                // columns of V side by side in a lane (FP8)
+                        const int d = kF8 ? (i >> 3) * 128 + g * kSide + 2 * (i & 7) + r : i * 16 + g + 8 * r;
+                        sts_f32(own + col * S::line + d * 4, o[i][e]);
+                    }
+            }
             __syncthreads();
-            // 16 threads a column, 4 values at a time
-            const int col = threadIdx.x >> 4, q = first + nt * 8 + col;
+            const int at = threadIdx.x / kEach, col = round * S::at_once * 8 + at, q = w.chunk * kCols + col;
             if (q < a.group) {
-                float M = kNone, f[kWarps], L = 0.0f;
+                float M = kNone, f[kParts], L = 0.0f;
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) M = fmaxf(M, s_m[v][nt * 8 + col]);
+                for (int v = 0; v < kParts; ++v) M = fmaxf(M, s_m[v][col]);
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v) {
-                    f[v] = ex2_approx(s_m[v][nt * 8 + col] - M);
-                    L += s_l[v][nt * 8 + col] * f[v];
+                for (int v = 0; v < kParts; ++v) {
+                    f[v] = ex2_approx(s_m[v][col] - M);
+                    L += s_l[v][col] * f[v];
                 }
-                const int qh = head * a.group + q;
+                const int qh = w.head * a.group + q;
                 float inv = 1.0f, lse = 0.0f;
                 if (whole) finish(a, w.b, qh, M, L, inv, lse);
-                const uint32_t all = (uint32_t)__cvta_generic_to_shared(stages) + slot * S::slot + col * kLine;
+                const uint32_t all = (uint32_t)__cvta_generic_to_shared(stages) + slot * S::slot + at * S::line;
 #pragma unroll
-                for (int d = (threadIdx.x & 15) * 4; d < DP; d += 64) {
+                for (int d = (threadIdx.x % kEach) * 4; d < DP; d += kEach * 4) {
                     float4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int v = 0; v < kWarps; ++v) {
+                    for (int v = 0; v < kParts; ++v) {
                         const uint4 u = lds16(all + v * S::stages * S::slot + d * 4);
                         y.x += __uint_as_float(u.x) * f[v];
                         y.y += __uint_as_float(u.y) * f[v];
@@ -528,7 +608,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
                         y.w += __uint_as_float(u.w) * f[v];
                     }
                     if (!whole) {
-                        *reinterpret_cast<float4*>(part + (nt * 8 + col) * DP + d) = y;
+                        *reinterpret_cast<float4*>(to_part + col * DP + d) = y;
                     } else if (d < a.c.D) {
                         uint16_t* to = a.out + ((int64_t)w.b * a.q.n + qh) * a.c.D + d;
                         const uint2 v = kDt == DT_BF16 ? make_uint2(f32x2_to_bf16x2(y.x * inv, y.y * inv), f32x2_to_bf16x2(y.z * inv, y.w * inv))
@@ -536,10 +616,10 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
                         *reinterpret_cast<uint2*>(to) = v;
                     }
                 }
-                if ((threadIdx.x & 15) == 0) {
+                if (threadIdx.x % kEach == 0) {
                     if (!whole) {
-                        part[kCols * DP + nt * 8 + col] = M;
-                        part[kCols * DP + kCols + nt * 8 + col] = L;
+                        to_part[kCols * DP + col] = M;
+                        to_part[kCols * DP + kCols + col] = L;
                     } else if (a.lse) {
                         a.lse[(int64_t)w.b * a.q.n + qh] = lse;
                     }
@@ -549,55 +629,62 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
         }
     };
 
-    // Copies run S::stages tiles ahead, a commit group each (empty behind the last).
-    int pid = page_of(ld);
-#pragma unroll 1
+    // Copies run S::stages tiles ahead, a commit group each (empty behind the last). The
+    // first ones' pages are asked for together.
+    int pids[S::stages];
+    {
+        W w = ld;
+#pragma unroll
+        for (int s = 0; s < S::stages; ++s) {
+            pids[s] = s < left ? page_of(w) : -1;
+            advance(w, false);
+        }
+    }
+    ask_q(cu);
+#pragma unroll
     for (int s = 0; s < S::stages; ++s) {
         if (left > 0) {
-            copy(ld, s, pid);
-            if (--left > 0) {
-                advance(ld, true);
-                pid = page_of(ld);
-            }
+            copy(ld, s, pids[s]);
+            --left;
+            advance(ld, true);
         }
         cp_async_commit();
     }
-    load_q(cu);
+    int pid = left > 0 ? page_of(ld) : -1;
+    ready_q();
     clear();
     bool begun_here = cu.tile == 0;
-    long long todo = to - from;
+    int todo = count;
     for (int slot = 0; todo > 0; slot = slot + 1 == S::stages ? 0 : slot + 1) {
         cp_async_wait<S::stages - 1>();
-        __syncwarp();
+        group_sync();
         tile(slot);
         --todo;
         const bool ends = cu.tile + 1 == cu.tiles;
         if (ends || todo == 0) {
-            const Walk done = cu;
+            const W done = cu;
             if (todo > 0) {
                 advance(cu, false);
-                load_q(cu);
+                ask_q(cu);
             }
             flush(done, slot, begun_here, ends);
             if (a.joined && todo == 0 && threadIdx.x == 0) {
-                // The item goes on in the next CTAs: the last of them holds its last tile.
                 Shared sh = {done.b, done.j, -1, -1};
                 if (begun_here && !ends) {
-                    const long long last = to + (done.tiles - done.tile - 1) - 1;
-                    long long k = last * G / total;
-                    while (total * (k + 1) / G <= last) ++k;
-                    while (total * k / G > last) --k;
-                    sh.first = blockIdx.x;
-                    sh.last = (int)k;
+                    // the item goes on in the next CTAs, to the one that has its last tile
+                    const int last = from + count - 1 + (done.tiles - done.tile - 1);
+                    sh.first = me;
+                    sh.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
                 }
                 reinterpret_cast<Shared*>(a.ws)[blockIdx.x] = sh;
             }
+            if (todo > 0) ready_q();
             clear();
             begun_here = true;
         } else {
             advance(cu, false);
         }
-        __syncwarp();
+        group_sync();
         if (left > 0) {
             copy(ld, slot, pid);
             if (--left > 0) {
@@ -609,30 +696,32 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const AttendArgs a) {
     }
 }
 
+constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * 32;
+
 // Joins the parts of the items that several CTAs share: CTA (c, column) those of the item that CTA c of the first launch has begun.
 template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, int cols) {
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int cols) {
     pdl_wait();
     pdl_trigger();
     const Shared sh = reinterpret_cast<const Shared*>(a.ws)[blockIdx.x];
     if (sh.first < 0) return;
     const int col = blockIdx.y, head = sh.j / a.chunks, q = (sh.j - head * a.chunks) * cols + col;
     if (q >= a.group) return;
-    __shared__ float s_m[kThreads], s_o[kWarps][DP + 1];
+    __shared__ float s_m[kJoinThreads], s_o[kJoinWarps][DP + 1];
     const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attend_header_bytes());
     const int n = sh.last - sh.first + 1, size = attend_part(cols, DP), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the first CTA's part is its second, the others' their first
     auto part = [&](int i) { return parts + (size_t)(2 * (sh.first + i) + (i == 0 ? 1 : 0)) * size; };
     float M = kNone;
-    for (int i = threadIdx.x; i < n; i += kThreads) M = fmaxf(M, part(i)[cols * DP + col]);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) M = fmaxf(M, part(i)[cols * DP + col]);
     s_m[threadIdx.x] = M;
     __syncthreads();
     M = kNone;
-    for (int i = 0; i < min(n, kThreads); ++i) M = fmaxf(M, s_m[i]);
+    for (int i = 0; i < min(n, kJoinThreads); ++i) M = fmaxf(M, s_m[i]);
     constexpr int kEach = DP / 32;
     float y[kEach] = {}, L = 0.0f;
 #pragma unroll 4
-    for (int i = warp; i < n; i += kWarps) {
+    for (int i = warp; i < n; i += kJoinWarps) {
         const float* p = part(i);
         const float f = ex2_approx(p[cols * DP + col] - M);
         L += f * p[cols * DP + cols + col];
@@ -647,7 +736,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     const int qh = head * a.group + q;
     float inv, lse;
     finish(a, sh.b, qh, M, L, inv, lse);
-    for (int d = threadIdx.x; d < a.c.D; d += kThreads) {
+    for (int d = threadIdx.x; d < a.c.D; d += kJoinThreads) {
         const float v = (s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv;
         const uint32_t r = DT == DT_BF16 ? f32x2_to_bf16x2(v, 0.0f) : f32x2_to_f16x2(v, 0.0f);
         a.out[((int64_t)sh.b * a.q.n + qh) * a.c.D + d] = (uint16_t)r;
@@ -655,42 +744,41 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)sh.b * a.q.n + qh] = lse;
 }
 
-template <int KIND, int DP, int NT>
+template <int KIND, int DP, int CG>
 cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t stream) {
-    using S = Shape<KIND, DP, NT>;
+    using S = Shape<KIND, DP, CG>;
     AttendArgs a = args;
     const int sms = dev.sms > 0 ? dev.sms : 152;
     // a window may begin anywhere in its first tile
     int64_t tiles = a.limit;
-    if (a.window > 0 && tiles > (int64_t)a.window + kAttendTile - 1) tiles = (int64_t)a.window + kAttendTile - 1;
-    tiles = tiles <= kAttendTile ? 1 : (tiles + kAttendTile - 1) / kAttendTile;
+    if (a.window > 0 && tiles > (int64_t)a.window + S::tokens - 1) tiles = (int64_t)a.window + S::tokens - 1;
+    tiles = tiles <= S::tokens ? 1 : (tiles + S::tokens - 1) / S::tokens;
     int64_t ctas = (int64_t)sms * S::ctas;
     if (ctas > kAttendCtas) ctas = kAttendCtas;
     if (ctas > (int64_t)a.B * a.items * tiles) ctas = (int64_t)a.B * a.items * tiles;
     // where no item has two tiles no two CTAs share one
     a.joined = tiles > 1;
-    cudaError_t e = launch_grid(attend_kernel<KIND, DP, NT>, dim3((unsigned)ctas), kThreads, S::smem, 1, dev.id, a, stream);
+    cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG>, dim3((unsigned)ctas), S::threads, S::smem, 1, dev.id, a, stream);
     if (e != cudaSuccess || !a.joined) return e;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.group < NT * 8 ? a.group : NT * 8));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.group < CG * 8 ? a.group : CG * 8));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<kDt, DP>, a, NT * 8);
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<kDt, DP>, a, CG * 8);
 }
 
 template <int KIND>
 cudaError_t launch_kind(const Device& dev, const AttendArgs& a, cudaStream_t stream) {
-    const int DP = attend_padded(a.c.D);
-    const bool one = attend_columns(a.group) == 8;
-    if (DP == 64) return one ? launch<KIND, 64, 1>(dev, a, stream) : launch<KIND, 64, 2>(dev, a, stream);
-    if (DP == 128) return one ? launch<KIND, 128, 1>(dev, a, stream) : launch<KIND, 128, 2>(dev, a, stream);
-    return one ? launch<KIND, 256, 1>(dev, a, stream) : launch<KIND, 256, 2>(dev, a, stream);
+    const int DP = attend_padded(a.c.D), cols = attend_columns(a.group, DP);
+    if (DP == 64) return cols == 8 ? launch<KIND, 64, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 64, 2>(dev, a, stream) : launch<KIND, 64, 4>(dev, a, stream);
+    if (DP == 128) return cols == 8 ? launch<KIND, 128, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 128, 2>(dev, a, stream) : launch<KIND, 128, 4>(dev, a, stream);
+    return cols == 8 ? launch<KIND, 256, 1>(dev, a, stream) : launch<KIND, 256, 2>(dev, a, stream);
 }
 
 cudaError_t launch_bf16(const Device& dev, const AttendArgs& a, cudaStream_t stream);

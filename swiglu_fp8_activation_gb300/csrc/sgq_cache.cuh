@@ -98,10 +98,10 @@ struct AttendArgs {
 
 // Most CTAs that one paged_attention runs, for which its workspace has room.
 constexpr int kAttendCtas = 512;
-constexpr int kAttendTile = 64;      // tokens a CTA takes at a time
+constexpr int kAttendTile = 64;      // tokens of a tile at least
 
 // Columns (heads of q) a CTA takes at once.
-constexpr int attend_columns(int group) { return group <= 8 ? 8 : 16; }
+constexpr int attend_columns(int group, int DP) { return group <= 8 ? 8 : group <= 16 || DP > 128 ? 16 : 32; }
 constexpr int attend_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }

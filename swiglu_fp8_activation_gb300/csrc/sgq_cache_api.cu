@@ -151,7 +151,7 @@ int64_t attend_ctas(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t wid
     if (B < 1 || B > SGQ_MAX_SEQUENCES || heads < 1 || heads > SGQ_MAX_HEADS || Hq < heads || Hq > SGQ_MAX_HEADS || Hq % heads != 0 || D < 1 ||
         D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size)
         return 0;
-    const int64_t cols = attend_columns((int)(Hq / heads)), chunks = (Hq / heads + cols - 1) / cols;
+    const int64_t cols = attend_columns((int)(Hq / heads), attend_padded((int)D)), chunks = (Hq / heads + cols - 1) / cols;
     const int64_t tiles = (width * page_size + kAttendTile - 1) / kAttendTile;
     *part = attend_part((int)cols, attend_padded((int)D));
     if (tiles <= 1) return 0;
@@ -302,8 +302,10 @@ int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* ca
     a.window = (int)(window > a.limit ? 0 : window);     // a window over all tokens is none
     a.B = (int)B;
     a.group = (int)(q->heads / cache->heads);
-    a.chunks = (a.group + attend_columns(a.group) - 1) / attend_columns(a.group);
+    const int cols = attend_columns(a.group, attend_padded((int)cache->D));
+    a.chunks = (a.group + cols - 1) / cols;
     a.items = (int)cache->heads * a.chunks;
+    if ((int64_t)a.B * a.items * ((a.limit + kAttendTile - 1) / kAttendTile + 1) > 0x7FFFFFFF) return SGQ_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
     return launched(launch_attend(fmt_of(fmt), dt_of(flags), current_device(), a, static_cast<cudaStream_t>(stream)));
 }
 
