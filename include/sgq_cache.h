@@ -187,7 +187,7 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  *   q             [B, Hq, D], read; Hq = q->heads a multiple of cache->heads
  *   pages         [B, width] int32, read
  *   width         pages a sequence, >= 0; width * page_size < 2^31, and B * Hq *
- *                 (width * page_size / 64 + 2) < 2^31
+ *                 (width * page_size / 64 + 1) < 2^31
  *   lengths       [B] int32, read
  *   scale         finite
  *   window        >= 0; 0 for none
@@ -203,8 +203,9 @@ int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* ca
                     const int32_t* pages, int64_t width, const int32_t* lengths, float scale, int64_t window,
                     const float* sinks, void* out, float* lse, void* workspace, sgq_stream_t stream);
 
-/* Bytes of paged_attention's workspace; 0 where it needs none, or an argument is outside its range. */
-int64_t sgq_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size);
+/* Bytes of paged_attention's workspace; 0 where it needs none (one launch), or an argument is outside its range. */
+int64_t sgq_attention_workspace_bytes(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width,
+                                      int64_t page_size, int64_t window);
 
 #ifdef __cplusplus
 }

@@ -18,12 +18,14 @@ is page * page_size + its place in the page.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
+import struct
 
 import torch
 
 from .binding import F_FP16, SgqError, _act_dtype, _check, library
-from .grouped import _at, _here, _need, _there
+from .grouped import _here, _need, _there
 
 F_ROPE_INTERLEAVED, F_ROPE_INVERSE = 64, 128
 MAX_HEAD = 256
@@ -53,24 +55,29 @@ class Rope(C.Structure):
     _fields_ = [("R", C.c_int64), ("freqs", C.c_void_p), ("positions", C.c_void_p), ("position_bytes", C.c_int), ("factor", C.c_float)]
 
 
+# The same as bytes: a third of the time of filling a ctypes structure.
+_heads_bytes = struct.Struct("@P3q").pack
+_cache_bytes = struct.Struct("@7q4P").pack
+_rope_bytes = struct.Struct("@q2Pif").pack
+
+
 def _lib() -> C.CDLL:
     global _bound
     L = library()
     if _bound is not L:
         vp, i64, u32, i32 = C.c_void_p, C.c_int64, C.c_uint32, C.c_int
-        heads, cache, turn = C.POINTER(Heads), C.POINTER(KvCache), C.POINTER(Rope)
         L.rope.restype = i32
-        L.rope.argtypes = [u32, i64, i64, turn, heads, heads, vp]
+        L.rope.argtypes = [u32, i64, i64, vp, vp, vp, vp]
         L.cache_write.restype = i32
-        L.cache_write.argtypes = [i32, u32, i64, cache, turn, heads, heads, heads, heads, vp, i32, vp]
+        L.cache_write.argtypes = [i32, u32, i64, vp, vp, vp, vp, vp, vp, vp, i32, vp]
         L.cache_read.restype = i32
-        L.cache_read.argtypes = [i32, u32, i64, cache, vp, i32, vp, vp, vp]
+        L.cache_read.argtypes = [i32, u32, i64, vp, vp, i32, vp, vp, vp]
         L.paged_attention.restype = i32
-        L.paged_attention.argtypes = [i32, u32, i64, cache, heads, vp, i64, vp, C.c_float, i64, vp, vp, vp, vp, vp]
+        L.paged_attention.argtypes = [i32, u32, i64, vp, vp, vp, i64, vp, C.c_float, i64, vp, vp, vp, vp, vp]
         L.sgq_attention_workspace_bytes.restype = i64
-        L.sgq_attention_workspace_bytes.argtypes = [i64] * 6
+        L.sgq_attention_workspace_bytes.argtypes = [i32] + [i64] * 7
         _bound = L
-    return _bound
+    return L
 
 
 def rope_turns(radians, device="cuda") -> torch.Tensor:
@@ -118,50 +125,57 @@ def rope_frequencies(R: int, base: float = 10000.0, *, scaling: str | None = Non
     return rope_turns(inv, device), factor
 
 
-def _heads(t: torch.Tensor, dtype, name: str, shape=None) -> Heads:
-    if t.dim() != 3 or t.dtype != dtype or (shape is not None and t.shape != shape):
-        raise SgqError(f"{name}: expected {dtype} {'[T, heads, D]' if shape is None else tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _heads(t: torch.Tensor, dtype, name: str, shape) -> bytes:
+    """sgq_heads_t of t, which has to have this shape [T, heads, D]."""
+    if t.dtype is not dtype or t.shape != shape or len(shape) != 3:
+        raise SgqError(f"{name}: expected {dtype} {tuple(shape) if len(shape) == 3 else '[T, heads, D]'}, got {t.dtype} {tuple(t.shape)}")
     ts, hs, one = t.stride()
-    if one != 1 and t.shape[2] > 1:
+    if one != 1 and shape[2] > 1:
         raise SgqError(f"{name}: the values of a head have to lie side by side")
-    return Heads(t.data_ptr(), t.shape[1], ts, hs)
+    return _heads_bytes(t.data_ptr(), shape[1], ts, hs)
 
 
-def _cache(k: torch.Tensor, v: torch.Tensor, fmt: str, k_scale, v_scale, dtype) -> KvCache:
-    if fmt not in CACHE_FORMATS:
+def _cache(k: torch.Tensor, v: torch.Tensor, fmt: str, k_scale, v_scale, dtype):
+    """(sgq_kv_cache_t of the caches, their shape, the format's code)."""
+    code = CACHE_FORMATS.get(fmt)
+    if code is None:
         raise SgqError(f"unknown cache format {fmt!r}")
-    want = dtype if fmt == "none" else torch.uint8
-    shape = k.shape
-    if k.dim() != 4 or k.dtype != want or v.dtype != want or v.shape != shape:
+    want = dtype if code == 3 else torch.uint8
+    shape, strides = k.shape, k.stride()
+    if k.dtype is not want or v.dtype is not want or len(shape) != 4 or v.shape != shape:
         raise SgqError(f"{fmt}: expected two {want} caches [pages, heads, page_size, D], got {k.dtype} {tuple(shape)}, {v.dtype} {tuple(v.shape)}")
-    strides = k.stride()
     if strides != v.stride() or strides[3] != 1:
         raise SgqError(f"the caches have to share their strides, the last one 1: got {strides}, {v.stride()}")
-    if fmt == "none":
+    if code == 3:
         if k_scale is not None or v_scale is not None:
             raise SgqError("k_scale, v_scale: of no use with format 'none'")
-        return KvCache(shape[0], shape[2], shape[1], shape[3], strides[0], strides[1], strides[2], k.data_ptr(), v.data_ptr(), None, None)
-    if k_scale is None or v_scale is None:
-        raise SgqError(f"k_scale, v_scale: missing with format {fmt!r}")
-    _need(k_scale, shape[:3], torch.float32, "k_scale")
-    _need(v_scale, shape[:3], torch.float32, "v_scale")
-    return KvCache(shape[0], shape[2], shape[1], shape[3], strides[0], strides[1], strides[2], k.data_ptr(), v.data_ptr(),
-                   k_scale.data_ptr(), v_scale.data_ptr())
+        ks = vs = 0
+    else:
+        if k_scale is None or v_scale is None:
+            raise SgqError(f"k_scale, v_scale: missing with format {fmt!r}")
+        _need(k_scale, shape[:3], torch.float32, "k_scale")
+        _need(v_scale, shape[:3], torch.float32, "v_scale")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    return (_cache_bytes(shape[0], shape[2], shape[1], shape[3], strides[0], strides[1], strides[2], k.data_ptr(), v.data_ptr(), ks, vs),
+            shape, code)
 
 
 def _index(t: torch.Tensor, n: int, name: str) -> int:
-    if t.dtype not in (torch.int32, torch.int64) or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    """Bytes of an index of n int32 or int64."""
+    dt = t.dtype
+    if (dt is not torch.int64 and dt is not torch.int32) or t.shape != (n,) or not t.is_contiguous():
         raise SgqError(f"{name}: expected contiguous int32 or int64 [{n}], got {t.dtype} {tuple(t.shape)}")
-    return t.element_size()
+    return 8 if dt is torch.int64 else 4
 
 
 def _turn(freqs: torch.Tensor, positions: torch.Tensor, T: int, layout: str, factor: float):
-    if layout not in ROPE_LAYOUTS:
+    """(sgq_rope_t, the layout's flag)."""
+    flag = ROPE_LAYOUTS.get(layout)
+    if flag is None:
         raise SgqError(f"unknown order of pairs {layout!r}")
-    if freqs.dim() != 1:
-        raise SgqError(f"freqs: expected [R / 2], got {tuple(freqs.shape)}")
-    _need(freqs, freqs.shape, torch.int64, "freqs")
-    return Rope(2 * freqs.shape[0], freqs.data_ptr(), positions.data_ptr(), _index(positions, T, "positions"), factor), ROPE_LAYOUTS[layout]
+    if freqs.dim() != 1 or freqs.dtype is not torch.int64 or not freqs.is_contiguous():
+        raise SgqError(f"freqs: expected contiguous int64 [R / 2], got {freqs.dtype} {tuple(freqs.shape)}")
+    return _rope_bytes(2 * len(freqs), freqs.data_ptr(), positions.data_ptr(), _index(positions, T, "positions"), factor), flag
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, layout: str = "half", factor: float = 1.0,
@@ -176,18 +190,21 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, layou
     passed on. inverse=True turns the other way: the gradient. Returns out
     [T, heads, D] of x's type, contiguous where it is not given; out=x rotates in place.
     """
-    dt = _act_dtype(x, "x")
-    src = _heads(x, dt, "x")
-    T, _, D = x.shape
+    dt, shape = _act_dtype(x, "x"), x.shape
+    src = _heads(x, dt, "x", shape)
+    T, _, D = shape
     turn, flags = _turn(freqs, positions, T, layout, factor)
     at = _here(stream, "rope", x, positions, freqs, out)
     if at is None:
         with _there(stream, x):
             return rope(x, positions, freqs, layout=layout, factor=factor, inverse=inverse, out=out)
     if out is None:
-        out = torch.empty(x.shape, dtype=dt, device=x.device)
-    flags |= (F_ROPE_INVERSE if inverse else 0) | (F_FP16 if dt == torch.float16 else 0)
-    st = _lib().rope(flags, T, D, C.byref(turn), C.byref(src), C.byref(_heads(out, dt, "out", x.shape)), at)
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    if inverse:
+        flags |= F_ROPE_INVERSE
+    if dt is torch.float16:
+        flags |= F_FP16
+    st = _lib().rope(flags, T, D, turn, src, _heads(out, dt, "out", shape), at)
     if st:
         _check(st, "rope")
     return out
@@ -209,18 +226,21 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     (allocated where it is not given; q itself to rotate in place), or None without q.
     """
     dt = _act_dtype(k, "k")
-    ck = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
-    T = k.shape[0]
-    shape = (T, ck.heads, ck.D)
+    ck, laid, code = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
+    T, D = k.shape[0], laid[3]
+    shape = (T, laid[1], D)
     hk, hv = _heads(k, dt, "k", shape), _heads(v, dt, "v", shape)
     slot_bytes = _index(slots, T, "slots")
-    if (positions is None) != (freqs is None):
+    turn, flags, hq = None, 0, None
+    if positions is not None and freqs is not None:
+        turn, flags = _turn(freqs, positions, T, layout, factor)
+    elif positions is not None or freqs is not None:
         raise SgqError("positions and freqs go together")
-    turn, flags = (None, 0) if freqs is None else _turn(freqs, positions, T, layout, factor)
     if q is not None:
         if turn is None:
             raise SgqError("q: of no use without positions")
-        hq = _heads(q, dt, "q", (T, q.shape[1], ck.D) if q.dim() == 3 else shape)
+        qshape = q.shape
+        hq = _heads(q, dt, "q", (T, qshape[1], D) if len(qshape) == 3 else (T, 1, D))
     elif q_out is not None:
         raise SgqError("q_out: of no use without q")
     at = _here(stream, "cache_write", k, v, k_cache, v_cache, slots, k_scale, v_scale, q, q_out, positions, freqs)
@@ -228,12 +248,14 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
         with _there(stream, k):
             return cache_write(k, v, k_cache, v_cache, slots, fmt=fmt, k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
                                positions=positions, freqs=freqs, layout=layout, factor=factor)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    flags |= F_FP16 if dt == torch.float16 else 0
-    st = _lib().cache_write(CACHE_FORMATS[fmt], flags, T, C.byref(ck), None if turn is None else C.byref(turn),
-                            None if q is None else C.byref(hq), None if q is None else C.byref(_heads(q_out, dt, "q_out", q.shape)),
-                            C.byref(hk), C.byref(hv), slots.data_ptr(), slot_bytes, at)
+    ho = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=dt, device=q.device)
+        ho = _heads(q_out, dt, "q_out", qshape)
+    if dt is torch.float16:
+        flags |= F_FP16
+    st = _lib().cache_write(code, flags, T, ck, turn, hq, ho, hk, hv, slots.data_ptr(), slot_bytes, at)
     if st:
         _check(st, "cache_write")
     return q_out
@@ -250,12 +272,12 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor
     """
     own = k_cache.dtype if fmt == "none" else None
     dt = dtype or own or (k_out.dtype if k_out is not None else torch.bfloat16)
-    if dt not in (torch.bfloat16, torch.float16) or (own is not None and dt != own):
+    if (dt is not torch.bfloat16 and dt is not torch.float16) or (own is not None and dt is not own):
         raise SgqError(f"rows of a {k_cache.dtype} cache as {dt}")
-    ck = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
+    ck, laid, code = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
     S = slots.shape[0] if slots.dim() == 1 else -1
     slot_bytes = _index(slots, S, "slots")
-    shape = (S, ck.heads, ck.D)
+    shape = (S, laid[1], laid[3])
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is not None:
             _need(t, shape, dt, name)
@@ -267,16 +289,23 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor
         k_out = torch.empty(shape, dtype=dt, device=k_cache.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dt, device=k_cache.device)
-    st = _lib().cache_read(CACHE_FORMATS[fmt], F_FP16 if dt == torch.float16 else 0, S, C.byref(ck), slots.data_ptr(), slot_bytes,
+    st = _lib().cache_read(code, F_FP16 if dt is torch.float16 else 0, S, ck, slots.data_ptr(), slot_bytes,
                            k_out.data_ptr(), v_out.data_ptr(), at)
     if st:
         _check(st, "cache_read")
     return k_out, v_out
 
 
-def attention_workspace_bytes(B: int, Hq: int, heads: int, D: int, width: int, page_size: int) -> int:
+@functools.lru_cache(maxsize=1024)
+def _workspace(lib, *sizes) -> int:
+    return lib.sgq_attention_workspace_bytes(*sizes)
+
+
+def attention_workspace_bytes(fmt: str, B: int, Hq: int, heads: int, D: int, width: int, page_size: int, window: int = 0) -> int:
     """Bytes of paged_attention's workspace (0 where it needs none, or out of range)."""
-    return _lib().sgq_attention_workspace_bytes(B, Hq, heads, D, width, page_size)
+    if fmt not in CACHE_FORMATS:
+        raise SgqError(f"unknown cache format {fmt!r}")
+    return _workspace(_lib(), CACHE_FORMATS[fmt], B, Hq, heads, D, width, page_size, window)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor, *,
@@ -295,40 +324,44 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     tokens (0: all). sinks [Hq] float32: a logit a head that joins the softmax without a
     value. Returns out [B, Hq, D], zeros where a sequence has no token; with
     lse=True, or a float32 [B, Hq] to write, (out, the log of the softmax's sum).
-    workspace: uint8 [attention_workspace_bytes(B, Hq, heads, D, width, page_size)] or
-    None (allocated where one is needed).
+    workspace: uint8 [attention_workspace_bytes(fmt, B, Hq, heads, D, width, page_size,
+    window)] or None (allocated where one is needed).
     """
-    dt = _act_dtype(q, "q")
-    ck = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
-    B, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
-    hq = _heads(q, dt, "q", (B, Hq, ck.D))
+    dt, shape = _act_dtype(q, "q"), q.shape
+    ck, laid, code = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
+    _, heads, page_size, D = laid
+    B, Hq, _ = shape if len(shape) == 3 else (0, 0, 0)
+    hq = _heads(q, dt, "q", (B, Hq, D))
     width = pages.shape[1] if pages.dim() == 2 else 0
     _need(pages, (B, width), torch.int32, "pages")
     _need(lengths, (B,), torch.int32, "lengths")
     if sinks is not None:
         _need(sinks, (Hq,), torch.float32, "sinks")
     if out is not None:
-        _need(out, (B, Hq, D), dt, "out")
-    room = _lib().sgq_attention_workspace_bytes(B, Hq, ck.heads, D, width, ck.page_size)
+        _need(out, shape, dt, "out")
+    L = _lib()
+    room = _workspace(L, code, B, Hq, heads, D, width, page_size, window)
     if workspace is not None:
         _need(workspace, (room,), torch.uint8, "workspace")
-    told = None if isinstance(lse, bool) else lse
-    if told is not None:
+    told = None
+    if lse is not False and lse is not True:
+        told = lse
         _need(told, (B, Hq), torch.float32, "lse")
     at = _here(stream, "paged_attention", q, k_cache, v_cache, pages, lengths, k_scale, v_scale, sinks, out, told, workspace)
     if at is None:
         with _there(stream, q):
             return paged_attention(q, k_cache, v_cache, pages, lengths, fmt=fmt, k_scale=k_scale, v_scale=v_scale, scale=scale,
                                    window=window, sinks=sinks, out=out, lse=lse, workspace=workspace)
+    device = q.device
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=dt, device=q.device)
+        out = torch.empty(shape, dtype=dt, device=device)
     if lse is True:
-        told = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        told = torch.empty((B, Hq), dtype=torch.float32, device=device)
     if workspace is None and room:
-        workspace = torch.empty((room,), dtype=torch.uint8, device=q.device)
-    st = _lib().paged_attention(CACHE_FORMATS[fmt], F_FP16 if dt == torch.float16 else 0, B, C.byref(ck), C.byref(hq), pages.data_ptr(),
-                                width, lengths.data_ptr(), D ** -0.5 if scale is None else scale, window, _at(sinks), out.data_ptr(),
-                                _at(told), _at(workspace), at)
+        workspace = torch.empty((room,), dtype=torch.uint8, device=device)
+    st = L.paged_attention(code, F_FP16 if dt is torch.float16 else 0, B, ck, hq, pages.data_ptr(), width, lengths.data_ptr(),
+                           D ** -0.5 if scale is None else scale, window, None if sinks is None else sinks.data_ptr(), out.data_ptr(),
+                           None if told is None else told.data_ptr(), None if workspace is None else workspace.data_ptr(), at)
     if st:
         _check(st, "paged_attention")
     return out if told is None else (out, told)

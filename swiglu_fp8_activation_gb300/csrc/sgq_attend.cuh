@@ -44,36 +44,42 @@ constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's sc
 // Kinds of rows and queries.
 enum Kind : int { BF16 = 0, F16 = 1, FP8_BF16 = 2, FP8_F16 = 3 };
 
-// CG: groups of 8 columns, a warp of each group of warps for each.
-template <int KIND, int DP, int CG>
+// CG: groups of 8 columns, a warp of each group of warps for each. DIRECT: see attend_kernel.
+template <int KIND, int DP, int CG, bool DIRECT>
 struct Shape {
     static constexpr bool fp8 = KIND >= FP8_BF16;
-#ifndef ATT_H
-#define ATT_H 2
-#endif
-#ifndef ATT_C16
-#define ATT_C16 2
-#endif
-#ifndef ATT_C8
-#define ATT_C8 2
-#endif
     static constexpr int warps = kParts * CG, threads = warps * 32;
-    static constexpr int halves = fp8 ? ATT_H : 1;               // 16 tokens each, of those that a warp takes at a time
-    static constexpr int rows = 16 * halves;
+    static constexpr int tokens = attend_tokens(fp8);            // of a tile
+    static constexpr int rows = tokens / kParts;                 // that a warp takes at a time, 16 of them a product
+    static constexpr int halves = rows / 16;
     static constexpr uint32_t full = rows == 32 ? 0xFFFFFFFFu : 0xFFFFu;         // the mask of rows that are all there
-    static constexpr int tokens = kParts * rows;                 // of a tile
     static constexpr int elem = fp8 ? 1 : 2;
     static constexpr int pieces = DP * elem / 16;                // 16-byte pieces of a row
-    static constexpr int stride = DP * elem + 16;                // of rows in shared memory: 8 rows' pieces meet no bank twice
+    // Rows in shared memory: 8 rows' pieces meet no bank twice, by 16 bytes between rows or, E4M3 rows of 128 and 256, by the
+    // pieces' order (see piece_at).
+    static constexpr bool swizzled = fp8 && DP >= 128;
+    static constexpr int stride = DP * elem + (swizzled ? 0 : 16);
     static constexpr int slot = 2 * rows * stride + (fp8 ? 2 * rows * 4 : 0);
-    static constexpr int ctas = DP == 256 ? (CG == 1 ? 2 : 1) : CG == 1 ? (fp8 ? ATT_C8 : ATT_C16) : CG == 2 ? 2 : 1;   // a multiprocessor
-    static constexpr int fit = (227 * 1024 / ctas - 4096) / (slot * kParts);
+#ifndef ATT_D64
+#define ATT_D64 3
+#endif
+#ifndef ATT_D8
+#define ATT_D8 3
+#endif
+#ifndef ATT_S8
+#define ATT_S8 2
+#endif
+    static constexpr int ctas = DP == 256 ? (CG == 1 ? 2 : 1) : CG == 1 ? (DIRECT ? (DP == 64 ? ATT_D64 : fp8 ? ATT_D8 : 3) : fp8 ? ATT_S8 : 2) : CG == 2 ? 2 : 1;   // a multiprocessor
+    static constexpr int fit = (227 * 1024 / ctas - 3072) / (slot * kParts);
     static constexpr int stages = fit < 2 ? 2 : fit > 8 ? 8 : fit;
     static constexpr int smem = stages * slot * kParts;
     static constexpr int parts = KIND == FP8_BF16 ? 1 : 2;       // 16-bit parts of p
     static constexpr int line = (DP + 4) * 4;                    // bytes of a column's sums: 4 lanes' columns meet no bank twice
     static constexpr int at_once = slot / (8 * line) < CG ? slot / (8 * line) : CG;      // groups of columns whose sums pass through a slot
     static_assert(at_once >= 1 && CG % at_once == 0 && smem <= 227 * 1024 - 2048, "");
+    // Where piece p of row r lies, from the row's beginning. E4M3: a quarter of a warp reads 4 pieces of rows r, r + 1 (k), or 2 pieces of
+    // rows r, r + 2, r + 4, r + 6 (v).
+    static __device__ __forceinline__ int piece_at(int r, int p) { return (swizzled ? p ^ ((r & 6) ^ ((r & 1) << 2)) : p) * 16; }
 };
 
 template <bool BF>
@@ -120,6 +126,10 @@ __device__ __forceinline__ float lds_f32(uint32_t at) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void sts16(uint32_t at, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 __device__ __forceinline__ void sts_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
@@ -176,9 +186,36 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int b, int head, flo
     lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <int KIND, int DP, int CG>
-__global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, CG>::ctas) attend_kernel(const AttendArgs a) {
-    using S = Shape<KIND, DP, CG>;
+// Four values, times f, to 16 bits.
+template <int DT>
+__device__ __forceinline__ void store4(uint16_t* to, float4 y, float f) {
+    *reinterpret_cast<uint2*>(to) = DT == DT_BF16 ? make_uint2(f32x2_to_bf16x2(y.x * f, y.y * f), f32x2_to_bf16x2(y.z * f, y.w * f))
+                                                  : make_uint2(f32x2_to_f16x2(y.x * f, y.y * f), f32x2_to_f16x2(y.z * f, y.w * f));
+}
+
+// Stores of one CTA of a cluster, read by another.
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster16(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_cluster4(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// DIRECT: a cluster of a.split CTAs takes one item, each an equal run of its tiles. Else CTAs take shares of all tiles.
+template <int KIND, int DP, int CG, bool DIRECT>
+__global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KIND, DP, CG, DIRECT>::ctas) attend_kernel(const AttendArgs a) {
+    using S = Shape<KIND, DP, CG, DIRECT>;
     constexpr bool kF8 = S::fp8, kBf = KIND == BF16;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     constexpr int kSteps = DP / 16, kCols = CG * 8, kThreads = S::threads;
@@ -197,66 +234,76 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
     pdl_wait();
     pdl_trigger();
 
-    // The CTA's share of all tiles, and where it begins: each thread sums the tiles of a run of sequences.
     using W = Walk<S::tokens>;
-    auto tiles_of = [&](int length) {
-        W w;
-        w.enter(a, 0, length);
-        return w.tiles * a.items;
-    };
-    const int run = (a.B + kThreads - 1) / kThreads, b_from = min((int)threadIdx.x * run, a.B), b_to = min(b_from + run, a.B);
-    int mine = 0;
-    for (int b = b_from; b < b_to; ++b) mine += tiles_of(a.lengths[b]);
-    int before = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
-        if (lane >= d) before += o;
-    }
-    if (lane == 31) sum_part[warp] = before;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < S::warps; ++w) {
-        if (w < warp) before += sum_part[w];
-        total += sum_part[w];
-    }
-    before -= mine;
-    // With fewer tiles than CTAs the last ones have none: no CTA between two that share an item is without a tile.
-    const int G = min((int)gridDim.x, total), me = (int)blockIdx.x;
-    const int each = total / G, more = total - each * G;         // the first `more` CTAs take one tile more
-    const int from = me * each + min(me, more), count = me >= G ? 0 : each + (me < more ? 1 : 0);
-    if (count > 0 && from >= before && from < before + mine) {
-        int at = before;
-        for (int b = b_from; b < b_to; ++b) {
-            const int n = a.lengths[b], next = at + tiles_of(n);
-            if (from < next) {
-                share_b = b;
-                share_n = n;
-                share_off = from - at;
-                break;
-            }
-            at = next;
-        }
-    }
-    __syncthreads();
-    if (count == 0) {
-        if (a.joined && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
-        return;
-    }
-
     W ld;
-    ld.enter(a, share_b, share_n);
-    ld.j = share_off / ld.tiles;
-    ld.tile = share_off - ld.j * ld.tiles;
-    ld.head = ld.j / a.chunks;
+    int total = 0, G = 1, each = 0, more = 0, from = 0, count = 0, next_n = 0;
+    const int me = (int)blockIdx.x;
+    if (DIRECT) {
+        const int rank = a.split > 1 ? (int)cluster_rank() : 0, item = me / a.split, b = item / a.items;
+        ld.enter(a, b, a.lengths[b]);
+        ld.j = item - b * a.items;
+        from = ld.tile = ld.tiles * rank / a.split;
+        count = ld.tiles * (rank + 1) / a.split - from;
+    } else {
+        // The CTA's share of all tiles, and where it begins: each thread sums the tiles of a run of sequences.
+        auto tiles_of = [&](int length) {
+            W w;
+            w.enter(a, 0, length);
+            return w.tiles * a.items;
+        };
+        const int run = (a.B + kThreads - 1) / kThreads, b_from = min((int)threadIdx.x * run, a.B), b_to = min(b_from + run, a.B);
+        int mine = 0;
+        for (int b = b_from; b < b_to; ++b) mine += tiles_of(a.lengths[b]);
+        int before = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= d) before += o;
+        }
+        if (lane == 31) sum_part[warp] = before;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < S::warps; ++w) {
+            if (w < warp) before += sum_part[w];
+            total += sum_part[w];
+        }
+        before -= mine;
+        // With fewer tiles than CTAs the last ones have none: no CTA between two that share an item is without a tile.
+        G = min((int)gridDim.x, total);
+        each = total / G;
+        more = total - each * G;         // the first `more` CTAs take one tile more
+        from = me * each + min(me, more);
+        count = me >= G ? 0 : each + (me < more ? 1 : 0);
+        if (count > 0 && from >= before && from < before + mine) {
+            int at = before;
+            for (int b = b_from; b < b_to; ++b) {
+                const int n = a.lengths[b], next = at + tiles_of(n);
+                if (from < next) {
+                    share_b = b;
+                    share_n = n;
+                    share_off = from - at;
+                    break;
+                }
+                at = next;
+            }
+        }
+        __syncthreads();
+        if (count == 0) {
+            if (a.joined && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
+            return;
+        }
+        ld.enter(a, share_b, share_n);
+        ld.j = share_off / ld.tiles;
+        ld.tile = share_off - ld.j * ld.tiles;
+        next_n = ld.b + 1 < a.B ? a.lengths[ld.b + 1] : 0;
+    }
+    ld.head = a.chunks > 1 ? ld.j / a.chunks : ld.j;
     ld.chunk = ld.j - ld.head * a.chunks;
     W cu = ld;
     int left = count;                                            // tiles to copy
-    int next_n = ld.b + 1 < a.B ? a.lengths[ld.b + 1] : 0;
 
     auto advance = [&](W& w, bool ahead) {
-        if (++w.tile < w.tiles) return;
+        if (++w.tile < w.tiles || DIRECT) return;
         w.tile = 0;
         if (++w.chunk == a.chunks) {
             w.chunk = 0;
@@ -278,7 +325,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
     constexpr int kRowsAt = 32 / S::pieces > 0 ? 32 / S::pieces : 1;              // rows that 32 lanes copy at once
     const int lane_row = kRowsAt > 1 ? lane / S::pieces : 0, piece = lane % S::pieces;
     const bool used = piece * 16 < a.c.D * S::elem;              // columns from D on are filled with zeros
-    const uint32_t lane_to = lane_row * S::stride + piece * 16;
+    const uint32_t lane_to = (lane_row + cg * kRowsAt) * S::stride;
+    const int lane_piece = S::piece_at(lane_row, piece) ^ S::piece_at(cg * kRowsAt, 0);      // turn i's: ^ piece_at(i * kRowsAt, 0)
     const int64_t lane_from = lane_row * a.c.ts + (used ? piece * 16 : 0), row_step = kRowsAt * a.c.ts;
     // the lane's token of w's tile (of 16 tokens both halves of a warp have the same)
     auto token_of = [&](const W& w) { return w.start + w.tile * S::tokens + part * S::rows + (lane & (S::rows - 1)); };
@@ -306,23 +354,25 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
             for (int h = 0; h < S::halves; ++h) {
                 const uint32_t some = (mask >> (16 * h)) & 0xFFFFu;
                 const uint8_t* k = a.c.k + ((S::halves > 1 ? __shfl_sync(0xFFFFFFFFu, off, 16 * h) : off) + lane_from + cg * row_step);
-                uint32_t to = at + h * 16 * S::stride + lane_to + cg * kRowsAt * S::stride;
+                uint32_t to = at + h * 16 * S::stride + lane_to;
                 if (some == 0xFFFFu) {
 #pragma unroll
                     for (int i = 0; i < kTurns; i += CG) {
                         if (kTurns % CG == 0 || i + cg < kTurns) {
-                            copy16(to, k, used);
-                            copy16(to + S::rows * S::stride, k + v_from_k, used);
+                            const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
+                            copy16(x, k, used);
+                            copy16(x + S::rows * S::stride, k + v_from_k, used);
                         }
                         k += CG * row_step;
                         to += CG * kRowsAt * S::stride;
                     }
                 } else {
 #pragma unroll 1
-                    for (int i = cg; i < kTurns; i += CG) {
-                        const bool ok = used && ((some >> (i * kRowsAt + lane_row)) & 1);
-                        copy16(to, ok ? k : a.c.k, ok);
-                        copy16(to + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
+                    for (int i = 0; i + cg < kTurns; i += CG) {
+                        const bool ok = used && ((some >> ((i + cg) * kRowsAt + lane_row)) & 1);
+                        const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
+                        copy16(x, ok ? k : a.c.k, ok);
+                        copy16(x + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
                         k += CG * row_step;
                         to += CG * kRowsAt * S::stride;
                     }
@@ -330,14 +380,15 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
             }
         } else {
             const int64_t off = there ? (int64_t)pid * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)place * a.c.ts : 0;
-            uint32_t to = at + lane_to + cg * kRowsAt * S::stride;
+            uint32_t to = at + lane_to;
 #pragma unroll 4
-            for (int i = cg; i < S::rows / kRowsAt; i += CG) {
-                const int row = i * kRowsAt + lane_row;
+            for (int i = 0; i + cg < S::rows / kRowsAt; i += CG) {
+                const int row = (i + cg) * kRowsAt + lane_row;
+                const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
                 const bool ok = used && ((mask >> row) & 1);
                 const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + (used ? piece * 16 : 0);
-                copy16(to, ok ? k : a.c.k, ok);
-                copy16(to + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
+                copy16(x, ok ? k : a.c.k, ok);
+                copy16(x + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
                 to += CG * kRowsAt * S::stride;
             }
         }
@@ -424,7 +475,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
                 const float k0 = lds_f32(sc + (h * 16 + g) * 4), k1 = lds_f32(sc + (h * 16 + g + 8) * 4);
 #pragma unroll
                 for (int blk = 0; blk < DP / 64; ++blk) {
-                    const uint32_t from = at + (h * 16 + g) * S::stride + blk * 64 + c * 16;
+                    const uint32_t from = at + (h * 16 + g) * S::stride + S::piece_at(g, blk * 4 + c);
                     const uint4 p = lds16(from), q = lds16(from + 8 * S::stride);
                     const uint32_t up[4] = {p.x, p.y, p.z, p.w}, dn[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -526,7 +577,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
                     uint32_t v[4][4];                            // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const uint32_t from = vt + (h * 16 + 2 * c + (t & 1) + (t >> 1) * 8) * S::stride + blk * 128 + g * kWords * 4;
+                        const int row = 2 * c + (t & 1);
+                        const uint32_t from = vt + (h * 16 + row + (t >> 1) * 8) * S::stride + (kWords == 4 ? S::piece_at(row, blk * 8 + g) : g * 8);
                         if (kWords == 4) {
                             const uint4 q = lds16(from);
                             v[t][0] = q.x, v[t][1] = q.y, v[t][2] = q.z, v[t][3] = q.w;
@@ -550,9 +602,14 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
         }
     };
 
+    // Where a CTA of a cluster leaves its sums of a column.
+    __shared__ float s_M[kCols], s_L[kCols];
+    auto part_at = [&](int col, int slot) {
+        return (uint32_t)__cvta_generic_to_shared(stages) + (uint32_t)((col >> 3) * S::stages * S::slot + slot * S::slot + (col & 7) * S::line);
+    };
     // Adds up what the warps have of the item at w and writes it: the result, or this CTA's part of it.
     auto flush = [&](const W& w, int slot, bool begun_here, bool ends_here) {
-        const bool whole = begun_here && ends_here;
+        const bool whole = DIRECT ? a.split == 1 : begun_here && ends_here;
         float* to_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attend_header_bytes()) +
                          (size_t)(2 * blockIdx.x + (begun_here ? 1 : 0)) * attend_part(kCols, DP);
 #pragma unroll
@@ -607,17 +664,19 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
                         y.z += __uint_as_float(u.z) * f[v];
                         y.w += __uint_as_float(u.w) * f[v];
                     }
-                    if (!whole) {
+                    if (!whole && DIRECT) {
+                        sts16(part_at(col, slot ^ 1) + d * 4, y);
+                    } else if (!whole) {
                         *reinterpret_cast<float4*>(to_part + col * DP + d) = y;
                     } else if (d < a.c.D) {
-                        uint16_t* to = a.out + ((int64_t)w.b * a.q.n + qh) * a.c.D + d;
-                        const uint2 v = kDt == DT_BF16 ? make_uint2(f32x2_to_bf16x2(y.x * inv, y.y * inv), f32x2_to_bf16x2(y.z * inv, y.w * inv))
-                                                       : make_uint2(f32x2_to_f16x2(y.x * inv, y.y * inv), f32x2_to_f16x2(y.z * inv, y.w * inv));
-                        *reinterpret_cast<uint2*>(to) = v;
+                        store4<kDt>(a.out + ((int64_t)w.b * a.q.n + qh) * a.c.D + d, y, inv);
                     }
                 }
                 if (threadIdx.x % kEach == 0) {
-                    if (!whole) {
+                    if (!whole && DIRECT) {
+                        s_M[col] = M;
+                        s_L[col] = L;
+                    } else if (!whole) {
                         to_part[kCols * DP + col] = M;
                         to_part[kCols * DP + kCols + col] = L;
                     } else if (a.lse) {
@@ -661,7 +720,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
         tile(slot);
         --todo;
         const bool ends = cu.tile + 1 == cu.tiles;
-        if (ends || todo == 0) {
+        if (!DIRECT && (ends || todo == 0)) {
             const W done = cu;
             if (todo > 0) {
                 advance(cu, false);
@@ -694,6 +753,40 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG>::threads, Shape<KIND, DP, 
         }
         cp_async_commit();
     }
+    if (!DIRECT) return;
+    cp_async_wait<0>();
+    __syncthreads();
+    flush(cu, 0, true, true);
+    if (a.split == 1) return;
+    // The cluster's CTAs each join some of the columns' values.
+    cluster_arrive();
+    cluster_wait();
+    constexpr int kEach = DP / 4;                                // of a column, 4 values each
+    for (int u = (int)cluster_rank() * kThreads + (int)threadIdx.x; u < kCols * kEach; u += a.split * kThreads) {
+        const int col = u / kEach, d = (u - col * kEach) * 4, q = cu.chunk * kCols + col;
+        if (q >= a.group) continue;
+        float M = kNone, L = 0.0f;
+        float4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t at_m = (uint32_t)__cvta_generic_to_shared(&s_M[col]), at_l = (uint32_t)__cvta_generic_to_shared(&s_L[col]), at = part_at(col, 1) + d * 4;
+        for (int r = 0; r < a.split; ++r) M = fmaxf(M, ld_cluster4(in_cta(at_m, r)));
+#pragma unroll 4
+        for (int r = 0; r < a.split; ++r) {
+            const float f = ex2_approx(ld_cluster4(in_cta(at_m, r)) - M);
+            const float4 v = ld_cluster16(in_cta(at, r));
+            L += f * ld_cluster4(in_cta(at_l, r));
+            y.x += f * v.x;
+            y.y += f * v.y;
+            y.z += f * v.z;
+            y.w += f * v.w;
+        }
+        const int qh = cu.head * a.group + q;
+        float inv, lse;
+        finish(a, cu.b, qh, M, L, inv, lse);
+        if (d < a.c.D) store4<kDt>(a.out + ((int64_t)cu.b * a.q.n + qh) * a.c.D + d, y, inv);
+        if (d == 0 && a.lse) a.lse[(int64_t)cu.b * a.q.n + qh] = lse;
+    }
+    cluster_arrive();                                            // no CTA leaves while another reads its sums
+    cluster_wait();
 }
 
 constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * 32;
@@ -746,21 +839,21 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
 
 template <int KIND, int DP, int CG>
 cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t stream) {
-    using S = Shape<KIND, DP, CG>;
-    AttendArgs a = args;
-    const int sms = dev.sms > 0 ? dev.sms : 152;
-    // a window may begin anywhere in its first tile
-    int64_t tiles = a.limit;
-    if (a.window > 0 && tiles > (int64_t)a.window + S::tokens - 1) tiles = (int64_t)a.window + S::tokens - 1;
-    tiles = tiles <= S::tokens ? 1 : (tiles + S::tokens - 1) / S::tokens;
-    int64_t ctas = (int64_t)sms * S::ctas;
-    if (ctas > kAttendCtas) ctas = kAttendCtas;
-    if (ctas > (int64_t)a.B * a.items * tiles) ctas = (int64_t)a.B * a.items * tiles;
-    // where no item has two tiles no two CTAs share one
-    a.joined = tiles > 1;
-    cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG>, dim3((unsigned)ctas), S::threads, S::smem, 1, dev.id, a, stream);
-    if (e != cudaSuccess || !a.joined) return e;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
+    AttendArgs a = args;
+    if (a.split > 0) {
+        using S = Shape<KIND, DP, CG, true>;
+        return launch_grid(attend_kernel<KIND, DP, CG, true>, dim3((unsigned)(a.B * a.items * a.split)), S::threads, S::smem, a.split, dev.id, a, stream);
+    }
+    using S = Shape<KIND, DP, CG, false>;
+    int64_t ctas = (int64_t)(dev.sms > 0 ? dev.sms : 152) * S::ctas;
+    if (ctas > kAttendCtas) ctas = kAttendCtas;
+    const int64_t most = (int64_t)a.B * a.items * a.tiles;
+    if (ctas > most) ctas = most;
+    // where no item has two tiles no two CTAs share one
+    a.joined = a.tiles > 1;
+    const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, false>, dim3((unsigned)ctas), S::threads, S::smem, 1, dev.id, a, stream);
+    if (e != cudaSuccess || !a.joined) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.group < CG * 8 ? a.group : CG * 8));
     cfg.blockDim = dim3(kJoinThreads);

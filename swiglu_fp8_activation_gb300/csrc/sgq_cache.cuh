@@ -94,15 +94,33 @@ struct AttendArgs {
     int chunks;          // column chunks a head of the cache
     int items;           // heads * chunks a sequence
     int joined;          // whether a second launch joins what several CTAs have computed
+    int split;           // CTAs of a cluster, where each takes one item; 0 for shares
+    int tiles;           // of the longest item
 };
 
-// Most CTAs that one paged_attention runs, for which its workspace has room.
+// Most CTAs that take shares of one paged_attention, for which its workspace has room.
 constexpr int kAttendCtas = 512;
-constexpr int kAttendTile = 64;      // tokens of a tile at least
 
 // Columns (heads of q) a CTA takes at once.
 constexpr int attend_columns(int group, int DP) { return group <= 8 ? 8 : group <= 16 || DP > 128 ? 16 : 32; }
 constexpr int attend_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// Tokens of a tile.
+__host__ __device__ constexpr int attend_tokens(bool fp8) { return fp8 ? 128 : 64; }
+// Tiles of the longest item; a window may begin anywhere in its first tile.
+constexpr int64_t attend_tiles(bool fp8, int64_t limit, int64_t window) {
+    const int tokens = attend_tokens(fp8);
+    if (window > 0 && limit > window + tokens - 1) limit = window + tokens - 1;
+    return limit <= tokens ? 1 : (limit + tokens - 1) / tokens;
+}
+// CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles.
+#ifndef ATT_PER
+#define ATT_PER 16
+#endif
+constexpr int attend_split(int64_t items, int64_t tiles) {
+    int split = 1;
+    while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * ATT_PER)) split *= 2;
+    return tiles <= split * ATT_PER && items * split <= 0x7FFFFFFF ? split : 0;
+}
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }
 

@@ -146,17 +146,23 @@ int dt_of(uint32_t flags) { return (flags & SGQ_F_FP16) ? DT_F16 : DT_BF16; }
 
 int fmt_of(int fmt) { return fmt == SGQ_FMT_FP8_PER_TOKEN ? (int)FMT_PT : FMT_16BIT; }
 
-// CTAs of paged_attention at most, and floats of each of their two parts; 0 CTAs out of range.
-int64_t attend_ctas(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size, int64_t* part) {
+// How paged_attention's items are cut: false when a size is out of range.
+struct AttendPlan {
+    int cols, chunks, split;
+    int64_t items, tiles;            // of a sequence; of the longest item
+};
+
+bool plan_attend(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size, int64_t window, AttendPlan* p) {
     if (B < 1 || B > SGQ_MAX_SEQUENCES || heads < 1 || heads > SGQ_MAX_HEADS || Hq < heads || Hq > SGQ_MAX_HEADS || Hq % heads != 0 || D < 1 ||
-        D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size)
-        return 0;
-    const int64_t cols = attend_columns((int)(Hq / heads), attend_padded((int)D)), chunks = (Hq / heads + cols - 1) / cols;
-    const int64_t tiles = (width * page_size + kAttendTile - 1) / kAttendTile;
-    *part = attend_part((int)cols, attend_padded((int)D));
-    if (tiles <= 1) return 0;
-    const int64_t most = B * heads * chunks * tiles;
-    return most < kAttendCtas ? most : kAttendCtas;
+        D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size || window < 0)
+        return false;
+    const int64_t group = Hq / heads;
+    p->cols = attend_columns((int)group, attend_padded((int)D));
+    p->chunks = (int)((group + p->cols - 1) / p->cols);
+    p->items = heads * p->chunks;
+    p->tiles = attend_tiles(fmt == SGQ_FMT_FP8_PER_TOKEN, width * page_size, window);
+    p->split = attend_split(B * p->items, p->tiles);
+    return B * p->items * p->tiles <= 0x7FFFFFFF;        // counted in 32 bits
 }
 
 }  // namespace
@@ -258,10 +264,12 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
     return launched(launch_cache_read(fmt_of(fmt), dt_of(flags), current_device(), a, static_cast<cudaStream_t>(stream)));
 }
 
-int64_t sgq_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size) {
-    int64_t part = 0;
-    const int64_t ctas = attend_ctas(B, Hq, heads, D, width, page_size, &part);
-    return ctas > 0 ? attend_header_bytes() + ctas * 2 * part * 4 : 0;
+int64_t sgq_attention_workspace_bytes(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size,
+                                      int64_t window) {
+    AttendPlan p;
+    if (!plan_attend(fmt, B, Hq, heads, D, width, page_size, window, &p) || p.split > 0) return 0;
+    const int64_t most = B * p.items * p.tiles, ctas = most < kAttendCtas ? most : kAttendCtas;
+    return attend_header_bytes() + ctas * 2 * attend_part(p.cols, attend_padded((int)D)) * 4;
 }
 
 int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* cache, const sgq_heads_t* q,
@@ -278,7 +286,9 @@ int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* ca
     st = take_heads(q, B, cache->D, false, &a.q, &qn);
     if (st != SGQ_OK) return st;
     if (q->heads % cache->heads != 0) return SGQ_ERR_INVALID_ARG;
-    const int64_t ws = sgq_attention_workspace_bytes(B, q->heads, cache->heads, cache->D, width, cache->page_size);
+    AttendPlan p;
+    if (!plan_attend(fmt, B, q->heads, cache->heads, cache->D, width, cache->page_size, window, &p)) return SGQ_ERR_UNSUPPORTED;
+    const int64_t ws = sgq_attention_workspace_bytes(fmt, B, q->heads, cache->heads, cache->D, width, cache->page_size, window);
     if (!lengths || !out || (width > 0 && !pages) || (ws > 0 && !workspace)) return SGQ_ERR_INVALID_ARG;
     if (!aligned(pages, 4) || !aligned(lengths, 4) || !aligned(sinks, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
         return SGQ_ERR_MISALIGNED;
@@ -302,10 +312,10 @@ int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* ca
     a.window = (int)(window > a.limit ? 0 : window);     // a window over all tokens is none
     a.B = (int)B;
     a.group = (int)(q->heads / cache->heads);
-    const int cols = attend_columns(a.group, attend_padded((int)cache->D));
-    a.chunks = (a.group + cols - 1) / cols;
-    a.items = (int)cache->heads * a.chunks;
-    if ((int64_t)a.B * a.items * ((a.limit + kAttendTile - 1) / kAttendTile + 1) > 0x7FFFFFFF) return SGQ_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
+    a.chunks = p.chunks;
+    a.items = (int)p.items;
+    a.tiles = (int)p.tiles;
+    a.split = p.split;
     return launched(launch_attend(fmt_of(fmt), dt_of(flags), current_device(), a, static_cast<cudaStream_t>(stream)));
 }
 

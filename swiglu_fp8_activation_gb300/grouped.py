@@ -51,6 +51,7 @@ def _dims(t: torch.Tensor, n: int, name: str):
     return t.shape
 
 
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device    # asked for with a CUDA tensor in hand
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
@@ -74,7 +75,7 @@ def _here(stream, what: str, *tensors):
         if stream.device != tensors[0].device:
             raise SgqError(f"{what}: a stream of {stream.device}, tensors on {tensors[0].device}")
         return None
-    return _raw_stream(d) if d == torch.cuda.current_device() else None
+    return _raw_stream(d) if d == _device() else None
 
 
 def _there(stream, t: torch.Tensor):

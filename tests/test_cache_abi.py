@@ -203,7 +203,7 @@ def test_read_refusals(L):
 
 
 def test_attention_refusals(L):
-    def att(fmt=3, flags=0, B=2, c=None, q=None, t=P(1), width=5, n=P(2), scale=1.0, window=0, sinks=None, out=P(3), lse=None, ws=P(4)):
+    def att(fmt=3, flags=0, B=2, c=None, q=None, t=P(1), width=6250, n=P(2), scale=1.0, window=0, sinks=None, out=P(3), lse=None, ws=P(4)):
         return refused(L.paged_attention(fmt, flags, B, c or kv(), q or heads(P(0), H=8, ts=512), t, width, n, scale, window, sinks, out, lse, ws, None))
     assert att(B=0, q=heads(None), out=None) == OK
     assert att(flags=INTERLEAVED) == INVALID
@@ -230,12 +230,16 @@ def test_attention_refusals(L):
     assert att(ws=P(3)) == INVALID
     assert att(fmt=2, c=fp8(), out=P(12)) == INVALID
     ws = L.sgq_attention_workspace_bytes
-    assert ws(2, 8, 4, 64, 4, 16) == 0                   # 64 tokens: one tile
-    assert ws(2, 8, 4, 64, 5, 16) > 0
-    assert ws(64, 64, 8, 128, 1000, 16) == ws(65536, 64, 8, 128, 10000, 16)      # bounded by the CTAs
-    for bad in ((0, 8, 4, 64, 5, 16), (2, 6, 4, 64, 5, 16), (2, 8, 4, 300, 5, 16), (2, 8, 4, 64, -1, 16), (2, 8, 4, 64, 1 << 28, 16), (2, 2048, 4, 64, 5, 16),
-                (2, 8, 0, 64, 5, 16), (2, 8, 4, 64, 5, 0), (65537, 8, 4, 64, 5, 16)):
-        assert ws(*bad) == 0, bad
+    assert ws(3, 2, 8, 4, 64, 4, 16, 0) == 0             # few tokens: one launch
+    assert ws(3, 2, 8, 4, 64, 6250, 16, 0) > 0
+    assert ws(3, 2, 8, 4, 64, 6250, 16, 100) == 0        # a short window
+    assert ws(3, 64, 64, 8, 128, 10000, 16, 0) == ws(3, 128, 64, 8, 128, 20000, 16, 0)      # bounded by the CTAs
+    for bad in ((0, 8, 4, 64, 6250, 16, 0), (2, 6, 4, 64, 6250, 16, 0), (2, 8, 4, 300, 6250, 16, 0), (2, 8, 4, 64, -1, 16, 0), (2, 8, 4, 64, 1 << 28, 16, 0),
+                (2, 2048, 4, 64, 6250, 16, 0), (2, 8, 0, 64, 6250, 16, 0), (2, 8, 4, 64, 6250, 0, 0), (65537, 8, 4, 64, 6250, 16, 0), (2, 8, 4, 64, 6250, 16, -1),
+                (65536, 1024, 1024, 64, 1 << 20, 16, 0)):
+        assert ws(3, *bad) == 0, bad
+    assert att(B=65536, width=1 << 20, q=heads(P(0), H=1024, ts=65536), c=kv(H=1024, ps=1 << 20)) == UNSUPPORTED        # 2^31 tiles
+    assert sgq.attention_workspace_bytes("none", 2, 8, 4, 64, 6250, 16) == ws(3, 2, 8, 4, 64, 6250, 16, 0)
 
 
 def bf(*shape):

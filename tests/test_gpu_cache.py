@@ -263,24 +263,29 @@ def attend(fmt, dtype, lengths, heads, group, D, P, *, order="head", window=0, s
             s.transpose(1, 2)[~used] = math.nan
     sk = torch.randn(Hq, generator=ref.gen(seed + 3)) * 2 if sinks else None
     want, tol, wl, tl = ref.attention(q, k, v, ks, vs, table, n, scale, window, sk)
-    out, uo = guarded((B, Hq, D), dtype)
-    lse, ul = guarded((B, Hq), torch.float32)
-    ws, uw = guarded((sgq.attention_workspace_bytes(B, Hq, heads, D, table.shape[1], P),), torch.uint8)
-    dq, dk, dv, dks, dvs, dt, dn, dsk = cuda(q, k, v, ks, vs, table, n, sk)
-    kw = dict(fmt=fmt, k_scale=dks, v_scale=dvs, scale=scale, window=window, sinks=dsk)
-    got = sgq.paged_attention(dq, dk, dv, dt, dn, out=out, lse=lse, workspace=ws, **kw)
-    torch.cuda.synchronize()
-    assert got[0] is out and got[1] is lse
-    uo(), ul(), uw()
     what = f"{fmt} {dtype} {lengths} H={heads}x{group} D={D} P={P} window={window}"
-    ref.check(out.cpu(), want, tol, what)
     none = wl == -math.inf
-    assert (lse.cpu()[none] == -math.inf).all()
-    ref.check(lse.cpu()[~none], wl[~none], tl[~none], what + " lse")
-    again = sgq.paged_attention(dq, dk, dv, dt, dn, **kw)
-    assert torch.equal(again.view(torch.int16), out.view(torch.int16)), "two runs differ"
-    if norm:
-        assert ref.off_by_rounding(out.cpu(), want) < 1.1
+    # the table as it is, and one for long sequences, which CTAs share (a window's items are short all the same)
+    room = 0
+    for wide in (table, torch.nn.functional.pad(table, (0, -(-60000 // P)), value=-1)) if int(n.max()) <= table.shape[1] * P else (table,):
+        out, uo = guarded((B, Hq, D), dtype)
+        lse, ul = guarded((B, Hq), torch.float32)
+        room = sgq.attention_workspace_bytes(fmt, B, Hq, heads, D, wide.shape[1], P, window)
+        ws, uw = guarded((room,), torch.uint8)
+        dq, dk, dv, dks, dvs, dt, dn, dsk = cuda(q, k, v, ks, vs, wide, n, sk)
+        kw = dict(fmt=fmt, k_scale=dks, v_scale=dvs, scale=scale, window=window, sinks=dsk)
+        got = sgq.paged_attention(dq, dk, dv, dt, dn, out=out, lse=lse, workspace=ws, **kw)
+        torch.cuda.synchronize()
+        assert got[0] is out and got[1] is lse
+        uo(), ul(), uw()
+        ref.check(out.cpu(), want, tol, what)
+        assert (lse.cpu()[none] == -math.inf).all()
+        ref.check(lse.cpu()[~none], wl[~none], tl[~none], what + " lse")
+        again = sgq.paged_attention(dq, dk, dv, dt, dn, **kw)
+        assert torch.equal(again.view(torch.int16), out.view(torch.int16)), "two runs differ"
+        if norm:
+            assert ref.off_by_rounding(out.cpu(), want) < 1.1
+    assert room or window or wide is table
     return out.cpu(), want
 
 
