@@ -38,18 +38,21 @@ namespace sgq {
 namespace attend {
 
 constexpr int kParts = 4;                        // of a tile's tokens, a group of warps each
+// Entries of items that CTAs share: one an item (few items, each of many CTAs), or one a CTA.
+enum Joined : int { kByCta = 1, kByItem = 2 };
+constexpr int kStages = 8;                       // tiles copied ahead, at most (and 2 at least)
 constexpr float kNone = -3.0e38f;                // below every logit
 constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
 
 // Kinds of rows and queries.
 enum Kind : int { BF16 = 0, F16 = 1, FP8_BF16 = 2, FP8_F16 = 3 };
 
-// CG: groups of 8 columns, a warp of each group of warps for each. DIRECT: see attend_kernel.
-template <int KIND, int DP, int CG, bool DIRECT>
+// Columns: NT times 8 a warp, CG warps side by side. DIRECT: see attend_kernel.
+template <int KIND, int DP, int CG, int NT, bool DIRECT>
 struct Shape {
     static constexpr bool fp8 = KIND >= FP8_BF16;
     static constexpr int warps = kParts * CG, threads = warps * 32;
-    static constexpr int tokens = attend_tokens(fp8);            // of a tile
+    static constexpr int tokens = attend_tokens(fp8, DP);            // of a tile
     static constexpr int rows = tokens / kParts;                 // that a warp takes at a time, 16 of them a product
     static constexpr int halves = rows / 16;
     static constexpr uint32_t full = rows == 32 ? 0xFFFFFFFFu : 0xFFFFu;         // the mask of rows that are all there
@@ -60,23 +63,17 @@ struct Shape {
     static constexpr bool swizzled = fp8 && DP >= 128;
     static constexpr int stride = DP * elem + (swizzled ? 0 : 16);
     static constexpr int slot = 2 * rows * stride + (fp8 ? 2 * rows * 4 : 0);
-#ifndef ATT_D64
-#define ATT_D64 3
-#endif
-#ifndef ATT_D8
-#define ATT_D8 3
-#endif
-#ifndef ATT_S8
-#define ATT_S8 2
-#endif
-    static constexpr int ctas = DP == 256 ? (CG == 1 ? 2 : 1) : CG == 1 ? (DIRECT ? (DP == 64 ? ATT_D64 : fp8 ? ATT_D8 : 3) : fp8 ? ATT_S8 : 2) : CG == 2 ? 2 : 1;   // a multiprocessor
-    static constexpr int fit = (227 * 1024 / ctas - 3072) / (slot * kParts);
-    static constexpr int stages = fit < 2 ? 2 : fit > 8 ? 8 : fit;
-    static constexpr int smem = stages * slot * kParts;
+    static constexpr int step = kParts * slot;                   // bytes of a tile: its parts' slots side by side
+    // CTAs a multiprocessor at most. Three CTAs that each take a short item hide one another's beginnings (64 sequences up to 4096, bf16:
+    // 82 us, with two 89); CTAs that take long shares are two, but for narrow E4M3 rows, which are bound by
+    // instructions (4 sequences of 32768, D 64: 50 us with two, 33 with three).
+    static constexpr int ctas = DP == 256 ? (fp8 && CG == 1 ? 2 : 1) : CG > 1 ? 1 : NT > 1 ? 2 : DIRECT || (fp8 && DP == 64) ? 3 : 2;
+    // Tiles that fit in shared memory where n CTAs share a multiprocessor.
+    static constexpr int fit(int n) { return (227 * 1024 / n - 3072) / step; }
     static constexpr int parts = KIND == FP8_BF16 ? 1 : 2;       // 16-bit parts of p
     static constexpr int line = (DP + 4) * 4;                    // bytes of a column's sums: 4 lanes' columns meet no bank twice
     static constexpr int at_once = slot / (8 * line) < CG ? slot / (8 * line) : CG;      // groups of columns whose sums pass through a slot
-    static_assert(at_once >= 1 && CG % at_once == 0 && smem <= 227 * 1024 - 2048, "");
+    static_assert(at_once >= 1 && CG % at_once == 0 && fit(ctas) >= 2, "");
     // Where piece p of row r lies, from the row's beginning. E4M3: a quarter of a warp reads 4 pieces of rows r, r + 1 (k), or 2 pieces of
     // rows r, r + 2, r + 4, r + 6 (v).
     static __device__ __forceinline__ int piece_at(int r, int p) { return (swizzled ? p ^ ((r & 6) ^ ((r & 1) << 2)) : p) * 16; }
@@ -148,6 +145,17 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
 }
 
+// Until at most n of this thread's copy groups are pending (n at least 1).
+__device__ __forceinline__ void wait_but(int n) {
+    if (n == 1) cp_async_wait<1>();
+    else if (n == 2) cp_async_wait<2>();
+    else if (n == 3) cp_async_wait<3>();
+    else if (n == 4) cp_async_wait<4>();
+    else if (n == 5) cp_async_wait<5>();
+    else if (n == 6) cp_async_wait<6>();
+    else cp_async_wait<7>();
+}
+
 // floor(log2 s) of a scale, held inside +-100; zero and what is not finite included.
 __device__ __forceinline__ float scale_log(float s) {
     const int e = (int)((__float_as_uint(s) >> 23) & 0xFF) - 127;
@@ -213,13 +221,13 @@ __device__ __forceinline__ float ld_cluster4(uint32_t at) {
 }
 
 // DIRECT: a cluster of a.split CTAs takes one item, each an equal run of its tiles. Else CTAs take shares of all tiles.
-template <int KIND, int DP, int CG, bool DIRECT>
-__global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KIND, DP, CG, DIRECT>::ctas) attend_kernel(const AttendArgs a) {
-    using S = Shape<KIND, DP, CG, DIRECT>;
+template <int KIND, int DP, int CG, int NT, bool DIRECT>
+__global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shape<KIND, DP, CG, NT, DIRECT>::ctas) attend_kernel(const AttendArgs a) {
+    using S = Shape<KIND, DP, CG, NT, DIRECT>;
     constexpr bool kF8 = S::fp8, kBf = KIND == BF16;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
-    constexpr int kSteps = DP / 16, kCols = CG * 8, kThreads = S::threads;
-    extern __shared__ __align__(16) uint8_t stages[];
+    constexpr int kSteps = DP / 16, kCols = CG * NT * 8, kThreads = S::threads;
+    extern __shared__ __align__(16) uint8_t tiles[];
     __shared__ int sum_part[S::warps];
     __shared__ int share_b, share_n, share_off;
     __shared__ float s_m[kParts][kCols], s_l[kParts][kCols];
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
         }
         __syncthreads();
         if (count == 0) {
-            if (a.joined && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
+            if (a.joined == kByCta && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
             return;
         }
         ld.enter(a, share_b, share_n);
@@ -318,8 +326,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
 
     // Copying. Where pages are whole multiples of 16 tokens, 16 tokens have one page and lie
     // a stride apart; else each lane finds its own token's row.
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(stages) + part * S::stages * S::slot;
-    __shared__ uint32_t s_mask[kParts][S::stages];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tiles) + part * S::slot;
+    __shared__ uint32_t s_mask[kParts][kStages];
     const bool even = (a.c.page.d & 15) == 0;
     const int64_t v_from_k = a.c.v - a.c.k;
     constexpr int kRowsAt = 32 / S::pieces > 0 ? 32 / S::pieces : 1;              // rows that 32 lanes copy at once
@@ -330,14 +338,14 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
     const int64_t lane_from = lane_row * a.c.ts + (used ? piece * 16 : 0), row_step = kRowsAt * a.c.ts;
     // the lane's token of w's tile (of 16 tokens both halves of a warp have the same)
     auto token_of = [&](const W& w) { return w.start + w.tile * S::tokens + part * S::rows + (lane & (S::rows - 1)); };
-    auto page_of = [&](const W& w) {                             // of the lane's token; -1 where it is masked
-        const int t = token_of(w);
+    auto page_of = [&](const W& w, int on = 0) {                 // of the lane's token, `on` tiles on; -1 where it is masked
+        const int t = token_of(w) + on * S::tokens;
         if (t < w.lo || t >= w.n) return -1;
         return a.table[w.b * a.width + quotient(t, a.c.page)];
     };
     // Copies w's tile into a slot, the group's warps each their share; pid: page_of(w), asked for a tile before.
     auto copy = [&](const W& w, int slot, int pid) {
-        const uint32_t at = base + slot * S::slot;
+        const uint32_t at = base + slot * S::step;
         const int t = token_of(w);
         const bool there = pid >= 0 && pid < a.c.pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & S::full;
@@ -401,78 +409,87 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
     };
 
     // q of the current item as the right operand of S, and the factors of its columns: asked for, then made ready.
-    uint32_t qf[kSteps][2];
-    float factor[2];
+    uint32_t qf[kSteps][NT][2];
+    float factor[NT][2];
     auto ask_q = [&](const W& w) {
-        const int col = w.chunk * kCols + cg * 8 + g;
-        const bool there = col < a.group;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q.p + (int64_t)w.b * a.q.ts + (int64_t)(there ? w.head * a.group + col : 0) * a.q.hs);
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {
-            // the columns that this lane's pieces of k meet
-            const int d0 = kF8 ? (kk >> 2) * 64 + c * 16 + (kk & 3) * 4 : kk * 16 + c * 2, d1 = kF8 ? d0 + 2 : d0 + 8;
-            qf[kk][0] = there && d0 < a.c.D ? q[d0 >> 1] : 0u;
-            qf[kk][1] = there && d1 < a.c.D ? q[d1 >> 1] : 0u;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = w.chunk * kCols + (cg * NT + nt) * 8 + g;
+            const bool there = col < a.group;
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q.p + (int64_t)w.b * a.q.ts + (int64_t)(there ? w.head * a.group + col : 0) * a.q.hs);
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) {
+                // the columns that this lane's pieces of k meet
+                const int d0 = kF8 ? (kk >> 2) * 64 + c * 16 + (kk & 3) * 4 : kk * 16 + c * 2, d1 = kF8 ? d0 + 2 : d0 + 8;
+                qf[kk][nt][0] = there && d0 < a.c.D ? q[d0 >> 1] : 0u;
+                qf[kk][nt][1] = there && d1 < a.c.D ? q[d1 >> 1] : 0u;
+            }
         }
     };
     auto ready_q = [&]() {
         constexpr float kLog2e = 1.44269504088896340736f;
-        float up = 1.0f;
-        if (KIND == FP8_BF16) {      // bf16 -> fp16 by a power of two a head, its largest value in [1, 2)
-            float top = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk)
+        for (int nt = 0; nt < NT; ++nt) {
+            float up = 1.0f;
+            if (KIND == FP8_BF16) {      // bf16 -> fp16 by a power of two a head, its largest value in [1, 2)
+                float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][i] << 16)), fabsf(__uint_as_float(qf[kk][i] & 0xFFFF0000u))));
-            top = group_max<4>(top);
-            const int e = max(-120, min(120, (int)(__float_as_uint(top) >> 23) - 127));
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            up = __uint_as_float((uint32_t)(127 + e) << 23);
+                for (int kk = 0; kk < kSteps; ++kk)
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk)
+                    for (int i = 0; i < 2; ++i)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[kk][nt][i] << 16)), fabsf(__uint_as_float(qf[kk][nt][i] & 0xFFFF0000u))));
+                top = group_max<4>(top);
+                const int e = max(-120, min(120, (int)(__float_as_uint(top) >> 23) - 127));
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t v = qf[kk][i];
-                    qf[kk][i] = f32x2_to_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
-                }
+                for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t v = qf[kk][nt][i];
+                        qf[kk][nt][i] = f32x2_to_f16x2(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xFFFF0000u) * down);
+                    }
+            }
+            // column 2c (+ 1)'s factor is held by the lanes of row 2c (+ 1)
+            factor[nt][0] = __shfl_sync(0xFFFFFFFFu, up, c * 8) * (a.scale * kLog2e);
+            factor[nt][1] = __shfl_sync(0xFFFFFFFFu, up, c * 8 + 4) * (a.scale * kLog2e);
         }
-        // column 2c (+ 1)'s factor is held by the lanes of row 2c (+ 1)
-        factor[0] = __shfl_sync(0xFFFFFFFFu, up, c * 8) * (a.scale * kLog2e);
-        factor[1] = __shfl_sync(0xFFFFFFFFu, up, c * 8 + 4) * (a.scale * kLog2e);
     };
 
-    float o[kSteps][4], ref[2], sum[2];
+    float o[kSteps][NT][4], ref[NT][2], sum[NT][2];
     auto clear = [&]() {
-        ref[0] = ref[1] = kNone;
-        sum[0] = sum[1] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) {
+            ref[nt][0] = ref[nt][1] = kNone;
+            sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
+        }
     };
 
     auto tile = [&](int slot) {
         constexpr int H = S::halves;
-        const uint32_t at = base + slot * S::slot, vt = at + S::rows * S::stride, sc = vt + S::rows * S::stride;
+        const uint32_t at = base + slot * S::step, vt = at + S::rows * S::stride, sc = vt + S::rows * S::stride;
         const uint32_t mask = s_mask[part][slot];
-        float x[H][4];
-        if (!kF8) {
-            float x2[4] = {};                        // two chains of products
-            const uint32_t from = at + (lane & 15) * S::stride + (lane >> 4) * 16;
-            x[0][0] = x[0][1] = x[0][2] = x[0][3] = 0.0f;
+        // S, in two chains of products a tile of 16 by 8
+        float x[H][NT][4];
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                uint32_t k[4];
-                ldmatrix4(k, from + kk * 32);
-                mma<kBf>(kk & 1 ? x2 : x[0], k, qf[kk][0], qf[kk][1]);
-            }
+        for (int h = 0; h < H; ++h) {
+            float x2[NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[0][i] = (x[0][i] + x2[i]) * factor[i & 1];
-        } else {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float x2[4] = {};
-                x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.0f;
-                const float k0 = lds_f32(sc + (h * 16 + g) * 4), k1 = lds_f32(sc + (h * 16 + g + 8) * 4);
+                for (int i = 0; i < 4; ++i) x[h][nt][i] = x2[nt][i] = 0.0f;
+            if (!kF8) {
+                const uint32_t from = at + (lane & 15) * S::stride + (lane >> 4) * 16;
+#pragma unroll
+                for (int kk = 0; kk < kSteps; ++kk) {
+                    uint32_t k[4];
+                    ldmatrix4(k, from + kk * 32);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma<kBf>(kk & 1 ? x2[nt] : x[h][nt], k, qf[kk][nt][0], qf[kk][nt][1]);
+                }
+            } else {
 #pragma unroll
                 for (int blk = 0; blk < DP / 64; ++blk) {
                     const uint32_t from = at + (h * 16 + g) * S::stride + S::piece_at(g, blk * 4 + c);
@@ -483,22 +500,29 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
                         uint32_t k[4];
                         widen(up[i], k[0], k[2]);
                         widen(dn[i], k[1], k[3]);
-                        mma<false>(i & 1 ? x2 : x[h], k, qf[blk * 4 + i][0], qf[blk * 4 + i][1]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma<false>(i & 1 ? x2[nt] : x[h][nt], k, qf[blk * 4 + i][nt][0], qf[blk * 4 + i][nt][1]);
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[h][i] = (x[h][i] + x2[i]) * (factor[i & 1] * (i < 2 ? k0 : k1));
             }
+            const float k0 = kF8 ? lds_f32(sc + (h * 16 + g) * 4) : 1.0f, k1 = kF8 ? lds_f32(sc + (h * 16 + g + 8) * 4) : 1.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[h][nt][i] = (x[h][nt][i] + x2[nt][i]) * (kF8 ? factor[nt][i & 1] * (i < 2 ? k0 : k1) : factor[nt][i & 1]);
         }
         if (mask != S::full) {
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!((mask >> (h * 16 + g + 8 * (i >> 1))) & 1)) x[h][i] = -INFINITY;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!((mask >> (h * 16 + g + 8 * (i >> 1))) & 1)) x[h][nt][i] = -INFINITY;
         }
         // p, and w = p times the row's v scale. Where one is out of bounds (or no number) the reference moves.
-        float vs[H][2], w[H][4], s0 = 0.0f, s1 = 0.0f;
+        float vs[H][2], w[H][NT][4], s0[NT], s1[NT];
         bool over = false;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -506,16 +530,19 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
             vs[h][1] = kF8 ? lds_f32(sc + (S::rows + h * 16 + g + 8) * 4) : 1.0f;
         }
         auto weigh = [&]() {
-            s0 = s1 = 0.0f;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
+            for (int nt = 0; nt < NT; ++nt) {
+                s0[nt] = s1[nt] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[h][i] = ex2_approx(x[h][i] - ref[i & 1]);
-                s0 += w[h][0] + w[h][2];
-                s1 += w[h][1] + w[h][3];
-                if (kF8) {
+                for (int h = 0; h < H; ++h) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[h][i] *= vs[h][i >> 1];
+                    for (int i = 0; i < 4; ++i) w[h][nt][i] = ex2_approx(x[h][nt][i] - ref[nt][i & 1]);
+                    s0[nt] += w[h][nt][0] + w[h][nt][2];
+                    s1[nt] += w[h][nt][1] + w[h][nt][3];
+                    if (kF8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[h][nt][i] *= vs[h][i >> 1];
+                    }
                 }
             }
         };
@@ -523,43 +550,52 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) over |= !(w[h][i] <= kMost);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) over |= !(w[h][nt][i] <= kMost);
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
-                float top = ref[col];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int col = 0; col < 2; ++col) {
+                    float top = ref[nt][col];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) top = fmaxf(top, kF8 ? x[h][2 * r + col] + scale_log(vs[h][r]) : x[h][2 * r + col]);
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                const float f = ex2_approx(ref[col] - top);
-                ref[col] = top;
-                sum[col] *= f;
+                        for (int r = 0; r < 2; ++r) top = fmaxf(top, kF8 ? x[h][nt][2 * r + col] + scale_log(vs[h][r]) : x[h][nt][2 * r + col]);
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    o[i][col] *= f;
-                    o[i][2 + col] *= f;
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    const float f = ex2_approx(ref[nt][col] - top);
+                    ref[nt][col] = top;
+                    sum[nt][col] *= f;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        o[i][nt][col] *= f;
+                        o[i][nt][2 + col] *= f;
+                    }
                 }
-            }
             weigh();
         }
-        sum[0] += s0;
-        sum[1] += s1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            sum[nt][0] += s0[nt];
+            sum[nt][1] += s1[nt];
+        }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            uint32_t p[S::parts][2];
+            uint32_t p[S::parts][NT][2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float w0 = w[h][2 * r], w1 = w[h][2 * r + 1];
-                const uint32_t hi = kBf ? f32x2_to_bf16x2(w0, w1) : f32x2_to_f16x2(w0, w1);
-                p[0][r] = transposed(hi);
-                if (S::parts == 2) {
-                    const float2 back = kBf ? make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)) : f16x2_to_f32x2(hi);
-                    p[S::parts - 1][r] = transposed(kBf ? f32x2_to_bf16x2(w0 - back.x, w1 - back.y) : f32x2_to_f16x2(w0 - back.x, w1 - back.y));
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float w0 = w[h][nt][2 * r], w1 = w[h][nt][2 * r + 1];
+                    const uint32_t hi = kBf ? f32x2_to_bf16x2(w0, w1) : f32x2_to_f16x2(w0, w1);
+                    p[0][nt][r] = transposed(hi);
+                    if (S::parts == 2) {
+                        const float2 back = kBf ? make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)) : f16x2_to_f32x2(hi);
+                        p[S::parts - 1][nt][r] = transposed(kBf ? f32x2_to_bf16x2(w0 - back.x, w1 - back.y) : f32x2_to_f16x2(w0 - back.x, w1 - back.y));
+                    }
                 }
-            }
             if (!kF8) {
                 // 8 x 8 pieces of V^T: tokens 0-7 by columns 0-7, columns 8-15, then tokens 8-15
                 const uint32_t from = vt + ((lane & 7) + (lane >> 4) * 8) * S::stride + ((lane >> 3) & 1) * 16;
@@ -568,7 +604,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
                     uint32_t v[4];
                     ldmatrix4t(v, from + i * 32);
 #pragma unroll
-                    for (int e = 0; e < S::parts; ++e) mma<kBf>(o[i], v, p[e][0], p[e][1]);
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < S::parts; ++e) mma<kBf>(o[i][nt], v, p[e][nt][0], p[e][nt][1]);
                 }
             } else {
                 constexpr int kWords = DP >= 128 ? 4 : 2;        // 4 codes of a token each
@@ -595,7 +633,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
                             widen(__byte_perm(v[0][i], v[1][i], e ? 0x7362 : 0x5140), m[0], m[1]);
                             widen(__byte_perm(v[2][i], v[3][i], e ? 0x7362 : 0x5140), m[2], m[3]);
 #pragma unroll
-                            for (int n = 0; n < S::parts; ++n) mma<false>(o[blk * 8 + 2 * i + e], m, p[n][0], p[n][1]);
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int n = 0; n < S::parts; ++n) mma<false>(o[blk * 8 + 2 * i + e][nt], m, p[n][nt][0], p[n][nt][1]);
                         }
                 }
             }
@@ -605,7 +645,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
     // Where a CTA of a cluster leaves its sums of a column.
     __shared__ float s_M[kCols], s_L[kCols];
     auto part_at = [&](int col, int slot) {
-        return (uint32_t)__cvta_generic_to_shared(stages) + (uint32_t)((col >> 3) * S::stages * S::slot + slot * S::slot + (col & 7) * S::line);
+        return (uint32_t)__cvta_generic_to_shared(tiles) + (uint32_t)(slot * S::step + (col >> 3) * S::slot + (col & 7) * S::line);
     };
     // Adds up what the warps have of the item at w and writes it: the result, or this CTA's part of it.
     auto flush = [&](const W& w, int slot, bool begun_here, bool ends_here) {
@@ -613,21 +653,24 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
         float* to_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attend_header_bytes()) +
                          (size_t)(2 * blockIdx.x + (begun_here ? 1 : 0)) * attend_part(kCols, DP);
 #pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            float l = sum[col];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-            if (g == 0) {
-                s_m[part][cg * 8 + 2 * c + col] = ref[col];
-                s_l[part][cg * 8 + 2 * c + col] = l;
+            for (int col = 0; col < 2; ++col) {
+                float l = sum[nt][col];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+                if (g == 0) {
+                    s_m[part][(cg * NT + nt) * 8 + 2 * c + col] = ref[nt][col];
+                    s_l[part][(cg * NT + nt) * 8 + 2 * c + col] = l;
+                }
             }
-        }
         group_sync();
         constexpr int kEach = kThreads / (8 * S::at_once);       // threads a column, 4 values at a time
 #pragma unroll
-        for (int round = 0; round < CG / S::at_once; ++round) {
+        for (int turn = 0; turn < NT * CG / S::at_once; ++turn) {
+            const int nt = turn % NT, round = turn / NT;
             if (cg / S::at_once == round) {
-                const uint32_t own = base + slot * S::slot + (cg % S::at_once) * 8 * S::line;
+                const uint32_t own = base + slot * S::step + (cg % S::at_once) * 8 * S::line;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -635,11 +678,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
                         const int col = 2 * c + (e & 1), r = e >> 1;
                         constexpr int kSide = DP >= 128 ? 16 : 8;                // columns of V side by side in a lane (FP8)
                         const int d = kF8 ? (i >> 3) * 128 + g * kSide + 2 * (i & 7) + r : i * 16 + g + 8 * r;
-                        sts_f32(own + col * S::line + d * 4, o[i][e]);
+                        sts_f32(own + col * S::line + d * 4, o[i][nt][e]);
                     }
             }
             __syncthreads();
-            const int at = threadIdx.x / kEach, col = round * S::at_once * 8 + at, q = w.chunk * kCols + col;
+            const int at = threadIdx.x / kEach, col = ((round * S::at_once + (at >> 3)) * NT + nt) * 8 + (at & 7), q = w.chunk * kCols + col;
             if (q < a.group) {
                 float M = kNone, f[kParts], L = 0.0f;
 #pragma unroll
@@ -652,13 +695,13 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
                 const int qh = w.head * a.group + q;
                 float inv = 1.0f, lse = 0.0f;
                 if (whole) finish(a, w.b, qh, M, L, inv, lse);
-                const uint32_t all = (uint32_t)__cvta_generic_to_shared(stages) + slot * S::slot + at * S::line;
+                const uint32_t all = (uint32_t)__cvta_generic_to_shared(tiles) + slot * S::step + at * S::line;
 #pragma unroll
                 for (int d = (threadIdx.x % kEach) * 4; d < DP; d += kEach * 4) {
                     float4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int v = 0; v < kParts; ++v) {
-                        const uint4 u = lds16(all + v * S::stages * S::slot + d * 4);
+                        const uint4 u = lds16(all + v * S::slot + d * 4);
                         y.x += __uint_as_float(u.x) * f[v];
                         y.y += __uint_as_float(u.y) * f[v];
                         y.z += __uint_as_float(u.z) * f[v];
@@ -688,71 +731,63 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
         }
     };
 
-    // Copies run S::stages tiles ahead, a commit group each (empty behind the last). The
-    // first ones' pages are asked for together.
-    int pids[S::stages];
-    {
-        W w = ld;
-#pragma unroll
-        for (int s = 0; s < S::stages; ++s) {
-            pids[s] = s < left ? page_of(w) : -1;
-            advance(w, false);
-        }
-    }
+    // Turn i copies tile i and computes tile i - a.stages, whose slot that is: copies run ahead, a
+    // commit group each (empty behind the last). One loop, so that the copying's code is there once.
     ask_q(cu);
-#pragma unroll
-    for (int s = 0; s < S::stages; ++s) {
-        if (left > 0) {
-            copy(ld, s, pids[s]);
-            --left;
-            advance(ld, true);
-        }
-        cp_async_commit();
-    }
-    int pid = left > 0 ? page_of(ld) : -1;
-    ready_q();
-    clear();
-    bool begun_here = cu.tile == 0;
-    int todo = count;
-    for (int slot = 0; todo > 0; slot = slot + 1 == S::stages ? 0 : slot + 1) {
-        cp_async_wait<S::stages - 1>();
-        group_sync();
-        tile(slot);
-        --todo;
-        const bool ends = cu.tile + 1 == cu.tiles;
-        if (!DIRECT && (ends || todo == 0)) {
-            const W done = cu;
-            if (todo > 0) {
-                advance(cu, false);
-                ask_q(cu);
+    // a tile's pages are asked for a tile before its copy; where all tiles are one item's, two
+    int pid = left > 0 ? page_of(ld) : -1, pid2 = DIRECT && left > 1 ? page_of(ld, 1) : -1, todo = count, slot = 0;
+    bool fresh = true, begun_here = cu.tile == 0;                // the item's first tile here; whether it is the item's first
+    for (int turn = 0; todo > 0; ++turn) {
+        if (turn >= a.stages) {
+            wait_but(a.stages - 1);
+            group_sync();
+            if (fresh) {
+                ready_q();
+                clear();
+                fresh = false;
             }
-            flush(done, slot, begun_here, ends);
-            if (a.joined && todo == 0 && threadIdx.x == 0) {
-                Shared sh = {done.b, done.j, -1, -1};
-                if (begun_here && !ends) {
-                    // the item goes on in the next CTAs, to the one that has its last tile
-                    const int last = from + count - 1 + (done.tiles - done.tile - 1);
-                    sh.first = me;
-                    sh.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
+            tile(slot);
+            --todo;
+            const bool ends = cu.tile + 1 == cu.tiles;
+            if (!DIRECT && (ends || todo == 0)) {
+                const W done = cu;
+                if (todo > 0) {
+                    advance(cu, false);
+                    ask_q(cu);
                 }
-                reinterpret_cast<Shared*>(a.ws)[blockIdx.x] = sh;
+                flush(done, slot, begun_here, ends);
+                // who joins: the entry of the item, by the CTA that begins it, or of this CTA
+                if (a.joined && threadIdx.x == 0 && (a.joined == kByItem ? begun_here : todo == 0)) {
+                    Shared sh = {done.b, done.j, -1, -1};
+                    if (begun_here && !ends) {
+                        // the item goes on in the next CTAs, to the one that has its last tile
+                        const int last = from + count - 1 + (done.tiles - done.tile - 1);
+                        sh.first = me;
+                        sh.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
+                    }
+                    reinterpret_cast<Shared*>(a.ws)[a.joined == kByItem ? done.b * a.items + done.j : me] = sh;
+                }
+                fresh = begun_here = true;
+            } else {
+                advance(cu, false);
             }
-            if (todo > 0) ready_q();
-            clear();
-            begun_here = true;
-        } else {
-            advance(cu, false);
+            group_sync();
         }
-        group_sync();
         if (left > 0) {
             copy(ld, slot, pid);
             if (--left > 0) {
                 advance(ld, true);
-                pid = page_of(ld);
+                if (!DIRECT) pid = page_of(ld);
+            }
+            if (DIRECT) {
+                pid = pid2;
+                pid2 = left > 1 ? page_of(ld, 1) : -1;
             }
         }
         cp_async_commit();
+        slot = slot + 1 == a.stages ? 0 : slot + 1;
     }
+    if (fresh) clear();                                          // a CTA of a cluster that had no tile
     if (!DIRECT) return;
     cp_async_wait<0>();
     __syncthreads();
@@ -789,89 +824,128 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, DIRECT>::threads, Shape<KI
     cluster_wait();
 }
 
-constexpr int kJoinWarps = 4, kJoinThreads = kJoinWarps * 32;
-
-// Joins the parts of the items that several CTAs share: CTA (c, column) those of the item that CTA c of the first launch has begun.
-template <int DT, int DP>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, int cols) {
+// Joins the parts of the items that several CTAs share: CTA (x, column) those of the item of entry x. Each warp takes
+// every WARPS-th part, four at a time, with a maximum of its own; the warps meet in shared memory. One round of
+// reads, bound by its latency, where an item has few parts; 16 warps where it may have many.
+template <int DT, int DP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) attend_join_kernel(const AttendArgs a, int cols) {
     pdl_wait();
     pdl_trigger();
     const Shared sh = reinterpret_cast<const Shared*>(a.ws)[blockIdx.x];
     if (sh.first < 0) return;
     const int col = blockIdx.y, head = sh.j / a.chunks, q = (sh.j - head * a.chunks) * cols + col;
     if (q >= a.group) return;
-    __shared__ float s_m[kJoinThreads], s_o[kJoinWarps][DP + 1];
+    __shared__ float s_o[WARPS][DP + 2];                         // sums, then the total and the maximum
     const float* parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + attend_header_bytes());
     const int n = sh.last - sh.first + 1, size = attend_part(cols, DP), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // the first CTA's part is its second, the others' their first
-    auto part = [&](int i) { return parts + (size_t)(2 * (sh.first + i) + (i == 0 ? 1 : 0)) * size; };
-    float M = kNone;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) M = fmaxf(M, part(i)[cols * DP + col]);
-    s_m[threadIdx.x] = M;
-    __syncthreads();
-    M = kNone;
-    for (int i = 0; i < min(n, kJoinThreads); ++i) M = fmaxf(M, s_m[i]);
-    constexpr int kEach = DP / 32;
-    float y[kEach] = {}, L = 0.0f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += kJoinWarps) {
-        const float* p = part(i);
-        const float f = ex2_approx(p[cols * DP + col] - M);
-        L += f * p[cols * DP + cols + col];
+    constexpr int kEach = DP / 32, kAhead = 4;
+    float y[kEach] = {}, L = 0.0f, M = kNone;
+    for (int i0 = warp; i0 < n; i0 += WARPS * kAhead) {
+        float m[kAhead], l[kAhead], v[kAhead][kEach];
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) y[e] += f * p[col * DP + e * 32 + lane];
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * WARPS;
+            // the first CTA's part is its second, the others' their first
+            const float* p = parts + (size_t)(2 * (sh.first + min(i, n - 1)) + (i == 0 ? 1 : 0)) * size;
+            m[k] = i < n ? p[cols * DP + col] : kNone;
+            l[k] = i < n ? p[cols * DP + cols + col] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v[k][e] = i < n ? p[col * DP + e * 32 + lane] : 0.0f;
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) top = fmaxf(top, m[k]);
+        const float old = ex2_approx(M - top);
+        M = top;
+        L *= old;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) y[e] *= old;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float f = ex2_approx(m[k] - top);
+            L += f * l[k];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) y[e] += f * v[k][e];
+        }
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) s_o[warp][e * 32 + lane] = y[e];
-    if (lane == 0) s_o[warp][DP] = L;
+    if (lane == 0) {
+        s_o[warp][DP] = L;
+        s_o[warp][DP + 1] = M;
+    }
     __syncthreads();
-    L = s_o[0][DP] + s_o[1][DP] + s_o[2][DP] + s_o[3][DP];
+    float f[WARPS];
+    M = kNone;
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_o[w][DP + 1]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        f[w] = ex2_approx(s_o[w][DP + 1] - M);
+        L += f[w] * s_o[w][DP];
+    }
     const int qh = head * a.group + q;
     float inv, lse;
     finish(a, sh.b, qh, M, L, inv, lse);
-    for (int d = threadIdx.x; d < a.c.D; d += kJoinThreads) {
-        const float v = (s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv;
-        const uint32_t r = DT == DT_BF16 ? f32x2_to_bf16x2(v, 0.0f) : f32x2_to_f16x2(v, 0.0f);
+    for (int d = threadIdx.x; d < a.c.D; d += WARPS * 32) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += f[w] * s_o[w][d];
+        const uint32_t r = DT == DT_BF16 ? f32x2_to_bf16x2(v * inv, 0.0f) : f32x2_to_f16x2(v * inv, 0.0f);
         a.out[((int64_t)sh.b * a.q.n + qh) * a.c.D + d] = (uint16_t)r;
     }
     if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)sh.b * a.q.n + qh] = lse;
 }
 
-template <int KIND, int DP, int CG>
+template <int KIND, int DP, int CG, int NT>
 cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t stream) {
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     AttendArgs a = args;
+    const int64_t sms = dev.sms > 0 ? dev.sms : 152;
     if (a.split > 0) {
-        using S = Shape<KIND, DP, CG, true>;
-        return launch_grid(attend_kernel<KIND, DP, CG, true>, dim3((unsigned)(a.B * a.items * a.split)), S::threads, S::smem, a.split, dev.id, a, stream);
+        using S = Shape<KIND, DP, CG, NT, true>;
+        // Few CTAs wait for each tile's copies, and have the room to copy all that they need at once (ROW1); as many as the
+        // device holds do better with two tiles of wide rows, eight of narrow ones.
+        const int64_t ctas = (int64_t)a.B * a.items * a.split;
+        const int each = ctas <= sms ? 1 : ctas <= 2 * sms && S::ctas > 2 ? 2 : S::ctas, most = each < S::ctas || DP == 64 ? kStages : 2;
+        const int need = (a.tiles + a.split - 1) / a.split;
+        a.stages = S::fit(each) < most ? S::fit(each) : most;
+        if (a.stages > need) a.stages = need < 2 ? 2 : need;
+        return launch_grid(attend_kernel<KIND, DP, CG, NT, true>, dim3((unsigned)ctas), S::threads, a.stages * S::step, a.split, dev.id, a, stream);
     }
-    using S = Shape<KIND, DP, CG, false>;
-    int64_t ctas = (int64_t)(dev.sms > 0 ? dev.sms : 152) * S::ctas;
+    using S = Shape<KIND, DP, CG, NT, false>;
+    // Two tiles ahead, three where one CTA fills a multiprocessor: three are worse (8 sequences up to 131072, E4M3: 345 and 291 us; bf16 of 65536: 292 and 288).
+    a.stages = S::ctas == 1 && S::fit(1) > 2 ? 3 : 2;
+    int64_t ctas = sms * S::ctas;
     if (ctas > kAttendCtas) ctas = kAttendCtas;
     const int64_t most = (int64_t)a.B * a.items * a.tiles;
     if (ctas > most) ctas = most;
     // where no item has two tiles no two CTAs share one
-    a.joined = a.tiles > 1;
-    const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, false>, dim3((unsigned)ctas), S::threads, S::smem, 1, dev.id, a, stream);
+    const int64_t items = (int64_t)a.B * a.items;
+    a.joined = a.tiles <= 1 ? 0 : items <= 64 ? kByItem : kByCta;
+    const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, NT, false>, dim3((unsigned)ctas), S::threads, a.stages * S::step, 1, dev.id, a, stream);
     if (e != cudaSuccess || !a.joined) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(a.group < CG * 8 ? a.group : CG * 8));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3((unsigned)(a.joined == kByItem ? items : ctas), (unsigned)(a.group < CG * NT * 8 ? a.group : CG * NT * 8));
+    cfg.blockDim = dim3(a.joined == kByItem ? 512 : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<kDt, DP>, a, CG * 8);
+    return cudaLaunchKernelEx(&cfg, a.joined == kByItem ? attend_join_kernel<kDt, DP, 16> : attend_join_kernel<kDt, DP, 4>, a, CG * NT * 8);
 }
 
 template <int KIND>
 cudaError_t launch_kind(const Device& dev, const AttendArgs& a, cudaStream_t stream) {
     const int DP = attend_padded(a.c.D), cols = attend_columns(a.group, DP);
-    if (DP == 64) return cols == 8 ? launch<KIND, 64, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 64, 2>(dev, a, stream) : launch<KIND, 64, 4>(dev, a, stream);
-    if (DP == 128) return cols == 8 ? launch<KIND, 128, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 128, 2>(dev, a, stream) : launch<KIND, 128, 4>(dev, a, stream);
-    return cols == 8 ? launch<KIND, 256, 1>(dev, a, stream) : launch<KIND, 256, 2>(dev, a, stream);
+    // 16 columns: two tiles of 8 a warp, so that each row is read and widened once. Heads of 256 have no
+    // registers for that, but for 32 columns' two warps side by side.
+    if (DP == 64) return cols == 8 ? launch<KIND, 64, 1, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 64, 1, 2>(dev, a, stream) : launch<KIND, 64, 2, 2>(dev, a, stream);
+    if (DP == 128) return cols == 8 ? launch<KIND, 128, 1, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 128, 1, 2>(dev, a, stream) : launch<KIND, 128, 2, 2>(dev, a, stream);
+    return cols == 8 ? launch<KIND, 256, 1, 1>(dev, a, stream) : launch<KIND, 256, 2, 1>(dev, a, stream);
 }
 
 cudaError_t launch_bf16(const Device& dev, const AttendArgs& a, cudaStream_t stream);

@@ -93,9 +93,10 @@ struct AttendArgs {
     int limit;           // width * page size: the longest sequence
     int chunks;          // column chunks a head of the cache
     int items;           // heads * chunks a sequence
-    int joined;          // whether a second launch joins what several CTAs have computed
+    int joined;          // how a second launch finds what several CTAs have computed; 0 for none
     int split;           // CTAs of a cluster, where each takes one item; 0 for shares
     int tiles;           // of the longest item
+    int stages;          // tiles copied ahead
 };
 
 // Most CTAs that take shares of one paged_attention, for which its workspace has room.
@@ -104,28 +105,25 @@ constexpr int kAttendCtas = 512;
 // Columns (heads of q) a CTA takes at once.
 constexpr int attend_columns(int group, int DP) { return group <= 8 ? 8 : group <= 16 || DP > 128 ? 16 : 32; }
 constexpr int attend_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-// Tokens of a tile.
-__host__ __device__ constexpr int attend_tokens(bool fp8) { return fp8 ? 128 : 64; }
+// Tokens of a tile: of E4M3 rows twice as many, up to heads of 128.
+__host__ __device__ constexpr int attend_tokens(bool fp8, int DP) { return fp8 && DP <= 128 ? 128 : 64; }
 // Tiles of the longest item; a window may begin anywhere in its first tile.
-constexpr int64_t attend_tiles(bool fp8, int64_t limit, int64_t window) {
-    const int tokens = attend_tokens(fp8);
+constexpr int64_t attend_tiles(bool fp8, int DP, int64_t limit, int64_t window) {
+    const int tokens = attend_tokens(fp8, DP);
     if (window > 0 && limit > window + tokens - 1) limit = window + tokens - 1;
     return limit <= tokens ? 1 : (limit + tokens - 1) / tokens;
 }
 // CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles.
-#ifndef ATT_PER
-#define ATT_PER 16
-#endif
 constexpr int attend_split(int64_t items, int64_t tiles) {
     int split = 1;
-    while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * ATT_PER)) split *= 2;
-    return tiles <= split * ATT_PER && items * split <= 0x7FFFFFFF ? split : 0;
+    while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * 16)) split *= 2;
+    return tiles <= split * 16 && items * split <= 0x7FFFFFFF ? split : 0;
 }
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }
 
-// The item that CTA c of paged_attention has begun and not ended, and the last CTA that
-// has some of it; first is c, or -1 where there is none. The workspace begins with them.
+// An item of paged_attention that a CTA has begun and not ended: that CTA, and the last that
+// has some of it; first is -1 where there is none. The workspace begins with these entries.
 struct Shared {
     int b, j, first, last;
 };

@@ -160,7 +160,7 @@ bool plan_attend(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64
     p->cols = attend_columns((int)group, attend_padded((int)D));
     p->chunks = (int)((group + p->cols - 1) / p->cols);
     p->items = heads * p->chunks;
-    p->tiles = attend_tiles(fmt == SGQ_FMT_FP8_PER_TOKEN, width * page_size, window);
+    p->tiles = attend_tiles(fmt == SGQ_FMT_FP8_PER_TOKEN, attend_padded((int)D), width * page_size, window);
     p->split = attend_split(B * p->items, p->tiles);
     return B * p->items * p->tiles <= 0x7FFFFFFF;        // counted in 32 bits
 }
