@@ -29,6 +29,17 @@ inline Div make_div(uint32_t d) {
 
 __device__ __forceinline__ uint32_t quotient(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.m) >> d.s); }
 
+// The page of a slot, and its place in it.
+__device__ __forceinline__ int64_t page_of_slot(int64_t slot, const Div& d, int& place) {
+    const int64_t page = (uint64_t)slot >> 31 ? slot / d.d : (int64_t)quotient((uint32_t)slot, d);
+    place = (int)(slot - page * d.d);
+    return page;
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int wide, int64_t i) {
+    return wide ? static_cast<const int64_t*>(p)[i] : (int64_t) static_cast<const int32_t*>(p)[i];
+}
+
 struct Heads {
     uint16_t* p;
     int64_t ts, hs;      // strides of tokens and heads, in elements
@@ -63,7 +74,7 @@ struct WriteArgs {
     const void* slots;
     int wide;            // 64-bit slots
     int64_t T;
-    int tpc;             // tokens a CTA
+    int per;             // threads a token
     int D;
 };
 
@@ -72,6 +83,8 @@ struct ReadArgs {
     const void* slots;
     int wide;
     int64_t S;
+    int tpc;             // tokens a CTA
+    Div pieces, row;     // pieces of a token and of a row
     uint16_t* k;         // either may be null
     uint16_t* v;
 };

@@ -247,7 +247,6 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
     if (S == 0) return SGQ_OK;
     if (!slots || (!k_out && !v_out)) return SGQ_ERR_INVALID_ARG;
     if (!aligned(slots, (uintptr_t)slot_bytes) || !aligned(k_out, 16) || !aligned(v_out, 16)) return SGQ_ERR_MISALIGNED;
-    if (S > 0x7FFFFFFF / ((cache->heads * cache->D + 4095) / 4096)) return SGQ_ERR_UNSUPPORTED;      // a CTA for each 4096 values at least
     const size_t n = (size_t)(S * cache->heads * cache->D) * 2;
     const Span out[] = {{k_out, n}, {v_out, n}}, s = {slots, (size_t)S * slot_bytes};
     if (any_overlap(out, 2)) return SGQ_ERR_INVALID_ARG;

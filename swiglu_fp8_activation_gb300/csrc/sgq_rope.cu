@@ -21,107 +21,131 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ int64_t load_index(const void* p, int wide, int64_t i) {
-    return wide ? static_cast<const int64_t*>(p)[i] : (int64_t) static_cast<const int32_t*>(p)[i];
-}
-
 __device__ __forceinline__ uint4 ld16(const void* p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
 
-// LPR lanes a row, 16 values a lane.
+// LPR lanes a row, 16 values a lane. a.per threads (a multiple of a warp) work on one token: each has a unit of the
+// rows' columns, whose cosines and sines it keeps for all heads that it turns. A row's reads go out a row before it
+// is worked on; the first of q, k and v before the angles.
 template <int FMT, int DT, bool INTERLEAVED, int LPR>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a) {
-    extern __shared__ float2 turn[];     // [tokens][pairs]: factor * (cos, sin)
+__global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const WriteArgs a) {
+    extern __shared__ float2 turn[];     // [tokens][8][pairs / 8]: factor * (cos, sin), a lane's 8 pairs a row apart (no bank twice)
     pdl_wait();
     pdl_trigger();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tpc;
-    const int tokens = (int)min((int64_t)a.tpc, a.T - t0);
-    const int half = a.rope.half;
+    const int tokens = kThreads / a.per, token = (int)threadIdx.x / a.per;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens, t = t0 + token;
+    const bool live = t < a.T;
+    const int half = a.rope.half, nch = a.D >> 3, turned = half >> 2;            // 16-byte pieces of a row, of its rotated part
+    const int lane = (int)threadIdx.x % LPR, heads = a.per / LPR * (int)gridDim.y;       // that are worked on at once
+    const int first = ((int)threadIdx.x % a.per) / LPR + (int)blockIdx.y * (a.per / LPR);
+    const bool rot = lane * 2 < turned;
+    // the lane's pieces of a rotated row (of another: 2 lane, 2 lane + 1)
+    const int c0 = INTERLEAVED || !rot ? 2 * lane : lane, c1 = INTERLEAVED || !rot ? 2 * lane + 1 : lane + (turned >> 1);
+
+    const bool on0 = live && c0 < nch, on1 = live && c1 < nch;
+    // The lane's two pieces of a row at p, the second `apart` values behind the first.
+    auto read = [&](const uint16_t* p, int apart, bool first_on, bool second_on, uint4& u, uint4& w) {
+        u = w = make_uint4(0, 0, 0, 0);
+        if (first_on) u = ld16(p);
+        if (second_on) w = ld16(p + apart);
+    };
+    const int apart = (c1 - c0) * 8;
+
     for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-        const int t = i / half;
-        const uint64_t phase = (uint64_t)load_index(a.rope.positions, a.rope.wide, t0 + t) * a.rope.freqs[i - t * half];
+        const int at = i / half;
+        if (t0 + at >= a.T) break;
+        const int pair = i - at * half;
+        const uint64_t phase = (uint64_t)load_index(a.rope.positions, a.rope.wide, t0 + at) * a.rope.freqs[pair];
         // half a turn is 1: sincospi's argument in [-1, 1)
         float s, c;
         sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-        turn[i] = make_float2(a.rope.factor * c, a.rope.factor * (a.rope.inverse ? -s : s));
+        turn[at * half + (pair & 7) * (half >> 3) + (pair >> 3)] = make_float2(a.rope.factor * c, a.rope.factor * (a.rope.inverse ? -s : s));
     }
     __syncthreads();
+    const float2* cs = turn + token * half + lane;
+    const int apart_cs = half >> 3;
+    auto rotate = [&](float (&u)[8], float (&w)[8]) {
+        if (!rot) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 e = cs[i * apart_cs];
+            float& p = INTERLEAVED ? (i < 4 ? u[2 * (i & 3)] : w[2 * (i & 3)]) : u[i];
+            float& o = INTERLEAVED ? (i < 4 ? u[2 * (i & 3) + 1] : w[2 * (i & 3) + 1]) : w[i];
+            const float x = p * e.x - o * e.y, y = p * e.y + o * e.x;
+            p = x;
+            o = y;
+        }
+    };
+    if (gridDim.z == 1 || blockIdx.z == 0) {
+        const uint16_t* x = a.q.p + t * a.q.ts + first * a.q.hs + c0 * 8;
+        uint16_t* y = a.qo.p + t * a.qo.ts + first * a.qo.hs + c0 * 8;
+        const int64_t xs = heads * a.q.hs, ys = heads * a.qo.hs;
+        for (int h = first; h < a.q.n; h += heads, x += xs, y += ys) {
+            uint4 r, e;
+            read(x, apart, on0, on1, r, e);
+            float u[8], w[8];
+            load8<DT>(r, u);
+            load8<DT>(e, w);
+            rotate(u, w);
+            st16_if(y, pack8<DT>(u), on0);
+            st16_if(y + apart, pack8<DT>(w), on1);
+        }
+    }
+    if (a.k.n == 0 || (gridDim.z > 1 && blockIdx.z == 0)) return;
 
-    const int D = a.D, nch = D >> 3, turned = half >> 2;         // 16-byte pieces of a row, of its rotated part
-    const int rows = a.q.n + 2 * a.k.n;
-    const int lane = threadIdx.x % LPR;
-    constexpr int kRows = kThreads / LPR;
-    const int total = tokens * rows;
-    for (int r0 = (int)blockIdx.y * kRows; r0 < total; r0 += (int)gridDim.y * kRows) {
-        const int at = r0 + (int)threadIdx.x / LPR;
-        const int t = min(at, total - 1) / rows, h = min(at, total - 1) - t * rows;
-        const bool is_q = h < a.q.n, is_k = !is_q && h < a.q.n + a.k.n;
-        int64_t slot = -1;
-        if (!is_q) slot = load_index(a.slots, a.wide, t0 + t);
-        const bool there = at < total && (is_q || (slot >= 0 && slot < a.c.pages * a.c.page.d));
-        const Heads& src = is_q ? a.q : is_k ? a.k : a.v;
-        const int head = is_q ? h : is_k ? h - a.q.n : h - a.q.n - a.k.n;
-        const uint16_t* x = src.p + (t0 + t) * src.ts + head * src.hs;
-        const bool rot = (is_q || is_k) && lane * 2 < turned;
-        const int c0 = INTERLEAVED || !rot ? 2 * lane : lane;
-        const int c1 = INTERLEAVED || !rot ? c0 + 1 : lane + (turned >> 1);
-        float u[8] = {}, w[8] = {};
-        if (there && c0 < nch) load8<DT>(ld16(x + c0 * 8), u);
-        if (there && c1 < nch) load8<DT>(ld16(x + c1 * 8), w);
-        if (rot) {
-            const float2* cs = turn + t * half + lane * 8;
+    const int64_t slot = live ? load_index(a.slots, a.wide, t) : -1;
+    const bool there = slot >= 0 && slot < a.c.pages * a.c.page.d;
+    int place = 0;
+    const int64_t page = there ? page_of_slot(slot, a.c.page, place) : 0;
+    // A row of 16 values a lane into the cache; every lane takes part in the shuffles.
+    constexpr int kPiece = FMT == FMT_PT ? 8 : 16;               // bytes of 8 values
+    auto put = [&](const float (&u)[8], const float (&w)[8], uint8_t* row, float* scale, int off, bool first_on, bool second_on, bool on) {
+        if (FMT != FMT_PT) {
+            st16_if(row, pack8<DT>(u), on && first_on);
+            st16_if(row + off * 2, pack8<DT>(w), on && second_on);
+            return;
+        }
+        float m = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 e = cs[i];
-                float& p = INTERLEAVED ? (i < 4 ? u[2 * (i & 3)] : w[2 * (i & 3)]) : u[i];
-                float& o = INTERLEAVED ? (i < 4 ? u[2 * (i & 3) + 1] : w[2 * (i & 3) + 1]) : w[i];
-                const float first = p * e.x - o * e.y, second = p * e.y + o * e.x;
-                p = first;
-                o = second;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(u[i]), fabsf(w[i])));
+        const float2 sr = per_token_scale(group_max<LPR>(m));
+        auto codes = [&](const float(&v)[8]) {
+            float f[8];
+            if (sr.x >= 0x1p-126f || sr.x == 0.0f) {             // the reciprocal is 0 for a scale of 0: every code is 0
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 q = div2_rn(make_float2(v[i], v[i + 1]), f2(-sr.x), f2(sr.y));
+                    f[i] = q.x;
+                    f[i + 1] = q.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(v[i], sr.x);
             }
-        }
-        if (is_q) {
-            uint16_t* y = a.qo.p + (t0 + t) * a.qo.ts + head * a.qo.hs;
-            st16_if(y + c0 * 8, pack8<DT>(u), there && c0 < nch);
-            st16_if(y + c1 * 8, pack8<DT>(w), there && c1 < nch);
-        }
-        if (FMT == FMT_PT) {             // every lane takes part in the shuffles
-            float m = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(u[i]), fabsf(w[i])));
-            m = group_max<LPR>(m);
-            if (!is_q && there) {
-                const int64_t page = slot / a.c.page.d, place = slot - page * a.c.page.d;
-                uint8_t* row = (is_k ? a.c.k : a.c.v) + page * a.c.ps + head * a.c.hs + place * a.c.ts;
-                const float2 sr = per_token_scale(m);
-                auto codes = [&](const float(&v)[8]) {
-                    float f[8];
-                    if (sr.x >= 0x1p-126f || sr.x == 0.0f) {     // the reciprocal is 0 for a scale of 0: every code is 0
-#pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const float2 q = div2_rn(make_float2(v[i], v[i + 1]), f2(-sr.x), f2(sr.y));
-                            f[i] = q.x;
-                            f[i + 1] = q.y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(v[i], sr.x);
-                    }
-                    return make_uint2(f32x4_to_e4m3x4(f[0], f[1], f[2], f[3]), f32x4_to_e4m3x4(f[4], f[5], f[6], f[7]));
-                };
-                st8_if(row + c0 * 8, codes(u), c0 < nch);
-                st8_if(row + c1 * 8, codes(w), c1 < nch);
-                st_f32_if((is_k ? a.c.ks : a.c.vs) + (page * a.c.heads + head) * a.c.page.d + place, sr.x, lane == 0);
-            }
-        } else if (!is_q && there) {
-            const int64_t page = slot / a.c.page.d, place = slot - page * a.c.page.d;
-            uint8_t* row = (is_k ? a.c.k : a.c.v) + page * a.c.ps + head * a.c.hs + place * a.c.ts;
-            st16_if(row + c0 * 16, pack8<DT>(u), c0 < nch);
-            st16_if(row + c1 * 16, pack8<DT>(w), c1 < nch);
-        }
+            return make_uint2(f32x4_to_e4m3x4(f[0], f[1], f[2], f[3]), f32x4_to_e4m3x4(f[4], f[5], f[6], f[7]));
+        };
+        st8_if(row, codes(u), on && first_on);
+        st8_if(row + off, codes(w), on && second_on);
+        st_f32_if(scale, sr.x, on && lane == 0);
+    };
+    const bool v0 = live && 2 * lane < nch, v1 = live && 2 * lane + 1 < nch;
+    for (int h = first; h - first < a.k.n; h += heads) {         // the same number of turns for all lanes
+        const bool on = there && h < a.k.n;
+        uint4 k0, k1, w0, w1;
+        read(a.k.p + t * a.k.ts + h * a.k.hs + c0 * 8, apart, on && on0, on && on1, k0, k1);
+        read(a.v.p + t * a.v.ts + h * a.v.hs + lane * 16, 8, on && v0, on && v1, w0, w1);
+        const int64_t row = page * a.c.ps + h * a.c.hs + place * a.c.ts, scale = (page * a.c.heads + h) * a.c.page.d + place;
+        float u[8], w[8];
+        load8<DT>(k0, u);
+        load8<DT>(k1, w);
+        rotate(u, w);
+        put(u, w, a.c.k + row + c0 * kPiece, a.c.ks + scale, apart, on0, on1, on);
+        load8<DT>(w0, u);
+        load8<DT>(w1, w);
+        put(u, w, a.c.v + row + lane * 2 * kPiece, a.c.vs + scale, 8, v0, v1, on);
     }
 }
 
@@ -141,20 +165,23 @@ auto pick(int lpr, bool interleaved) {
 cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& dev, const WriteArgs& w, cudaStream_t stream) {
     WriteArgs a = w;
     const int units = (a.D + 15) / 16, lpr = units <= 4 ? 4 : units <= 8 ? 8 : 16;
-    const int rows = a.q.n + 2 * a.k.n, per = kThreads / lpr;
-    // Few tokens: a CTA for each pass over a token's rows, so that none waits for another; many: a
-    // CTA walks over the rows of a token, or of several narrow ones, and shares their angles.
+    const int most = a.q.n > a.k.n ? a.q.n : a.k.n;
+    // Few tokens: as many threads a token as it has heads, in several CTAs where they do not fit in one, so that none waits for another;
+    // many: two warps a token, whose lanes keep the angles for several heads.
     const int sms = dev.sms > 0 ? dev.sms : 152;
     int split = 1;
-    a.tpc = 1;
-    if (a.T < 4 * (int64_t)sms) split = (rows + per - 1) / per;
-    else while (a.tpc < 8 && a.tpc * rows < 4 * per && a.T >= 16 * (int64_t)sms * a.tpc) a.tpc *= 2;
-    const int64_t ctas = (a.T + a.tpc - 1) / a.tpc;
+    a.per = 64;
+    if (a.T < 8 * (int64_t)sms) {
+        while (a.per < kThreads && a.per / lpr < most) a.per *= 2;
+        if (a.T < 2 * (int64_t)sms) split = (most + a.per / lpr - 1) / (a.per / lpr);
+    }
+    const int tokens = kThreads / a.per;
+    const int64_t ctas = (a.T + tokens - 1) / tokens;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const int smem = a.tpc * a.rope.half * (int)sizeof(float2);
+    const int smem = tokens * a.rope.half * (int)sizeof(float2);
     const auto k = fmt == FMT_PT ? (dt == DT_F16 ? pick<FMT_PT, DT_F16>(lpr, interleaved) : pick<FMT_PT, DT_BF16>(lpr, interleaved))
                                  : (dt == DT_F16 ? pick<FMT_16BIT, DT_F16>(lpr, interleaved) : pick<FMT_16BIT, DT_BF16>(lpr, interleaved));
-    return launch_grid(k, dim3((unsigned)ctas, (unsigned)split), kThreads, smem, 1, dev.id, a, stream);
+    return launch_grid(k, dim3((unsigned)ctas, (unsigned)split, (unsigned)(a.q.n > 0 && a.k.n > 0 && a.T < 2 * (int64_t)sms ? 2 : 1)), kThreads, smem, 1, dev.id, a, stream);
 }
 
 }  // namespace sgq
