@@ -33,6 +33,7 @@
 #pragma once
 
 #include "sgq_cache.cuh"
+#include "sgq_tc.cuh"
 
 namespace sgq {
 namespace attend {
@@ -57,26 +58,31 @@ struct Shape {
     static constexpr int halves = rows / 16;
     static constexpr uint32_t full = rows == 32 ? 0xFFFFFFFFu : 0xFFFFu;         // the mask of rows that are all there
     static constexpr int elem = fp8 ? 1 : 2;
-    static constexpr int pieces = DP * elem / 16;                // 16-byte pieces of a row
-    // Rows in shared memory: 8 rows' pieces meet no bank twice, by 16 bytes between rows or, E4M3 rows of 128 and 256, by the
-    // pieces' order (see piece_at).
-    static constexpr bool swizzled = fp8 && DP >= 128;
-    static constexpr int stride = DP * elem + (swizzled ? 0 : 16);
-    static constexpr int slot = 2 * rows * stride + (fp8 ? 2 * rows * 4 : 0);
+    // Rows in shared memory: blocks of 128 bytes (64: narrow E4M3 heads) of all rows, their 16-byte pieces in the order
+    // that the copy engine's swizzle gives them.
+    static constexpr int block = DP * elem < 128 ? 64 : 128, blocks = DP * elem / block;
+    static constexpr int half = rows * DP * elem, slot = 2 * half;               // k's rows, and v's behind them
+    static constexpr int scales = fp8 ? 2 * rows * 4 : 0;
     static constexpr int step = kParts * slot;                   // bytes of a tile: its parts' slots side by side
     // CTAs a multiprocessor at most. Three CTAs that each take a short item hide one another's beginnings (64 sequences up to 4096, bf16:
     // 82 us, with two 89); CTAs that take long shares are two, but for narrow E4M3 rows, which are bound by
     // instructions (4 sequences of 32768, D 64: 50 us with two, 33 with three).
     static constexpr int ctas = DP == 256 ? (fp8 && CG == 1 ? 2 : 1) : CG > 1 ? 1 : NT > 1 ? 2 : DIRECT || (fp8 && DP == 64) ? 3 : 2;
     // Tiles that fit in shared memory where n CTAs share a multiprocessor.
-    static constexpr int fit(int n) { return (227 * 1024 / n - 3072) / step; }
+    static constexpr int bytes(int n) { return n * (step + kParts * scales) + 1024; }    // dynamic shared memory of n tiles
+    static constexpr int fit(int n) { return (227 * 1024 / n - 4096) / (step + kParts * scales); }
     static constexpr int parts = KIND == FP8_BF16 ? 1 : 2;       // 16-bit parts of p
-    static constexpr int line = (DP + 4) * 4;                    // bytes of a column's sums: 4 lanes' columns meet no bank twice
+    // bytes of a column's sums: 4 lanes' columns meet no bank twice, where a slot has room for that
+    static constexpr int line = (DP + (8 * (DP + 4) * 4 <= slot ? 4 : 0)) * 4;
     static constexpr int at_once = slot / (8 * line) < CG ? slot / (8 * line) : CG;      // groups of columns whose sums pass through a slot
     static_assert(at_once >= 1 && CG % at_once == 0 && fit(ctas) >= 2, "");
-    // Where piece p of row r lies, from the row's beginning. E4M3: a quarter of a warp reads 4 pieces of rows r, r + 1 (k), or 2 pieces of
-    // rows r, r + 2, r + 4, r + 6 (v).
-    static __device__ __forceinline__ int piece_at(int r, int p) { return (swizzled ? p ^ ((r & 6) ^ ((r & 1) << 2)) : p) * 16; }
+    // Where piece p (of 16 bytes) of row r lies, from the first row's beginning: two bits of the row, or three, turn the
+    // pieces' order. Eight rows' pieces of one number meet no bank twice; of E4M3 k rows, read four pieces of two rows at a time, two do.
+    static __device__ __forceinline__ int piece_at(int r, int p) {
+        return block == 64 ? r * 64 + ((p << 4) ^ turn(r)) : (p >> 3) * (rows * 128) + r * 128 + (((p & 7) << 4) ^ turn(r));
+    }
+    static __device__ __forceinline__ int turn(int r) { return block == 64 ? ((r >> 1) & 3) << 4 : (r & 7) << 4; }
+    static constexpr int pieces = DP * elem / 16;                // of a row
 };
 
 template <bool BF>
@@ -137,23 +143,23 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
         : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                 ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// An arrival of this thread, one of those that the barrier counts, once its own copies have landed.
+__device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
 
 __device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
-}
-
-// Until at most n of this thread's copy groups are pending (n at least 1).
-__device__ __forceinline__ void wait_but(int n) {
-    if (n == 1) cp_async_wait<1>();
-    else if (n == 2) cp_async_wait<2>();
-    else if (n == 3) cp_async_wait<3>();
-    else if (n == 4) cp_async_wait<4>();
-    else if (n == 5) cp_async_wait<5>();
-    else if (n == 6) cp_async_wait<6>();
-    else cp_async_wait<7>();
 }
 
 // floor(log2 s) of a scale, held inside +-100; zero and what is not finite included.
@@ -201,6 +207,8 @@ __device__ __forceinline__ void store4(uint16_t* to, float4 y, float f) {
                                                   : make_uint2(f32x2_to_f16x2(y.x * f, y.y * f), f32x2_to_f16x2(y.z * f, y.w * f));
 }
 
+static __device__ uint32_t gave_up;   // CTAs in which a wait ran out of time
+
 // Stores of one CTA of a cluster, read by another.
 __device__ __forceinline__ uint32_t in_cta(uint32_t at, uint32_t rank) {
     uint32_t r;
@@ -222,12 +230,16 @@ __device__ __forceinline__ float ld_cluster4(uint32_t at) {
 
 // DIRECT: a cluster of a.split CTAs takes one item, each an equal run of its tiles. Else CTAs take shares of all tiles.
 template <int KIND, int DP, int CG, int NT, bool DIRECT>
-__global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shape<KIND, DP, CG, NT, DIRECT>::ctas) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shape<KIND, DP, CG, NT, DIRECT>::ctas) attend_kernel(const __grid_constant__ AttendArgs a) {
     using S = Shape<KIND, DP, CG, NT, DIRECT>;
     constexpr bool kF8 = S::fp8, kBf = KIND == BF16;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     constexpr int kSteps = DP / 16, kCols = CG * NT * 8, kThreads = S::threads;
-    extern __shared__ __align__(16) uint8_t tiles[];
+    extern __shared__ uint8_t raw[];
+    uint8_t* const tiles = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);      // the swizzle goes by 1024 bytes
+    __shared__ uint64_t s_bar[kParts][kStages];                  // a tile's copies have landed
+    __shared__ uint32_t s_stop;                                  // a wait ran out of time
+    volatile uint32_t* const stop = &s_stop;
     __shared__ int sum_part[S::warps];
     __shared__ int share_b, share_n, share_off;
     __shared__ float s_m[kParts][kCols], s_l[kParts][kCols];
@@ -239,6 +251,17 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + part), "n"(CG * 32) : "memory");
     };
 
+    if (threadIdx.x < kParts * kStages) {
+        if (threadIdx.x == 0) s_stop = 0;
+        // the copy engine's, and each lane's own
+        tc::bar_init(tc::smem_addr(&s_bar[0][0] + threadIdx.x), 33);
+        tc::fence_barrier_init();
+    }
+    if (a.boxes && threadIdx.x == 0) {
+        tc::prefetch_map(&a.km);
+        tc::prefetch_map(&a.vm);
+    }
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
 
@@ -324,18 +347,20 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         if (ahead) next_n = w.b + 1 < a.B ? a.lengths[w.b + 1] : 0;
     };
 
-    // Copying. Where pages are whole multiples of 16 tokens, 16 tokens have one page and lie
-    // a stride apart; else each lane finds its own token's row.
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tiles) + part * S::slot;
+    // Copying, by the first warp of each group, in one of two ways. a.boxes, where pages are whole multiples of 16 tokens: boxes of 16 tokens by 128
+    // bytes, which the copy engine brings while the warp computes. Else 16 bytes a lane and instruction, each lane with the rows of
+    // its own token's page: their issue keeps the warp from computing, 700 cycles a tile and more the more of them are under way, but
+    // boxes as small as odd pages allow take longer. (8 sequences of 65536, bf16: 271 us by boxes, 288 by lanes; 32 of 8192,
+    // pages of one token: 248 by boxes of one, 136 by lanes.)
+    const uint32_t base = tc::smem_addr(tiles) + part * S::slot;
     __shared__ uint32_t s_mask[kParts][kStages];
-    const bool even = (a.c.page.d & 15) == 0;
+    auto scales_at = [&](int slot) { return tc::smem_addr(tiles) + a.stages * S::step + (slot * kParts + part) * S::scales; };
+    auto bar_at = [&](int slot) { return tc::smem_addr(&s_bar[part][slot]); };
     const int64_t v_from_k = a.c.v - a.c.k;
     constexpr int kRowsAt = 32 / S::pieces > 0 ? 32 / S::pieces : 1;              // rows that 32 lanes copy at once
     const int lane_row = kRowsAt > 1 ? lane / S::pieces : 0, piece = lane % S::pieces;
     const bool used = piece * 16 < a.c.D * S::elem;              // columns from D on are filled with zeros
-    const uint32_t lane_to = (lane_row + cg * kRowsAt) * S::stride;
-    const int lane_piece = S::piece_at(lane_row, piece) ^ S::piece_at(cg * kRowsAt, 0);      // turn i's: ^ piece_at(i * kRowsAt, 0)
-    const int64_t lane_from = lane_row * a.c.ts + (used ? piece * 16 : 0), row_step = kRowsAt * a.c.ts;
+    const int lane_piece = S::piece_at(lane_row, piece);
     // the lane's token of w's tile (of 16 tokens both halves of a warp have the same)
     auto token_of = [&](const W& w) { return w.start + w.tile * S::tokens + part * S::rows + (lane & (S::rows - 1)); };
     auto page_of = [&](const W& w, int on = 0) {                 // of the lane's token, `on` tiles on; -1 where it is masked
@@ -343,69 +368,55 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         if (t < w.lo || t >= w.n) return -1;
         return a.table[w.b * a.width + quotient(t, a.c.page)];
     };
-    // Copies w's tile into a slot, the group's warps each their share; pid: page_of(w), asked for a tile before.
+    // Copies w's tile into a slot; pid: page_of(w), asked for a tile before. Masked rows of a box come with it.
     auto copy = [&](const W& w, int slot, int pid) {
-        const uint32_t at = base + slot * S::step;
+        const uint32_t at = base + slot * S::step, bar = bar_at(slot);
         const int t = token_of(w);
         const bool there = pid >= 0 && pid < a.c.pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & S::full;
-        if (lane == 0 && cg == 0) s_mask[part][slot] = mask;
         const int place = t - (int)(quotient(t, a.c.page) * a.c.page.d);
-        constexpr int kTurns = 16 / kRowsAt;                     // of 16 tokens
-        if (even) {
-            // a token of the 16 that is there has their page
-            const int h0 = S::rows == 32 ? lane & 16 : 0;
-            const uint32_t some0 = (mask >> h0) & 0xFFFFu;
-            const int p = __shfl_sync(0xFFFFFFFFu, pid, h0 + (some0 ? __ffs(some0) - 1 : 0)), first = __shfl_sync(0xFFFFFFFFu, place, h0);
-            const int64_t off = (int64_t)(some0 ? p : 0) * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)first * a.c.ts;
+        if (lane == 0) {
+            s_mask[part][slot] = mask;
+            const int n = a.boxes ? ((mask & 0xFFFFu) ? 1 : 0) + ((mask >> 16) ? 1 : 0) : 0;
+            tc::bar_arrive_expect(bar, n * 16 * 2 * DP * S::elem);
+        }
+        __syncwarp();
+        if (a.boxes) {
+            // of 16 tokens in one page: the page, the place of the first
 #pragma unroll
             for (int h = 0; h < S::halves; ++h) {
                 const uint32_t some = (mask >> (16 * h)) & 0xFFFFu;
-                const uint8_t* k = a.c.k + ((S::halves > 1 ? __shfl_sync(0xFFFFFFFFu, off, 16 * h) : off) + lane_from + cg * row_step);
-                uint32_t to = at + h * 16 * S::stride + lane_to;
-                if (some == 0xFFFFu) {
+                const int page = __shfl_sync(0xFFFFFFFFu, pid, 16 * h + (some ? __ffs(some) - 1 : 0)), y = __shfl_sync(0xFFFFFFFFu, place, 16 * h);
+                if (some && tc::elect()) {
 #pragma unroll
-                    for (int i = 0; i < kTurns; i += CG) {
-                        if (kTurns % CG == 0 || i + cg < kTurns) {
-                            const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
-                            copy16(x, k, used);
-                            copy16(x + S::rows * S::stride, k + v_from_k, used);
-                        }
-                        k += CG * row_step;
-                        to += CG * kRowsAt * S::stride;
-                    }
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i + cg < kTurns; i += CG) {
-                        const bool ok = used && ((some >> ((i + cg) * kRowsAt + lane_row)) & 1);
-                        const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
-                        copy16(x, ok ? k : a.c.k, ok);
-                        copy16(x + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
-                        k += CG * row_step;
-                        to += CG * kRowsAt * S::stride;
+                    for (int b = 0; b < S::blocks; ++b) {
+                        const uint32_t to = at + b * S::rows * S::block + h * 16 * S::block;
+                        load_4d(to, &a.km, bar, b * S::block, y, w.head, page);
+                        load_4d(to + S::half, &a.vm, bar, b * S::block, y, w.head, page);
                     }
                 }
             }
         } else {
             const int64_t off = there ? (int64_t)pid * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)place * a.c.ts : 0;
-            uint32_t to = at + lane_to;
-#pragma unroll 4
-            for (int i = 0; i + cg < S::rows / kRowsAt; i += CG) {
-                const int row = (i + cg) * kRowsAt + lane_row;
-                const uint32_t x = to + (lane_piece ^ S::piece_at(i * kRowsAt, 0));
+#pragma unroll
+            for (int i = 0; i < S::rows / kRowsAt; ++i) {
+                const int row = i * kRowsAt + lane_row;
                 const bool ok = used && ((mask >> row) & 1);
-                const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + (used ? piece * 16 : 0);
-                copy16(x, ok ? k : a.c.k, ok);
-                copy16(x + S::rows * S::stride, ok ? k + v_from_k : a.c.k, ok);
-                to += CG * kRowsAt * S::stride;
+                const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + piece * 16;
+                const uint32_t to = at + i * kRowsAt * S::block + (lane_piece ^ S::turn(i * kRowsAt));
+                copy16(to, ok ? k : a.c.k, ok);
+                copy16(to + S::half, ok ? k + v_from_k : a.c.k, ok);
             }
         }
-        if (kF8 && cg == CG - 1 && lane < S::rows) {
-            const int64_t row = there ? ((int64_t)pid * a.c.heads + w.head) * a.c.page.d + place : 0;
-            const uint32_t to = at + 2 * S::rows * S::stride + lane * 4;
-            copy4(to, a.c.ks + row, there);
-            copy4(to + S::rows * 4, a.c.vs + row, there);
+        if (kF8) {
+            if (lane < S::rows) {
+                const int64_t row = there ? ((int64_t)pid * a.c.heads + w.head) * a.c.page.d + place : 0;
+                const uint32_t to = scales_at(slot) + lane * 4;
+                copy4(to, a.c.ks + row, there);
+                copy4(to + S::rows * 4, a.c.vs + row, there);
+            }
         }
+        arrive_with_copies(bar);
     };
 
     // q of the current item as the right operand of S, and the factors of its columns: asked for, then made ready.
@@ -469,8 +480,17 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
 
     auto tile = [&](int slot) {
         constexpr int H = S::halves;
-        const uint32_t at = base + slot * S::step, vt = at + S::rows * S::stride, sc = vt + S::rows * S::stride;
+        const uint32_t at = base + slot * S::step, vt = at + S::half, sc = kF8 ? scales_at(slot) : 0;
         const uint32_t mask = s_mask[part][slot];
+        if (mask != S::full) {                       // what masked rows of v hold is multiplied by 0: it has to be a number
+            if (cg == 0)
+                for (int i = lane; i < S::half / 16; i += 32) {
+                    const int r = i * 16 / S::block % S::rows;
+                    if (!((mask >> r) & 1)) sts16(vt + i * 16, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+                }
+            tc::fence_async_smem();                  // before the copies that come here next
+            group_sync();
+        }
         // S, in two chains of products a tile of 16 by 8
         float x[H][NT][4];
 #pragma unroll
@@ -481,19 +501,18 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[h][nt][i] = x2[nt][i] = 0.0f;
             if (!kF8) {
-                const uint32_t from = at + (lane & 15) * S::stride + (lane >> 4) * 16;
 #pragma unroll
                 for (int kk = 0; kk < kSteps; ++kk) {
                     uint32_t k[4];
-                    ldmatrix4(k, from + kk * 32);
+                    ldmatrix4(k, at + S::piece_at(lane & 15, kk * 2 + (lane >> 4)));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma<kBf>(kk & 1 ? x2[nt] : x[h][nt], k, qf[kk][nt][0], qf[kk][nt][1]);
                 }
             } else {
 #pragma unroll
                 for (int blk = 0; blk < DP / 64; ++blk) {
-                    const uint32_t from = at + (h * 16 + g) * S::stride + S::piece_at(g, blk * 4 + c);
-                    const uint4 p = lds16(from), q = lds16(from + 8 * S::stride);
+                    const uint32_t from = at + S::piece_at(h * 16 + g, blk * 4 + c);
+                    const uint4 p = lds16(from), q = lds16(from + 8 * S::block);
                     const uint32_t up[4] = {p.x, p.y, p.z, p.w}, dn[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -598,11 +617,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 }
             if (!kF8) {
                 // 8 x 8 pieces of V^T: tokens 0-7 by columns 0-7, columns 8-15, then tokens 8-15
-                const uint32_t from = vt + ((lane & 7) + (lane >> 4) * 8) * S::stride + ((lane >> 3) & 1) * 16;
+                const int row = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     uint32_t v[4];
-                    ldmatrix4t(v, from + i * 32);
+                    ldmatrix4t(v, vt + S::piece_at(row, i * 2 + ((lane >> 3) & 1)));
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -615,8 +634,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                     uint32_t v[4][4];                            // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const int row = 2 * c + (t & 1);
-                        const uint32_t from = vt + (h * 16 + row + (t >> 1) * 8) * S::stride + (kWords == 4 ? S::piece_at(row, blk * 8 + g) : g * 8);
+                        const int row = h * 16 + 2 * c + (t & 1) + (t >> 1) * 8;
+                        const uint32_t from = vt + (kWords == 4 ? S::piece_at(row, blk * 8 + g) : S::piece_at(row, g >> 1) + (g & 1) * 8);
                         if (kWords == 4) {
                             const uint4 q = lds16(from);
                             v[t][0] = q.x, v[t][1] = q.y, v[t][2] = q.z, v[t][3] = q.w;
@@ -680,6 +699,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                         const int d = kF8 ? (i >> 3) * 128 + g * kSide + 2 * (i & 7) + r : i * 16 + g + 8 * r;
                         sts_f32(own + col * S::line + d * 4, o[i][nt][e]);
                     }
+                tc::fence_async_smem();                          // before the copies that come here next
             }
             __syncthreads();
             const int at = threadIdx.x / kEach, col = ((round * S::at_once + (at >> 3)) * NT + nt) * 8 + (at & 7), q = w.chunk * kCols + col;
@@ -734,13 +754,15 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     // Turn i copies tile i and computes tile i - a.stages, whose slot that is: copies run ahead, a
     // commit group each (empty behind the last). One loop, so that the copying's code is there once.
     ask_q(cu);
+    const bool copies = cg == 0;
+    uint32_t parity = 1;                                         // of the slots' barriers: 0 the first time round
     // a tile's pages are asked for a tile before its copy; where all tiles are one item's, two
-    int pid = left > 0 ? page_of(ld) : -1, pid2 = DIRECT && left > 1 ? page_of(ld, 1) : -1, todo = count, slot = 0;
+    int pid = copies && left > 0 ? page_of(ld) : -1, pid2 = DIRECT && copies && left > 1 ? page_of(ld, 1) : -1, todo = count, slot = 0;
     bool fresh = true, begun_here = cu.tile == 0;                // the item's first tile here; whether it is the item's first
     for (int turn = 0; todo > 0; ++turn) {
         if (turn >= a.stages) {
-            wait_but(a.stages - 1);
-            group_sync();
+            tc::bar_wait(bar_at(slot), parity, stop);
+            __syncwarp();
             if (fresh) {
                 ready_q();
                 clear();
@@ -773,7 +795,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             }
             group_sync();
         }
-        if (left > 0) {
+        if (copies && left > 0 && !*stop) {
             copy(ld, slot, pid);
             if (--left > 0) {
                 advance(ld, true);
@@ -784,12 +806,22 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 pid2 = left > 1 ? page_of(ld, 1) : -1;
             }
         }
-        cp_async_commit();
-        slot = slot + 1 == a.stages ? 0 : slot + 1;
+        if (++slot == a.stages) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+    if (*stop) {
+        // Out of time: what was computed since is no result. The last copies get as long again, so that none lands behind this CTA's end.
+        uint32_t none = 0;
+        if (copies)
+            for (int s = 0; s < a.stages; ++s)
+                for (uint32_t p = 0; p < 2; ++p) tc::bar_wait(bar_at(s), p, &none);
+        __syncthreads();
+        if (threadIdx.x == 0) atomicAdd(&gave_up, 1);
     }
     if (fresh) clear();                                          // a CTA of a cluster that had no tile
     if (!DIRECT) return;
-    cp_async_wait<0>();
     __syncthreads();
     flush(cu, 0, true, true);
     if (a.split == 1) return;
@@ -902,6 +934,10 @@ template <int KIND, int DP, int CG, int NT>
 cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t stream) {
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     AttendArgs a = args;
+    using Any = Shape<KIND, DP, CG, NT, true>;
+    a.boxes = a.c.page.d % 16 == 0;
+    if (a.boxes && (!encode_cache(&a.km, a.c, a.c.k, Any::block, Any::elem) || !encode_cache(&a.vm, a.c, a.c.v, Any::block, Any::elem)))
+        return cudaErrorInvalidValue;
     const int64_t sms = dev.sms > 0 ? dev.sms : 152;
     if (a.split > 0) {
         using S = Shape<KIND, DP, CG, NT, true>;
@@ -912,7 +948,7 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
         const int need = (a.tiles + a.split - 1) / a.split;
         a.stages = S::fit(each) < most ? S::fit(each) : most;
         if (a.stages > need) a.stages = need < 2 ? 2 : need;
-        return launch_grid(attend_kernel<KIND, DP, CG, NT, true>, dim3((unsigned)ctas), S::threads, a.stages * S::step, a.split, dev.id, a, stream);
+        return launch_grid(attend_kernel<KIND, DP, CG, NT, true>, dim3((unsigned)ctas), S::threads, S::bytes(a.stages), a.split, dev.id, a, stream);
     }
     using S = Shape<KIND, DP, CG, NT, false>;
     // Two tiles ahead, three where one CTA fills a multiprocessor: three are worse (8 sequences up to 131072, E4M3: 345 and 291 us; bf16 of 65536: 292 and 288).
@@ -924,7 +960,7 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
     // where no item has two tiles no two CTAs share one
     const int64_t items = (int64_t)a.B * a.items;
     a.joined = a.tiles <= 1 ? 0 : items <= 64 ? kByItem : kByCta;
-    const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, NT, false>, dim3((unsigned)ctas), S::threads, a.stages * S::step, 1, dev.id, a, stream);
+    const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, NT, false>, dim3((unsigned)ctas), S::threads, S::bytes(a.stages), 1, dev.id, a, stream);
     if (e != cudaSuccess || !a.joined) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.joined == kByItem ? items : ctas), (unsigned)(a.group < CG * NT * 8 ? a.group : CG * NT * 8));
@@ -940,7 +976,7 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
 
 template <int KIND>
 cudaError_t launch_kind(const Device& dev, const AttendArgs& a, cudaStream_t stream) {
-    const int DP = attend_padded(a.c.D), cols = attend_columns(a.group, DP);
+    const int DP = a.DP, cols = attend_columns(a.group, DP);
     // 16 columns: two tiles of 8 a warp, so that each row is read and widened once. Heads of 256 have no
     // registers for that, but for 32 columns' two warps side by side.
     if (DP == 64) return cols == 8 ? launch<KIND, 64, 1, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 64, 1, 2>(dev, a, stream) : launch<KIND, 64, 2, 2>(dev, a, stream);
@@ -948,10 +984,16 @@ cudaError_t launch_kind(const Device& dev, const AttendArgs& a, cudaStream_t str
     return cols == 8 ? launch<KIND, 256, 1, 1>(dev, a, stream) : launch<KIND, 256, 2, 1>(dev, a, stream);
 }
 
+inline cudaError_t read_gave_up(uint32_t* n) { return cudaMemcpyFromSymbol(n, gave_up, sizeof *n); }
+
 cudaError_t launch_bf16(const Device& dev, const AttendArgs& a, cudaStream_t stream);
+cudaError_t gave_up_bf16(uint32_t* n);
 cudaError_t launch_f16(const Device& dev, const AttendArgs& a, cudaStream_t stream);
+cudaError_t gave_up_f16(uint32_t* n);
 cudaError_t launch_fp8_bf16(const Device& dev, const AttendArgs& a, cudaStream_t stream);
+cudaError_t gave_up_fp8_bf16(uint32_t* n);
 cudaError_t launch_fp8_f16(const Device& dev, const AttendArgs& a, cudaStream_t stream);
+cudaError_t gave_up_fp8_f16(uint32_t* n);
 
 }  // namespace attend
 }  // namespace sgq

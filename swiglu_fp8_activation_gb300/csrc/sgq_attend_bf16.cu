@@ -7,4 +7,6 @@ cudaError_t attend::launch_bf16(const Device& dev, const AttendArgs& a, cudaStre
     return launch_kind<BF16>(dev, a, stream);
 }
 
+cudaError_t attend::gave_up_bf16(uint32_t* n) { return read_gave_up(n); }
+
 }  // namespace sgq

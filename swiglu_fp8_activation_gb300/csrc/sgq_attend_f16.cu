@@ -7,4 +7,6 @@ cudaError_t attend::launch_f16(const Device& dev, const AttendArgs& a, cudaStrea
     return launch_kind<F16>(dev, a, stream);
 }
 
+cudaError_t attend::gave_up_f16(uint32_t* n) { return read_gave_up(n); }
+
 }  // namespace sgq

@@ -7,4 +7,6 @@ cudaError_t attend::launch_fp8_bf16(const Device& dev, const AttendArgs& a, cuda
     return launch_kind<FP8_BF16>(dev, a, stream);
 }
 
+cudaError_t attend::gave_up_fp8_bf16(uint32_t* n) { return read_gave_up(n); }
+
 }  // namespace sgq

@@ -7,4 +7,6 @@ cudaError_t attend::launch_fp8_f16(const Device& dev, const AttendArgs& a, cudaS
     return launch_kind<FP8_F16>(dev, a, stream);
 }
 
+cudaError_t attend::gave_up_fp8_f16(uint32_t* n) { return read_gave_up(n); }
+
 }  // namespace sgq

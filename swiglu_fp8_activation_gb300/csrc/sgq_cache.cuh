@@ -90,6 +90,7 @@ struct ReadArgs {
 };
 
 struct AttendArgs {
+    CUtensorMap km, vm;  // of the cache's rows
     CacheArgs c;
     Heads q;
     const int32_t* table;
@@ -109,7 +110,9 @@ struct AttendArgs {
     int joined;          // how a second launch finds what several CTAs have computed; 0 for none
     int split;           // CTAs of a cluster, where each takes one item; 0 for shares
     int tiles;           // of the longest item
+    int DP;              // attend_padded's width
     int stages;          // tiles copied ahead
+    int boxes;           // whether the copy engine brings the rows
 };
 
 // Most CTAs that take shares of one paged_attention, for which its workspace has room.
@@ -126,11 +129,17 @@ constexpr int64_t attend_tiles(bool fp8, int DP, int64_t limit, int64_t window) 
     if (window > 0 && limit > window + tokens - 1) limit = window + tokens - 1;
     return limit <= tokens ? 1 : (limit + tokens - 1) / tokens;
 }
-// CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles.
-constexpr int attend_split(int64_t items, int64_t tiles) {
+// CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles. A cluster needs no workspace
+// and no second launch, and the device gives its multiprocessors the next item as they come free; but it is 8 CTAs at most, and where
+// few long items are to be taken, some multiprocessors end long before others. The host knows the table's width alone: up to 8
+// tiles a CTA, or 16 where four rounds of CTAs even that out. (Times in a graph, clusters and shares: 1 sequence of 4000, 8 heads: 10.4
+// and 9.1 us, but 5 us of the host's time less; 256 up to 300: 33 and 44; 64 up to 4096: 81 and 85; 32 up to 8192, 4 heads with groups of
+// 16: 84 and 72.)
+constexpr int attend_split(int64_t items, int64_t tiles, int cols) {
     int split = 1;
     while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * 16)) split *= 2;
-    return tiles <= split * 16 && items * split <= 0x7FFFFFFF ? split : 0;
+    const int64_t each = (tiles + split - 1) / split, ctas = items * split;
+    return (each <= 8 || (each <= 16 && cols == 8 && ctas >= 1824)) && ctas <= 0x7FFFFFFF ? split : 0;
 }
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }
@@ -145,6 +154,12 @@ __host__ __device__ constexpr int attend_header_bytes() { return kAttendCtas * (
 
 cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& dev, const WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(int fmt, int dt, const Device& dev, const ReadArgs& a, cudaStream_t stream);
+// Boxes of 16 tokens by `block` bytes of the rows of k or v, in the order of that block's swizzle, zeros outside a row. False when the
+// driver refuses the strides.
+bool encode_cache(CUtensorMap* m, const CacheArgs& c, const void* rows, int block, int elem);
+
 cudaError_t launch_attend(int fmt, int dt, const Device& dev, const AttendArgs& a, cudaStream_t stream);
+// CTAs of paged_attention on the current device in which a wait ran out of time (waits for the device).
+cudaError_t attend_gave_up(uint32_t* n);
 
 }  // namespace sgq

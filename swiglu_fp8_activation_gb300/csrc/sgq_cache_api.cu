@@ -148,7 +148,7 @@ int fmt_of(int fmt) { return fmt == SGQ_FMT_FP8_PER_TOKEN ? (int)FMT_PT : FMT_16
 
 // How paged_attention's items are cut: false when a size is out of range.
 struct AttendPlan {
-    int cols, chunks, split;
+    int DP, cols, chunks, split;
     int64_t items, tiles;            // of a sequence; of the longest item
 };
 
@@ -157,11 +157,13 @@ bool plan_attend(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64
         D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size || window < 0)
         return false;
     const int64_t group = Hq / heads;
-    p->cols = attend_columns((int)group, attend_padded((int)D));
+    const bool fp8 = fmt == SGQ_FMT_FP8_PER_TOKEN;
+    p->DP = attend_padded((int)D);
+    p->cols = attend_columns((int)group, p->DP);
     p->chunks = (int)((group + p->cols - 1) / p->cols);
     p->items = heads * p->chunks;
-    p->tiles = attend_tiles(fmt == SGQ_FMT_FP8_PER_TOKEN, attend_padded((int)D), width * page_size, window);
-    p->split = attend_split(B * p->items, p->tiles);
+    p->tiles = attend_tiles(fp8, p->DP, width * page_size, window);
+    p->split = attend_split(B * p->items, p->tiles, p->cols);
     return B * p->items * p->tiles <= 0x7FFFFFFF;        // counted in 32 bits
 }
 
@@ -268,7 +270,7 @@ int64_t sgq_attention_workspace_bytes(int fmt, int64_t B, int64_t Hq, int64_t he
     AttendPlan p;
     if (!plan_attend(fmt, B, Hq, heads, D, width, page_size, window, &p) || p.split > 0) return 0;
     const int64_t most = B * p.items * p.tiles, ctas = most < kAttendCtas ? most : kAttendCtas;
-    return attend_header_bytes() + ctas * 2 * attend_part(p.cols, attend_padded((int)D)) * 4;
+    return attend_header_bytes() + ctas * 2 * attend_part(p.cols, p.DP) * 4;
 }
 
 int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* cache, const sgq_heads_t* q,
@@ -315,6 +317,7 @@ int paged_attention(int fmt, uint32_t flags, int64_t B, const sgq_kv_cache_t* ca
     a.items = (int)p.items;
     a.tiles = (int)p.tiles;
     a.split = p.split;
+    a.DP = p.DP;
     return launched(launch_attend(fmt_of(fmt), dt_of(flags), current_device(), a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,6 +1,6 @@
 // sgq_group_api.cu -- the C ABI declared in include/sgq_group.h: host-side
 // argument checks, then the operation's launches.
-#include "sgq_group.cuh"
+#include "sgq_cache.cuh"
 
 #include "sgq_group.h"
 
@@ -167,13 +167,14 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
 
 int sgq_wait_timeouts(uint32_t* count) {
     if (!count) return SGQ_ERR_INVALID_ARG;
-    uint32_t gemm = 0, lora = 0;
+    uint32_t gemm = 0, lora = 0, attend = 0;
     // the copies of the counts wait for the default stream alone, which streams
     // made not to block it do not wait for either
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = gemm_gave_up(&gemm);
     if (e == cudaSuccess) e = lora_gave_up(&lora);
-    if (e == cudaSuccess) *count = gemm + lora;
+    if (e == cudaSuccess) e = attend_gave_up(&attend);
+    if (e == cudaSuccess) *count = gemm + lora + attend;
     return launched(e);
 }
 
