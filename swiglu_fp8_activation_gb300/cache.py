@@ -24,8 +24,9 @@ import struct
 
 import torch
 
+from . import binding
 from .binding import F_FP16, SgqError, _act_dtype, _check, library
-from .grouped import _here, _need, _there
+from .grouped import _device, _here, _need, _raw_stream, _there
 
 F_ROPE_INTERLEAVED, F_ROPE_INVERSE = 64, 128
 MAX_HEAD = 256
@@ -36,6 +37,7 @@ MAX_SEQUENCES = 65536
 CACHE_FORMATS = {"none": 3, "per_token": 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": F_ROPE_INTERLEAVED}
 _bound = None
+_bf16, _f16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 class Heads(C.Structure):
@@ -63,6 +65,8 @@ _rope_bytes = struct.Struct("@q2Pif").pack
 
 def _lib() -> C.CDLL:
     global _bound
+    if _bound is not None and _bound is binding._lib:
+        return _bound
     L = library()
     if _bound is not L:
         vp, i64, u32, i32 = C.c_void_p, C.c_int64, C.c_uint32, C.c_int
@@ -190,11 +194,17 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, *, layou
     passed on. inverse=True turns the other way: the gradient. Returns out
     [T, heads, D] of x's type, contiguous where it is not given; out=x rotates in place.
     """
-    dt, shape = _act_dtype(x, "x"), x.shape
+    dt, shape = x.dtype, x.shape
+    if dt is not _bf16 and dt is not _f16:
+        _act_dtype(x, "x")
     src = _heads(x, dt, "x", shape)
     T, _, D = shape
     turn, flags = _turn(freqs, positions, T, layout, factor)
-    at = _here(stream, "rope", x, positions, freqs, out)
+    d = x.get_device()
+    if stream is None and d >= 0 and positions.get_device() == freqs.get_device() == d == _device() and (out is None or out.get_device() == d):
+        at = _raw_stream(d)
+    else:
+        at = _here(stream, "rope", x, positions, freqs, out)
     if at is None:
         with _there(stream, x):
             return rope(x, positions, freqs, layout=layout, factor=factor, inverse=inverse, out=out)
@@ -225,7 +235,9 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     quantize_fp8's rule, keys from their 32-bit rotation. Returns q_out
     (allocated where it is not given; q itself to rotate in place), or None without q.
     """
-    dt = _act_dtype(k, "k")
+    dt = k.dtype
+    if dt is not _bf16 and dt is not _f16:
+        _act_dtype(k, "k")
     ck, laid, code = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
     T, D = k.shape[0], laid[3]
     shape = (T, laid[1], D)
@@ -243,7 +255,13 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
         hq = _heads(q, dt, "q", (T, qshape[1], D) if len(qshape) == 3 else (T, 1, D))
     elif q_out is not None:
         raise SgqError("q_out: of no use without q")
-    at = _here(stream, "cache_write", k, v, k_cache, v_cache, slots, k_scale, v_scale, q, q_out, positions, freqs)
+    d = k.get_device()
+    if (stream is None and d >= 0 and d == _device() == v.get_device() == k_cache.get_device() == v_cache.get_device() == slots.get_device()
+            and (k_scale is None or d == k_scale.get_device() == v_scale.get_device()) and (turn is None or d == positions.get_device() == freqs.get_device())
+            and (q is None or q.get_device() == d) and (q_out is None or q_out.get_device() == d)):
+        at = _raw_stream(d)
+    else:
+        at = _here(stream, "cache_write", k, v, k_cache, v_cache, slots, k_scale, v_scale, q, q_out, positions, freqs)
     if at is None:
         with _there(stream, k):
             return cache_write(k, v, k_cache, v_cache, slots, fmt=fmt, k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
@@ -281,7 +299,12 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is not None:
             _need(t, shape, dt, name)
-    at = _here(stream, "cache_read", k_cache, v_cache, slots, k_scale, v_scale, k_out, v_out)
+    d = slots.get_device()
+    if (stream is None and d >= 0 and d == _device() == k_cache.get_device() == v_cache.get_device()
+            and (k_scale is None or d == k_scale.get_device() == v_scale.get_device()) and k_out is None and v_out is None):
+        at = _raw_stream(d)
+    else:
+        at = _here(stream, "cache_read", k_cache, v_cache, slots, k_scale, v_scale, k_out, v_out)
     if at is None:
         with _there(stream, k_cache):
             return cache_read(k_cache, v_cache, slots, fmt=fmt, k_scale=k_scale, v_scale=v_scale, dtype=dt, k_out=k_out, v_out=v_out)
@@ -327,14 +350,19 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     workspace: uint8 [attention_workspace_bytes(fmt, B, Hq, heads, D, width, page_size,
     window)] or None (allocated where one is needed).
     """
-    dt, shape = _act_dtype(q, "q"), q.shape
+    dt, shape = q.dtype, q.shape
+    if dt is not _bf16 and dt is not _f16:
+        _act_dtype(q, "q")
     ck, laid, code = _cache(k_cache, v_cache, fmt, k_scale, v_scale, dt)
     _, heads, page_size, D = laid
     B, Hq, _ = shape if len(shape) == 3 else (0, 0, 0)
     hq = _heads(q, dt, "q", (B, Hq, D))
-    width = pages.shape[1] if pages.dim() == 2 else 0
-    _need(pages, (B, width), torch.int32, "pages")
-    _need(lengths, (B,), torch.int32, "lengths")
+    wide = pages.shape
+    width = wide[1] if len(wide) == 2 else 0
+    if pages.dtype is not _i32 or wide != (B, width) or not pages.is_contiguous():
+        _need(pages, (B, width), _i32, "pages")
+    if lengths.dtype is not _i32 or lengths.shape != (B,) or not lengths.is_contiguous():
+        _need(lengths, (B,), _i32, "lengths")
     if sinks is not None:
         _need(sinks, (Hq,), torch.float32, "sinks")
     if out is not None:
@@ -347,7 +375,13 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if lse is not False and lse is not True:
         told = lse
         _need(told, (B, Hq), torch.float32, "lse")
-    at = _here(stream, "paged_attention", q, k_cache, v_cache, pages, lengths, k_scale, v_scale, sinks, out, told, workspace)
+    d = q.get_device()
+    if (stream is None and d >= 0 and d == _device() == k_cache.get_device() == v_cache.get_device() == pages.get_device() == lengths.get_device()
+            and (k_scale is None or d == k_scale.get_device() == v_scale.get_device()) and (sinks is None or sinks.get_device() == d)
+            and out is None and told is None and workspace is None):
+        at = _raw_stream(d)
+    else:
+        at = _here(stream, "paged_attention", q, k_cache, v_cache, pages, lengths, k_scale, v_scale, sinks, out, told, workspace)
     if at is None:
         with _there(stream, q):
             return paged_attention(q, k_cache, v_cache, pages, lengths, fmt=fmt, k_scale=k_scale, v_scale=v_scale, scale=scale,

@@ -132,14 +132,15 @@ constexpr int64_t attend_tiles(bool fp8, int DP, int64_t limit, int64_t window) 
 // CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles. A cluster needs no workspace
 // and no second launch, and the device gives its multiprocessors the next item as they come free; but it is 8 CTAs at most, and where
 // few long items are to be taken, some multiprocessors end long before others. The host knows the table's width alone: up to 8
-// tiles a CTA, or 16 where four rounds of CTAs even that out. (Times in a graph, clusters and shares: 1 sequence of 4000, 8 heads: 10.4
-// and 9.1 us, but 5 us of the host's time less; 256 up to 300: 33 and 44; 64 up to 4096: 81 and 85; 32 up to 8192, 4 heads with groups of
+// tiles a CTA, or 16 where all CTAs run at once, or in four rounds that even that out. (Times in a graph, clusters and shares: 1 sequence of 4000, 8 heads: 10.4
+// and 9.1 us, but 5 us of the host's time less; 256 up to 300: 33 and 44; 200 up to 900, 2 heads of 64: 12 and 19; 64 up to 4096: 81 and 85; 32 up to 8192, 4 heads with groups of
 // 16: 84 and 72.)
 constexpr int attend_split(int64_t items, int64_t tiles, int cols) {
     int split = 1;
     while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * 16)) split *= 2;
     const int64_t each = (tiles + split - 1) / split, ctas = items * split;
-    return (each <= 8 || (each <= 16 && cols == 8 && ctas >= 1824)) && ctas <= 0x7FFFFFFF ? split : 0;
+    const bool rounds = ctas >= 4 * 456 || (ctas >= 152 && ctas <= 456);         // of three CTAs on each of 152 multiprocessors
+    return (each <= 8 || (each <= 16 && cols == 8 && rounds)) && ctas <= 0x7FFFFFFF ? split : 0;
 }
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }

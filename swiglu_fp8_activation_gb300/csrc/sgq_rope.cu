@@ -19,7 +19,7 @@ namespace sgq {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 __device__ __forceinline__ uint4 ld16(const void* p) {
     uint4 v;
@@ -27,11 +27,12 @@ __device__ __forceinline__ uint4 ld16(const void* p) {
     return v;
 }
 
-// LPR lanes a row, 16 values a lane. a.per threads (a multiple of a warp) work on one token: each has a unit of the
-// rows' columns, whose cosines and sines it keeps for all heads that it turns. A row's reads go out a row before it
-// is worked on; the first of q, k and v before the angles.
+// LPR lanes a row, 16 values a lane; a.per threads (a multiple of a warp) work on one token, its heads one after the other.
+// Registers bound it: nine CTAs of 128 threads a multiprocessor (56 registers, a few spilled) against eight and ten: 8192 tokens, 32 heads
+// of 128 and 8 of k and v, bf16: 33.2 us (201 MB, 6065 GB/s), 34.0 and 34.3; E4M3: 33.5, 34.3 and 33.5; 40 heads of 16384 tokens turned:
+// 54.5 (336 MB, 6156 GB/s), 55.5 and 55.2. Reads of the next row held in registers cost more warps than they gain: 65.
 template <int FMT, int DT, bool INTERLEAVED, int LPR>
-__global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 9) cache_write_kernel(const WriteArgs a) {
     extern __shared__ float2 turn[];     // [tokens][8][pairs / 8]: factor * (cos, sin), a lane's 8 pairs a row apart (no bank twice)
     pdl_wait();
     pdl_trigger();
@@ -166,11 +167,11 @@ cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& 
     WriteArgs a = w;
     const int units = (a.D + 15) / 16, lpr = units <= 4 ? 4 : units <= 8 ? 8 : 16;
     const int most = a.q.n > a.k.n ? a.q.n : a.k.n;
-    // Few tokens: as many threads a token as it has heads, in several CTAs where they do not fit in one, so that none waits for another;
-    // many: two warps a token, whose lanes keep the angles for several heads.
+    // Few tokens: as many threads a token as it has heads, in several CTAs where they do not fit in one, and q beside k and v, so
+    // that none waits for another; many: two warps a token, one where it has few heads, whose lanes keep their part of the angles.
     const int sms = dev.sms > 0 ? dev.sms : 152;
     int split = 1;
-    a.per = 64;
+    a.per = most * lpr < 128 ? 32 : 64;
     if (a.T < 8 * (int64_t)sms) {
         while (a.per < kThreads && a.per / lpr < most) a.per *= 2;
         if (a.T < 2 * (int64_t)sms) split = (most + a.per / lpr - 1) / (a.per / lpr);
