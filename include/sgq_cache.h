@@ -42,6 +42,8 @@
  * multiprocessors, which sgq_set_sm_budget replaces; so may its last bit.)
  * Values that are not finite in a row give non-finite or unspecified results in what
  * is computed from that row, and in nothing else: not where the row is masked.
+ * Every wait inside paged_attention is limited to some seconds, as those of
+ * sgq_group.h's products are: sgq_wait_timeouts counts them too.
  */
 #ifndef SGQ_CACHE_H
 #define SGQ_CACHE_H
@@ -67,9 +69,10 @@ typedef struct sgq_heads {
     int64_t token_stride, head_stride;
 } sgq_heads_t;
 
-/* A paged cache (see above); pages 1 .. SGQ_MAX_ROWS, page_size 1 .. SGQ_MAX_PAGE, heads
- * 1 .. SGQ_MAX_HEADS. k and v may lie between one another (the halves of each page). Strides in elements of the format's type, multiples of 16 bytes;
- * k_scale and v_scale NULL with SGQ_FMT_16BIT. */
+/* A paged cache (see above): pages 1 .. SGQ_MAX_ROWS, page_size 1 .. SGQ_MAX_PAGE,
+ * heads 1 .. SGQ_MAX_HEADS. Strides in elements of the format's type, of k and v
+ * alike: multiples of 16 bytes, below 2^40 bytes. k and v may lie between one
+ * another (the halves of each page). k_scale and v_scale are NULL with SGQ_FMT_16BIT. */
 typedef struct sgq_kv_cache {
     int64_t pages, page_size, heads, D;
     int64_t page_stride, head_stride, token_stride;
@@ -159,7 +162,8 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
                void* k_out, void* v_out, sgq_stream_t stream);
 
 /*
- * Attention of one new token a sequence over its pages. For sequence b, its
+ * Attention of one new token a sequence over its pages, one launch where the table is
+ * short and two else. For sequence b, its
  * length n = lengths[b] held to [0, width * page_size], and head h of q with
  * j = h / (Hq / heads) the head of the cache that it reads:
  *

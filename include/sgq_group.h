@@ -199,9 +199,9 @@ int lora_add(uint32_t flags, int64_t T, int64_t S, int64_t groups, int64_t R, in
 int64_t sgq_lora_workspace_bytes(int64_t S, int64_t groups, int64_t R);
 
 /*
- * Launches of grouped_gemm and lora_add on the current device, since the
- * library was loaded, in which a wait inside the kernel ran out of time (see
- * above). A diagnosis: it waits for the device, all streams of it, and may not be
+ * Launches of grouped_gemm and lora_add (and of sgq_cache.h's paged_attention) on the
+ * current device, since the library was loaded, in which a wait inside the kernel ran
+ * out of time (see above; a launch counts once for each of its CTAs). A diagnosis: it waits for the device, all streams of it, and may not be
  * called during graph capture. NULL returns SGQ_ERR_INVALID_ARG.
  */
 int sgq_wait_timeouts(uint32_t* count);

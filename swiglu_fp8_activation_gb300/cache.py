@@ -348,7 +348,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     value. Returns out [B, Hq, D], zeros where a sequence has no token; with
     lse=True, or a float32 [B, Hq] to write, (out, the log of the softmax's sum).
     workspace: uint8 [attention_workspace_bytes(fmt, B, Hq, heads, D, width, page_size,
-    window)] or None (allocated where one is needed).
+    window)] or None (allocated where one is needed). Waits inside the kernel are limited: see
+    wait_timeouts.
     """
     dt, shape = q.dtype, q.shape
     if dt is not _bf16 and dt is not _f16:

@@ -2,18 +2,20 @@
 // (include/sgq_cache.h, paged_attention).
 //
 // Reading the cache bounds it: every key and value row is used by `group` heads
-// of q, 4 to 16 operations a byte. One launch gives all CTAs equal shares of the
-// cache's tiles, whatever the sequences' lengths; a second joins what several CTAs
-// have computed of one sequence.
+// of q, 4 to 16 operations a byte up to groups of 8.
 //
-// Shares. An item is a sequence and a head of the cache (a chunk of its group of
-// q heads, where there are more than a CTA's columns); its tiles are 64 tokens,
-// 128 of E4M3 rows. All items' tiles stand in one row, and CTA c of G takes those from
-// c total / G on, total / G of them, rounded up or down. The lengths are summed on the device, so a
-// captured graph follows them.
+// An item is a sequence and a head of the cache (a chunk of its group of q heads, where
+// there are more than a CTA's columns); its tiles are 64 tokens, 128 of E4M3 rows of
+// up to 128. Two ways of sharing them out, by the sizes that the host knows (attend_split):
+//   * A cluster of 1 to 8 CTAs takes an item, each CTA an equal run of its tiles, and joins
+//     in its shared memory. One launch.
+//   * All items' tiles stand in one row, and CTA c of G takes those from c total / G on,
+//     total / G of them, rounded up or down; a second launch joins what several CTAs
+//     have computed of one item.
+// Lengths are read on the device in both, so a captured graph follows them.
 //
 // Inside a CTA each of four groups of warps takes a quarter of every tile's tokens, and each warp of a
-// group 8 columns of them. A group runs by itself: its own asynchronous copies, several tiles
+// group 8 or 16 columns of them. A group runs by itself: its own copies, several tiles
 // ahead and across the items' borders; a warp has its own running maximum and sums. All warps meet where an
 // item ends, to add up.
 //
@@ -28,8 +30,8 @@
 // summed, and in which the rows of V^T stand in their tiles, is free: both
 // follow what a lane's 16-byte reads bring, so no byte is moved twice.
 //
-// The running maximum is a reference that is moved only when a value exceeds it
-// by 2^8, so most tiles need no reduction over lanes and no rescaling.
+// The running maximum is a reference that is moved only when a weight exceeds it 512
+// times, so most tiles need no reduction over lanes and no rescaling.
 #pragma once
 
 #include "sgq_cache.cuh"
@@ -751,8 +753,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         }
     };
 
-    // Turn i copies tile i and computes tile i - a.stages, whose slot that is: copies run ahead, a
-    // commit group each (empty behind the last). One loop, so that the copying's code is there once.
+    // Turn i copies tile i and computes tile i - a.stages, whose slot that is. One loop, so that the copying's code is there once.
     ask_q(cu);
     const bool copies = cg == 0;
     uint32_t parity = 1;                                         // of the slots' barriers: 0 the first time round
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 }
                 flush(done, slot, begun_here, ends);
                 // who joins: the entry of the item, by the CTA that begins it, or of this CTA
-                if (a.joined && threadIdx.x == 0 && (a.joined == kByItem ? begun_here : todo == 0)) {
+                if (threadIdx.x == 0 && (a.joined == kByItem ? begun_here : todo == 0)) {
                     Shared sh = {done.b, done.j, -1, -1};
                     if (begun_here && !ends) {
                         // the item goes on in the next CTAs, to the one that has its last tile
@@ -941,8 +942,8 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
     const int64_t sms = dev.sms > 0 ? dev.sms : 152;
     if (a.split > 0) {
         using S = Shape<KIND, DP, CG, NT, true>;
-        // Few CTAs wait for each tile's copies, and have the room to copy all that they need at once (ROW1); as many as the
-        // device holds do better with two tiles of wide rows, eight of narrow ones.
+        // Few CTAs have the room to copy many tiles at once; as many as the device holds do better with two tiles of
+        // wide rows, eight of narrow ones (200 sequences up to 900, D 64: 11.3 us, with two 12.3).
         const int64_t ctas = (int64_t)a.B * a.items * a.split;
         const int each = ctas <= sms ? 1 : ctas <= 2 * sms && S::ctas > 2 ? 2 : S::ctas, most = each < S::ctas || DP == 64 ? kStages : 2;
         const int need = (a.tiles + a.split - 1) / a.split;
@@ -957,11 +958,10 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
     if (ctas > kAttendCtas) ctas = kAttendCtas;
     const int64_t most = (int64_t)a.B * a.items * a.tiles;
     if (ctas > most) ctas = most;
-    // where no item has two tiles no two CTAs share one
     const int64_t items = (int64_t)a.B * a.items;
-    a.joined = a.tiles <= 1 ? 0 : items <= 64 ? kByItem : kByCta;
+    a.joined = items <= 64 ? kByItem : kByCta;
     const cudaError_t e = launch_grid(attend_kernel<KIND, DP, CG, NT, false>, dim3((unsigned)ctas), S::threads, S::bytes(a.stages), 1, dev.id, a, stream);
-    if (e != cudaSuccess || !a.joined) return e;
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.joined == kByItem ? items : ctas), (unsigned)(a.group < CG * NT * 8 ? a.group : CG * NT * 8));
     cfg.blockDim = dim3(a.joined == kByItem ? 512 : 128);
@@ -977,8 +977,8 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
 template <int KIND>
 cudaError_t launch_kind(const Device& dev, const AttendArgs& a, cudaStream_t stream) {
     const int DP = a.DP, cols = attend_columns(a.group, DP);
-    // 16 columns: two tiles of 8 a warp, so that each row is read and widened once. Heads of 256 have no
-    // registers for that, but for 32 columns' two warps side by side.
+    // 16 columns: two tiles of 8 a warp, so that each row is read from shared memory and widened once (8 sequences of 65536, 4 heads, E4M3: 89 us,
+    // by two warps side by side 118); heads of 256 have no registers for that.
     if (DP == 64) return cols == 8 ? launch<KIND, 64, 1, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 64, 1, 2>(dev, a, stream) : launch<KIND, 64, 2, 2>(dev, a, stream);
     if (DP == 128) return cols == 8 ? launch<KIND, 128, 1, 1>(dev, a, stream) : cols == 16 ? launch<KIND, 128, 1, 2>(dev, a, stream) : launch<KIND, 128, 2, 2>(dev, a, stream);
     return cols == 8 ? launch<KIND, 256, 1, 1>(dev, a, stream) : launch<KIND, 256, 2, 1>(dev, a, stream);

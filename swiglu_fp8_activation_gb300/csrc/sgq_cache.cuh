@@ -107,7 +107,7 @@ struct AttendArgs {
     int limit;           // width * page size: the longest sequence
     int chunks;          // column chunks a head of the cache
     int items;           // heads * chunks a sequence
-    int joined;          // how a second launch finds what several CTAs have computed; 0 for none
+    int joined;          // how a second launch finds what several CTAs have computed
     int split;           // CTAs of a cluster, where each takes one item; 0 for shares
     int tiles;           // of the longest item
     int DP;              // attend_padded's width

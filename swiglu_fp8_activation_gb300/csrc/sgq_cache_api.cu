@@ -11,6 +11,7 @@ using namespace sgq;
 namespace {
 
 constexpr int64_t kMaxRows = SGQ_MAX_ROWS;
+constexpr int64_t kMaxStride = int64_t(1) << 40;     // bytes, of a tensor map
 
 bool bad_count(int64_t v) { return v < 0 || v > kMaxRows; }
 
@@ -103,6 +104,8 @@ int take_cache(int fmt, const sgq_kv_cache_t* c, CacheArgs* to, CacheSpans* span
     if (!extent(d, 3, c->D, elem, &bytes)) return SGQ_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i)
         if (d[i].size > 1 && d[i].stride * elem % 16 != 0) return SGQ_ERR_MISALIGNED;
+    for (int i = 0; i < 3; ++i)
+        if (d[i].size > 1 && d[i].stride * elem >= kMaxStride) return SGQ_ERR_UNSUPPORTED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return SGQ_ERR_MISALIGNED;
     to->k = static_cast<uint8_t*>(c->k);
     to->v = static_cast<uint8_t*>(c->v);

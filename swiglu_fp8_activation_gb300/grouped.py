@@ -233,8 +233,8 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
 
 
 def wait_timeouts() -> int:
-    """Launches of grouped_gemm and lora_add on the current device in which a
-    wait inside the kernel ran out of time (some seconds without progress). Such
+    """Launches of grouped_gemm, lora_add and paged_attention on the current device in
+    which a wait inside the kernel ran out of time (some seconds without progress). Such
     a launch ends, its call having returned, and leaves its outputs unspecified:
     this count is where it shows. Waits for the device; not during graph capture."""
     n = C.c_uint32(0)
