@@ -67,9 +67,9 @@ struct Shape {
     static constexpr int scales = fp8 ? 2 * rows * 4 : 0;
     static constexpr int step = kParts * slot;                   // bytes of a tile: its parts' slots side by side
     // CTAs a multiprocessor at most. Three CTAs that each take a short item hide one another's beginnings (64 sequences up to 4096, bf16:
-    // 82 us, with two 89); CTAs that take long shares are two, but for narrow E4M3 rows, which are bound by
-    // instructions (4 sequences of 32768, D 64: 50 us with two, 33 with three).
-    static constexpr int ctas = DP == 256 ? (fp8 && CG == 1 ? 2 : 1) : CG > 1 ? 1 : NT > 1 ? 2 : DIRECT || (fp8 && DP == 64) ? 3 : 2;
+    // 82 us, with two 89); CTAs that take long shares are two, but for narrow rows (8 sequences of
+    // 65536, D 64, bf16: 152 us with two, 140 with three; 4 of 32768, E4M3: 50 and 33; 8 up to 131072, D 128, E4M3: 283 and 299).
+    static constexpr int ctas = DP == 256 ? (fp8 && CG == 1 ? 2 : 1) : CG > 1 ? 1 : NT > 1 ? 2 : DIRECT || DP == 64 ? 3 : 2;
     // Tiles that fit in shared memory where n CTAs share a multiprocessor.
     static constexpr int bytes(int n) { return n * (step + kParts * scales) + 1024; }    // dynamic shared memory of n tiles
     static constexpr int fit(int n) { return (227 * 1024 / n - 4096) / (step + kParts * scales); }
