@@ -174,8 +174,8 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  *   lse[b][h] = log(sum_t exp(x_t) + exp(sinks[h]))
  *
  * n counts the new token itself where its row has been written. Tokens whose
- * page is outside [0, pages) are masked as those outside the window are: their
- * rows are not read. Where nothing is left out[b] is zeros and lse the sink, or -infinity.
+ * page is outside [0, pages) are masked as those outside the window are: what masked
+ * rows hold has no influence, and no page outside is read. Where nothing is left out[b] is zeros and lse the sink, or -infinity.
  *
  * Products in 16 bits by 16 bits, exact; sums, the softmax and its statistics in
  * fp32; FP8 codes enter as they are and the rows' scales in fp32. The

@@ -177,6 +177,8 @@ def _turn(freqs: torch.Tensor, positions: torch.Tensor, T: int, layout: str, fac
     flag = ROPE_LAYOUTS.get(layout)
     if flag is None:
         raise SgqError(f"unknown order of pairs {layout!r}")
+    if not abs(factor) <= 3.4e38:
+        raise SgqError(f"factor: expected a finite number, got {factor}")
     if freqs.dim() != 1 or freqs.dtype is not torch.int64 or not freqs.is_contiguous():
         raise SgqError(f"freqs: expected contiguous int64 [R / 2], got {freqs.dtype} {tuple(freqs.shape)}")
     return _rope_bytes(2 * len(freqs), freqs.data_ptr(), positions.data_ptr(), _index(positions, T, "positions"), factor), flag

@@ -184,7 +184,7 @@ struct Walk {
         n = min(max(length, 0), a.limit);
         lo = a.window > 0 && n > a.window ? n - a.window : 0;
         start = lo / TOKENS * TOKENS;
-        tiles = max(1, (n - start + TOKENS - 1) / TOKENS);
+        tiles = max(1, (int)(((uint32_t)(n - start) + TOKENS - 1) / TOKENS));
     }
 };
 
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     const int lane_row = kRowsAt > 1 ? lane / S::pieces : 0, piece = lane % S::pieces;
     const bool used = piece * 16 < a.c.D * S::elem;              // columns from D on are filled with zeros
     const int lane_piece = S::piece_at(lane_row, piece);
-    // the lane's token of w's tile (of 16 tokens both halves of a warp have the same)
+    // the lane's token of w's tile (of 16 tokens both halves of a warp have the same); behind the last that an int counts: negative, masked
     auto token_of = [&](const W& w) { return w.start + w.tile * S::tokens + part * S::rows + (lane & (S::rows - 1)); };
     auto page_of = [&](const W& w, int on = 0) {                 // of the lane's token, `on` tiles on; -1 where it is masked
         const int t = token_of(w) + on * S::tokens;

@@ -142,6 +142,7 @@ def test_cache_refusals(L):
         no(MISALIGNED, fp8(ks=P(12, 2)), 2)
         no(INVALID, kv(ps=-4096))
         no(INVALID, kv(ps=1 << 60))
+        no(UNSUPPORTED, kv(ps=1 << 39))                  # 2^40 bytes
         no(INVALID, kv(hs=512))                          # rows share addresses
         no(INVALID, kv(ts=32))
         no(INVALID, kv(v=P(10)))
@@ -270,6 +271,8 @@ def test_python_refusals():
     no(sgq.rope, x, i64(8)[::2], f)
     no(sgq.rope, x, i64(4), f.float())
     no(sgq.rope, x, i64(4), i64(32, 1))
+    for factor in (math.inf, math.nan, -math.inf, 1e39):
+        no(sgq.rope, x, i64(4), f, factor=factor)
     no(sgq.rope, x, i64(4), f)                                               # on the CPU
     c, s = bf(6, 2, 16, 64), i32(4)
     no(sgq.cache_write, x, x, c, c.clone(), s, fmt="mxfp8")

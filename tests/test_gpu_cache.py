@@ -20,6 +20,12 @@ BF16, F16 = torch.bfloat16, torch.float16
 KINDS = [("none", BF16), ("none", F16), ("per_token", BF16), ("per_token", F16)]
 
 
+@pytest.fixture(autouse=True, scope="module")
+def no_wait_ran_out():
+    yield
+    assert sgq.wait_timeouts() == 0
+
+
 @contextlib.contextmanager
 def planned_for(sms):
     binding.set_sm_budget(sms)
@@ -342,6 +348,36 @@ def test_attention_long_sequences_are_summed_in_32_bits(fmt, dtype, D):
     """Two q heads' worth of spread and none: the error is that of the one rounding at the end."""
     attend(fmt, dtype, [20000, 12345], 2, 8, D, 64, seed=D, norm=True)
     attend(fmt, dtype, [9001], 2, 16, D, 32, seed=D, spread=4.0, norm=True)
+
+
+@pytest.mark.parametrize("fmt,dtype", KINDS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_long_windows(fmt, dtype, D):
+    """Windows of many tiles, that begin anywhere in one."""
+    attend(fmt, dtype, [20001, 9000, 8999, 17], 1, 8, D, 16, window=9000, sinks=True, seed=D)
+
+
+@pytest.mark.parametrize("fmt,dtype", KINDS)
+@pytest.mark.parametrize("P,lengths", [(4096, [4096, 4097, 100]), (65536, [5000]), (2048, [1])])
+def test_attention_large_pages(fmt, dtype, P, lengths):
+    attend(fmt, dtype, lengths, 1, 2, 64, P, seed=P)
+
+
+@pytest.mark.parametrize("fmt,dtype", KINDS)
+@pytest.mark.parametrize("P", [16, 5])
+def test_attention_of_a_part_of_each_row(fmt, dtype, P):
+    """Heads that lie in the first columns of wider rows, of every second page; one query for all sequences."""
+    def part(pages):
+        k, v, ks, vs = ref.pool(fmt, 2 * pages, 2, P, 96, dtype, 0)
+        return (*(t[::2, :, :, :80] for t in (k, v)), *(t if t is None else t[::2].contiguous() for t in (ks, vs)))
+    attend(fmt, dtype, [200, 0, 77], 2, 3, 80, P, cache=part)
+    table, pages = ref.table_of([200, 0, 77], P)
+    k, v, ks, vs = part(pages)
+    q = torch.randn(1, 6, 80, generator=ref.gen(0)).to(dtype)
+    n = torch.tensor([200, 0, 77], dtype=torch.int32)
+    want, tol, _, _ = ref.attention(q.expand(3, -1, -1), k, v, ks, vs, table, n)
+    dq, dk, dv, dks, dvs, dt, dn = cuda(q, k, v, ks, vs, table, n)
+    ref.check(sgq.paged_attention(dq.expand(3, -1, -1), dk, dv, dt, dn, fmt=fmt, k_scale=dks, v_scale=dvs).cpu(), want, tol)
 
 
 @pytest.mark.parametrize("fmt,dtype", KINDS)
