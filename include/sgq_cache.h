@@ -191,7 +191,7 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  *   q             [B, Hq, D], read; Hq = q->heads a multiple of cache->heads
  *   pages         [B, width] int32, read
  *   width         pages a sequence, >= 0; width * page_size < 2^31, and B * Hq *
- *                 (width * page_size / 64 + 1) < 2^31
+ *                 (width * page_size / 64 + 3) < 2^31
  *   lengths       [B] int32, read
  *   scale         finite
  *   window        >= 0; 0 for none

@@ -43,6 +43,7 @@ namespace attend {
 constexpr int kParts = 4;                        // of a tile's tokens, a group of warps each
 // Entries of items that CTAs share: one an item (few items, each of many CTAs), or one a CTA.
 enum Joined : int { kByCta = 1, kByItem = 2 };
+constexpr int kEnd = kAttendEnd;
 constexpr int kStages = 8;                       // tiles copied ahead, at most (and 2 at least)
 constexpr float kNone = -3.0e38f;                // below every logit
 constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
@@ -66,10 +67,7 @@ struct Shape {
     static constexpr int half = rows * DP * elem, slot = 2 * half;               // k's rows, and v's behind them
     static constexpr int scales = fp8 ? 2 * rows * 4 : 0;
     static constexpr int step = kParts * slot;                   // bytes of a tile: its parts' slots side by side
-    // CTAs a multiprocessor at most. Three CTAs that each take a short item hide one another's beginnings (64 sequences up to 4096, bf16:
-    // 82 us, with two 89); CTAs that take long shares are two, but for narrow rows (8 sequences of
-    // 65536, D 64, bf16: 152 us with two, 140 with three; 4 of 32768, E4M3: 50 and 33; 8 up to 131072, D 128, E4M3: 283 and 299).
-    static constexpr int ctas = DP == 256 ? (fp8 && CG == 1 ? 2 : 1) : CG > 1 ? 1 : NT > 1 ? 2 : DIRECT || DP == 64 ? 3 : 2;
+    static constexpr int ctas = attend_resident(fp8, DP, CG * NT * 8, DIRECT);
     // Tiles that fit in shared memory where n CTAs share a multiprocessor.
     static constexpr int bytes(int n) { return n * (step + kParts * scales) + 1024; }    // dynamic shared memory of n tiles
     static constexpr int fit(int n) { return (227 * 1024 / n - 4096) / (step + kParts * scales); }
@@ -175,7 +173,7 @@ template <int TOKENS>
 struct Walk {
     int b, j;            // sequence, item of it: chunk `chunk` of the cache's head `head`
     int head, chunk;
-    int tile, tiles;     // of the item
+    int tile, tiles;     // of the item; none where the sequence is empty
     int lo, n;           // tokens [lo, n) are not masked
     int start;           // first token of the first tile
 
@@ -184,7 +182,7 @@ struct Walk {
         n = min(max(length, 0), a.limit);
         lo = a.window > 0 && n > a.window ? n - a.window : 0;
         start = lo / TOKENS * TOKENS;
-        tiles = max(1, (int)(((uint32_t)(n - start) + TOKENS - 1) / TOKENS));
+        tiles = (int)(((uint32_t)(n - start) + TOKENS - 1) / TOKENS);
     }
 };
 
@@ -200,6 +198,19 @@ __device__ __forceinline__ void finish(const AttendArgs& a, int b, int head, flo
         inv = l == 0.0f ? 0.0f : 1.0f / l;
     }
     lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// The results of an empty sequence, whose items are in no CTA's share.
+__device__ __forceinline__ void empty(const AttendArgs& a, int b) {
+    uint2* const out = reinterpret_cast<uint2*>(a.out + (int64_t)b * a.q.n * a.c.D);
+    for (int i = threadIdx.x; i < a.q.n * a.c.D / 4; i += blockDim.x) out[i] = make_uint2(0, 0);
+    if (a.lse)
+        for (int h = threadIdx.x; h < a.q.n; h += blockDim.x) {
+            float inv;
+            finish(a, b, h, kNone, 0.0f, inv, a.lse[(int64_t)b * a.q.n + h]);
+        }
+    if (a.joined == kByItem)
+        for (int j = threadIdx.x; j < a.items; j += blockDim.x) reinterpret_cast<Shared*>(a.ws)[b * a.items + j].first = -1;
 }
 
 // Four values, times f, to 16 bits.
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
 
     using W = Walk<S::tokens>;
     W ld;
-    int total = 0, G = 1, each = 0, more = 0, from = 0, count = 0, next_n = 0;
+    int total = 0, G = 1, each = 0, more = 0, from = 0, count = 0, next_n = 0;       // counted in tiles, an item's end as kEnd of them
     const int me = (int)blockIdx.x;
     if (DIRECT) {
         const int rank = a.split > 1 ? (int)cluster_rank() : 0, item = me / a.split, b = item / a.items;
@@ -282,7 +293,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         auto tiles_of = [&](int length) {
             W w;
             w.enter(a, 0, length);
-            return w.tiles * a.items;
+            return w.tiles > 0 ? (w.tiles + kEnd) * a.items : 0;
         };
         const int run = (a.B + kThreads - 1) / kThreads, b_from = min((int)threadIdx.x * run, a.B), b_to = min(b_from + run, a.B);
         int mine = 0;
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         }
         before -= mine;
         // With fewer tiles than CTAs the last ones have none: no CTA between two that share an item is without a tile.
-        G = min((int)gridDim.x, total);
+        G = max(1, min((int)gridDim.x, total));
         each = total / G;
         more = total - each * G;         // the first `more` CTAs take one tile more
         from = me * each + min(me, more);
@@ -321,20 +332,21 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             }
         }
         __syncthreads();
+        for (int b = me; b < a.B; b += (int)gridDim.x)
+            if (a.lengths[b] <= 0) empty(a, b);
         if (count == 0) {
             if (a.joined == kByCta && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
             return;
         }
         ld.enter(a, share_b, share_n);
-        ld.j = share_off / ld.tiles;
-        ld.tile = share_off - ld.j * ld.tiles;
+        ld.j = share_off / (ld.tiles + kEnd);
+        ld.tile = share_off - ld.j * (ld.tiles + kEnd);
         next_n = ld.b + 1 < a.B ? a.lengths[ld.b + 1] : 0;
     }
     ld.head = a.chunks > 1 ? ld.j / a.chunks : ld.j;
     ld.chunk = ld.j - ld.head * a.chunks;
-    W cu = ld;
-    int left = count;                                            // tiles to copy
 
+    // The next tile of the share.
     auto advance = [&](W& w, bool ahead) {
         if (++w.tile < w.tiles || DIRECT) return;
         w.tile = 0;
@@ -344,10 +356,24 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         }
         if (++w.j < a.items) return;
         w.j = w.head = 0;
-        if (w.b + 1 >= a.B) return;                              // behind the last: not used
-        w.enter(a, w.b + 1, ahead ? next_n : a.lengths[w.b + 1]);
-        if (ahead) next_n = w.b + 1 < a.B ? a.lengths[w.b + 1] : 0;
+        while (w.b + 1 < a.B) {                                  // behind the last: not used
+            w.enter(a, w.b + 1, ahead ? next_n : a.lengths[w.b + 1]);
+            if (ahead) next_n = w.b + 1 < a.B ? a.lengths[w.b + 1] : 0;
+            if (w.tiles > 0) return;
+        }
     };
+    if (!DIRECT && ld.tile >= ld.tiles) {                        // the share begins in an item's end
+        const int rest = ld.tiles + kEnd - ld.tile;
+        from += rest;
+        count -= rest;
+        advance(ld, true);
+        if (count <= 0) {
+            if (a.joined == kByCta && threadIdx.x == 0) reinterpret_cast<Shared*>(a.ws)[blockIdx.x].first = -1;
+            return;
+        }
+    }
+    W cu = ld;
+    int left = count;                                            // to copy
 
     // Copying, by the first warp of each group, in one of two ways. a.boxes, where pages are whole multiples of 16 tokens: boxes of 16 tokens by 128
     // bytes, which the copy engine brings while the warp computes. Else 16 bytes a lane and instruction, each lane with the rows of
@@ -770,9 +796,10 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 fresh = false;
             }
             tile(slot);
-            --todo;
             const bool ends = cu.tile + 1 == cu.tiles;
-            if (!DIRECT && (ends || todo == 0)) {
+            const int at = from + count - todo;
+            todo -= !DIRECT && ends ? 1 + kEnd : 1;
+            if (!DIRECT && (ends || todo <= 0)) {
                 const W done = cu;
                 if (todo > 0) {
                     advance(cu, false);
@@ -780,11 +807,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 }
                 flush(done, slot, begun_here, ends);
                 // who joins: the entry of the item, by the CTA that begins it, or of this CTA
-                if (threadIdx.x == 0 && (a.joined == kByItem ? begun_here : todo == 0)) {
+                if (threadIdx.x == 0 && (a.joined == kByItem ? begun_here : todo <= 0)) {
                     Shared sh = {done.b, done.j, -1, -1};
                     if (begun_here && !ends) {
                         // the item goes on in the next CTAs, to the one that has its last tile
-                        const int last = from + count - 1 + (done.tiles - done.tile - 1);
+                        const int last = at + (done.tiles - done.tile - 1);
                         sh.first = me;
                         sh.last = last < more * (each + 1) ? last / (each + 1) : more + (last - more * (each + 1)) / each;
                     }
@@ -798,7 +825,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         }
         if (copies && left > 0 && !*stop) {
             copy(ld, slot, pid);
-            if (--left > 0) {
+            left -= !DIRECT && ld.tile + 1 == ld.tiles ? 1 + kEnd : 1;
+            if (left > 0) {
                 advance(ld, true);
                 if (!DIRECT) pid = page_of(ld);
             }
@@ -945,7 +973,7 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
         // Few CTAs have the room to copy many tiles at once; as many as the device holds do better with two tiles of
         // wide rows, eight of narrow ones (200 sequences up to 900, D 64: 11.3 us, with two 12.3).
         const int64_t ctas = (int64_t)a.B * a.items * a.split;
-        const int each = ctas <= sms ? 1 : ctas <= 2 * sms && S::ctas > 2 ? 2 : S::ctas, most = each < S::ctas || DP == 64 ? kStages : 2;
+        const int each = ctas <= attend_room(sms, 1, a.split) ? 1 : S::ctas > 2 && ctas <= attend_room(sms, 2, a.split) ? 2 : S::ctas, most = each < S::ctas || DP == 64 ? kStages : 2;
         const int need = (a.tiles + a.split - 1) / a.split;
         a.stages = S::fit(each) < most ? S::fit(each) : most;
         if (a.stages > need) a.stages = need < 2 ? 2 : need;

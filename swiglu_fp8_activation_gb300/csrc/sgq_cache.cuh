@@ -129,18 +129,29 @@ constexpr int64_t attend_tiles(bool fp8, int DP, int64_t limit, int64_t window) 
     if (window > 0 && limit > window + tokens - 1) limit = window + tokens - 1;
     return limit <= tokens ? 1 : (limit + tokens - 1) / tokens;
 }
+// What an item's end costs a CTA that takes shares, in tiles. (256 sequences up to 4000, 2 heads, E4M3: 59.5 us with 0, 56.1 with 2, 57.9 with 5.)
+constexpr int kAttendEnd = 2;
+// CTAs of paged_attention on a multiprocessor at most. Three CTAs that each take a short item hide one another's beginnings (64 sequences up to
+// 4096, bf16: 82 us, with two 89); CTAs that take long shares are two, but for narrow rows (8 sequences of
+// 65536, D 64, bf16: 152 us with two, 140 with three; 4 of 32768, E4M3: 50 and 33; 8 up to 131072, D 128, E4M3: 283 and 299).
+__host__ __device__ constexpr int attend_resident(bool fp8, int DP, int cols, bool direct) {
+    return DP == 256 ? (fp8 && cols == 8 ? 2 : 1) : cols == 32 ? 1 : cols == 16 ? 2 : direct || DP == 64 ? 3 : 2;
+}
+// CTAs in clusters of `split` that surely run at once, n a multiprocessor: clusters do not fill the device's processor groups. (In clusters of
+// 8: 120, 288 and 408 with n of 1, 2 and 3; of 4: 144, 296 and 440.)
+constexpr int64_t attend_room(int64_t sms, int n, int split) { return n * sms - (split == 1 ? 0 : (n > 2 ? 6 : 4) * split); }
 // CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles. A cluster needs no workspace
-// and no second launch, and the device gives its multiprocessors the next item as they come free; but it is 8 CTAs at most, and where
-// few long items are to be taken, some multiprocessors end long before others. The host knows the table's width alone: up to 8
-// tiles a CTA, or 16 where all CTAs run at once, or in four rounds that even that out. (Times in a graph, clusters and shares: 1 sequence of 4000, 8 heads: 10.4
-// and 9.1 us, but 5 us of the host's time less; 256 up to 300: 33 and 44; 200 up to 900, 2 heads of 64: 12 and 19; 64 up to 4096: 81 and 85; 32 up to 8192, 4 heads with groups of
-// 16: 84 and 72.)
-constexpr int attend_split(int64_t items, int64_t tiles, int cols) {
+// and no second launch; but it is 8 CTAs at most, and where long items are to be taken, or many sequences are empty, some multiprocessors
+// end long before others. The host knows the table's width alone: up to 8 tiles a CTA, or 1024 tokens where all CTAs run
+// at once. (Times in a graph, clusters and shares: 32 of 1024, 8 heads, bf16: 24.6 and 28.2 us; 24 of 2000, E4M3: 20.6 and 24.9; 1 of 4000, bf16: 11.1
+// and 9.4, but 5 us of the host's time less; 33 up to 5001, 3 heads, E4M3, 10 tiles a CTA: 24.1 and 19.7; 128 up to 8000, bf16, 16 tiles in 9 rounds: 318 and 283.)
+constexpr int attend_split(bool fp8, int DP, int64_t items, int64_t tiles, int cols) {
+    const int n = attend_resident(fp8, DP, cols, true);
     int split = 1;
-    while (split < 8 && split * 2 <= tiles && (items * split * 2 <= 304 || tiles > split * 16)) split *= 2;
+    while (split < 8 && split * 2 <= tiles && (items * split * 2 <= attend_room(152, n, split * 2) || tiles > split * 16)) split *= 2;
     const int64_t each = (tiles + split - 1) / split, ctas = items * split;
-    const bool rounds = ctas >= 4 * 456 || (ctas >= 152 && ctas <= 456);         // of three CTAs on each of 152 multiprocessors
-    return (each <= 8 || (each <= 16 && cols == 8 && rounds)) && ctas <= 0x7FFFFFFF ? split : 0;
+    const bool once = cols == 8 && ctas >= 152 && ctas <= attend_room(152, n, split);
+    return (each <= 8 || (once && each * attend_tokens(fp8, DP) <= 1024)) && ctas <= 0x7FFFFFFF ? split : 0;
 }
 // Floats of what one CTA leaves of an unfinished item: the sums, then the maxima and the totals.
 __host__ __device__ constexpr int attend_part(int cols, int DP) { return cols * (DP + 2); }

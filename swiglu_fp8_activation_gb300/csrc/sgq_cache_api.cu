@@ -166,8 +166,8 @@ bool plan_attend(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64
     p->chunks = (int)((group + p->cols - 1) / p->cols);
     p->items = heads * p->chunks;
     p->tiles = attend_tiles(fp8, p->DP, width * page_size, window);
-    p->split = attend_split(B * p->items, p->tiles, p->cols);
-    return B * p->items * p->tiles <= 0x7FFFFFFF;        // counted in 32 bits
+    p->split = attend_split(fp8, p->DP, B * p->items, p->tiles, p->cols);
+    return B * p->items * (p->tiles + kAttendEnd) <= 0x7FFFFFFF;         // counted in 32 bits
 }
 
 }  // namespace

@@ -381,6 +381,16 @@ def test_attention_of_a_part_of_each_row(fmt, dtype, P):
 
 
 @pytest.mark.parametrize("fmt,dtype", KINDS)
+@pytest.mark.parametrize("heads", [1, 3])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attention_of_a_padded_batch(fmt, dtype, heads, sinks):
+    """Most sequences, or all of them, are empty: their rows are zeros, whoever writes them."""
+    attend(fmt, dtype, [0] * 9 + [700] + [0] * 25 + [65, 1] + [0] * 12 + [3000], heads, 2, 64, 16, sinks=sinks)
+    attend(fmt, dtype, [0] * 400 + [700] + [0] * 100 + [300, 1], heads, 9, 48, 16, sinks=sinks)
+    attend(fmt, dtype, [0] * 200, heads, 8, 128, 16, width=3, sinks=sinks)
+
+
+@pytest.mark.parametrize("fmt,dtype", KINDS)
 def test_attention_many_sequences(fmt, dtype):
     attend(fmt, dtype, [(7 * i) % 40 for i in range(1500)], 1, 2, 64, 16, seed=1)
     with planned_for(5):
