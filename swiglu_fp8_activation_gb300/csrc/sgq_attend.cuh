@@ -9,9 +9,9 @@
 // up to 128. Two ways of sharing them out, by the sizes that the host knows (attend_split):
 //   * A cluster of 1 to 8 CTAs takes an item, each CTA an equal run of its tiles, and joins
 //     in its shared memory. One launch.
-//   * All items' tiles stand in one row, and CTA c of G takes those from c total / G on,
-//     total / G of them, rounded up or down; a second launch joins what several CTAs
-//     have computed of one item.
+//   * All items' tiles stand in one row, an item's end counted as some tiles more, and CTA c of G
+//     takes those from c total / G on, total / G of them, rounded up or down; a second launch
+//     joins what several CTAs have computed of one item. Empty sequences are not in the row.
 // Lengths are read on the device in both, so a captured graph follows them.
 //
 // Inside a CTA each of four groups of warps takes a quarter of every tile's tokens, and each warp of a
@@ -980,7 +980,7 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
         return launch_grid(attend_kernel<KIND, DP, CG, NT, true>, dim3((unsigned)ctas), S::threads, S::bytes(a.stages), a.split, dev.id, a, stream);
     }
     using S = Shape<KIND, DP, CG, NT, false>;
-    // Two tiles ahead, three where one CTA fills a multiprocessor: three are worse (8 sequences up to 131072, E4M3: 345 and 291 us; bf16 of 65536: 292 and 288).
+    // Two tiles ahead, three where one CTA fills a multiprocessor: three are worse (64 sequences up to 4096, bf16: 84 us and 78; 8 up to 131072, E4M3: 284 and 281).
     a.stages = S::ctas == 1 && S::fit(1) > 2 ? 3 : 2;
     int64_t ctas = sms * S::ctas;
     if (ctas > kAttendCtas) ctas = kAttendCtas;
