@@ -149,6 +149,13 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* m, uint
                  : "memory");
 }
 
+// n bytes, a multiple of 16, from and to multiples of 16.
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* from, uint32_t n, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(from), "r"(n), "r"(bar)
+                 : "memory");
+}
+
 // An arrival of this thread, one of those that the barrier counts, once its own copies have landed.
 __device__ __forceinline__ void arrive_with_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -266,8 +273,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
 
     if (threadIdx.x < kParts * kStages) {
         if (threadIdx.x == 0) s_stop = 0;
-        // the copy engine's, and each lane's own
-        tc::bar_init(tc::smem_addr(&s_bar[0][0] + threadIdx.x), 33);
+        // the copy engine's, and where lanes copy each lane's own
+        tc::bar_init(tc::smem_addr(&s_bar[0][0] + threadIdx.x), a.boxes ? 1 : 33);
         tc::fence_barrier_init();
     }
     if (a.boxes && threadIdx.x == 0) {
@@ -403,46 +410,63 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         const bool there = pid >= 0 && pid < a.c.pages;
         const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there) & S::full;
         const int place = t - (int)(quotient(t, a.c.page) * a.c.page.d);
-        if (lane == 0) {
-            s_mask[part][slot] = mask;
-            const int n = a.boxes ? ((mask & 0xFFFFu) ? 1 : 0) + ((mask >> 16) ? 1 : 0) : 0;
-            tc::bar_arrive_expect(bar, n * 16 * 2 * DP * S::elem);
-        }
-        __syncwarp();
         if (a.boxes) {
-            // of 16 tokens in one page: the page, the place of the first
+            // each box's tokens lie in one page: that of any that is there, from the place of the first on
+            const int n = a.boxes / 16, boxes = S::halves / n;
+            int page[S::halves], y[S::halves];
+            uint32_t some[S::halves];
 #pragma unroll
             for (int h = 0; h < S::halves; ++h) {
-                const uint32_t some = (mask >> (16 * h)) & 0xFFFFu;
-                const int page = __shfl_sync(0xFFFFFFFFu, pid, 16 * h + (some ? __ffs(some) - 1 : 0)), y = __shfl_sync(0xFFFFFFFFu, place, 16 * h);
-                if (some && tc::elect()) {
+                some[h] = boxes == 1 ? (h == 0 ? mask : 0) : (mask >> (16 * h)) & 0xFFFFu;
+                page[h] = __shfl_sync(0xFFFFFFFFu, pid, 16 * h + (some[h] ? __ffs(some[h]) - 1 : 0));
+                y[h] = __shfl_sync(0xFFFFFFFFu, place, 16 * h);
+            }
+            if (tc::elect()) {
+                s_mask[part][slot] = mask;
+                int count = 0;
+#pragma unroll
+                for (int h = 0; h < S::halves; ++h) count += some[h] ? a.boxes : 0;
+                tc::bar_arrive_expect(bar, count * 2 * (DP * S::elem + (kF8 ? 4 : 0)));
+#pragma unroll
+                for (int h = 0; h < S::halves; ++h) {
+                    if (!some[h]) continue;
 #pragma unroll
                     for (int b = 0; b < S::blocks; ++b) {
                         const uint32_t to = at + b * S::rows * S::block + h * 16 * S::block;
-                        load_4d(to, &a.km, bar, b * S::block, y, w.head, page);
-                        load_4d(to + S::half, &a.vm, bar, b * S::block, y, w.head, page);
+                        load_4d(to, &a.km, bar, b * S::block, y[h], w.head, page[h]);
+                        load_4d(to + S::half, &a.vm, bar, b * S::block, y[h], w.head, page[h]);
+                    }
+                    if (kF8) {
+                        const int64_t row = ((int64_t)page[h] * a.c.heads + w.head) * a.c.page.d + y[h];
+                        const uint32_t to = scales_at(slot) + h * 64;
+                        load_bytes(to, a.c.ks + row, a.boxes * 4, bar);
+                        load_bytes(to + S::rows * 4, a.c.vs + row, a.boxes * 4, bar);
                     }
                 }
             }
-        } else {
-            const int64_t off = there ? (int64_t)pid * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)place * a.c.ts : 0;
-#pragma unroll
-            for (int i = 0; i < S::rows / kRowsAt; ++i) {
-                const int row = i * kRowsAt + lane_row;
-                const bool ok = used && ((mask >> row) & 1);
-                const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + piece * 16;
-                const uint32_t to = at + i * kRowsAt * S::block + (lane_piece ^ S::turn(i * kRowsAt));
-                copy16(to, ok ? k : a.c.k, ok);
-                copy16(to + S::half, ok ? k + v_from_k : a.c.k, ok);
-            }
+            __syncwarp();
+            return;
         }
-        if (kF8) {
-            if (lane < S::rows) {
-                const int64_t row = there ? ((int64_t)pid * a.c.heads + w.head) * a.c.page.d + place : 0;
-                const uint32_t to = scales_at(slot) + lane * 4;
-                copy4(to, a.c.ks + row, there);
-                copy4(to + S::rows * 4, a.c.vs + row, there);
-            }
+        if (lane == 0) {
+            s_mask[part][slot] = mask;
+            tc::bar_arrive(bar);
+        }
+        __syncwarp();
+        const int64_t off = there ? (int64_t)pid * a.c.ps + (int64_t)w.head * a.c.hs + (int64_t)place * a.c.ts : 0;
+#pragma unroll
+        for (int i = 0; i < S::rows / kRowsAt; ++i) {
+            const int row = i * kRowsAt + lane_row;
+            const bool ok = used && ((mask >> row) & 1);
+            const uint8_t* k = a.c.k + __shfl_sync(0xFFFFFFFFu, off, row) + piece * 16;
+            const uint32_t to = at + i * kRowsAt * S::block + (lane_piece ^ S::turn(i * kRowsAt));
+            copy16(to, ok ? k : a.c.k, ok);
+            copy16(to + S::half, ok ? k + v_from_k : a.c.k, ok);
+        }
+        if (kF8 && lane < S::rows) {
+            const int64_t row = there ? ((int64_t)pid * a.c.heads + w.head) * a.c.page.d + place : 0;
+            const uint32_t to = scales_at(slot) + lane * 4;
+            copy4(to, a.c.ks + row, there);
+            copy4(to + S::rows * 4, a.c.vs + row, there);
         }
         arrive_with_copies(bar);
     };
@@ -510,7 +534,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         constexpr int H = S::halves;
         const uint32_t at = base + slot * S::step, vt = at + S::half, sc = kF8 ? scales_at(slot) : 0;
         const uint32_t mask = s_mask[part][slot];
-        if (mask != S::full) {                       // what masked rows of v hold is multiplied by 0: it has to be a number
+        if (mask != S::full) {                       // what masked rows of v hold, and their scales, is multiplied by 0: it has to be a number
+            if (kF8 && cg == 0 && lane < S::rows && !((mask >> lane) & 1)) sts_f32(sc + (S::rows + lane) * 4, 0.0f);
             if (cg == 0)
                 for (int i = lane; i < S::half / 16; i += 32) {
                     const int r = i * 16 / S::block % S::rows;
@@ -964,8 +989,9 @@ cudaError_t launch(const Device& dev, const AttendArgs& args, cudaStream_t strea
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     AttendArgs a = args;
     using Any = Shape<KIND, DP, CG, NT, true>;
-    a.boxes = a.c.page.d % 16 == 0;
-    if (a.boxes && (!encode_cache(&a.km, a.c, a.c.k, Any::block, Any::elem) || !encode_cache(&a.vm, a.c, a.c.v, Any::block, Any::elem)))
+    // Boxes of as many tokens as a warp takes, or 16, whose rows and scales lie in one page.
+    a.boxes = a.c.page.d % 16 != 0 || ((uintptr_t)a.c.ks | (uintptr_t)a.c.vs) % 16 != 0 ? 0 : a.c.page.d % Any::rows == 0 ? Any::rows : 16;
+    if (a.boxes && (!encode_cache(&a.km, a.c, a.c.k, a.boxes, Any::block, Any::elem) || !encode_cache(&a.vm, a.c, a.c.v, a.boxes, Any::block, Any::elem)))
         return cudaErrorInvalidValue;
     const int64_t sms = dev.sms > 0 ? dev.sms : 152;
     if (a.split > 0) {

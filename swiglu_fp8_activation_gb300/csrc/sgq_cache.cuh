@@ -112,7 +112,7 @@ struct AttendArgs {
     int tiles;           // of the longest item
     int DP;              // attend_padded's width
     int stages;          // tiles copied ahead
-    int boxes;           // whether the copy engine brings the rows
+    int boxes;           // tokens of the copy engine's boxes; 0 where lanes copy
 };
 
 // Most CTAs that take shares of one paged_attention, for which its workspace has room.
@@ -166,9 +166,9 @@ __host__ __device__ constexpr int attend_header_bytes() { return kAttendCtas * (
 
 cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& dev, const WriteArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(int fmt, int dt, const Device& dev, const ReadArgs& a, cudaStream_t stream);
-// Boxes of 16 tokens by `block` bytes of the rows of k or v, in the order of that block's swizzle, zeros outside a row. False when the
+// Boxes of `tokens` tokens by `block` bytes of the rows of k or v, in the order of that block's swizzle, zeros outside a row. False when the
 // driver refuses the strides.
-bool encode_cache(CUtensorMap* m, const CacheArgs& c, const void* rows, int block, int elem);
+bool encode_cache(CUtensorMap* m, const CacheArgs& c, const void* rows, int tokens, int block, int elem);
 
 cudaError_t launch_attend(int fmt, int dt, const Device& dev, const AttendArgs& a, cudaStream_t stream);
 // CTAs of paged_attention on the current device in which a wait ran out of time (waits for the device).

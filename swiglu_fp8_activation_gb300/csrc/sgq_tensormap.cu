@@ -45,13 +45,13 @@ bool encode_tiles512(CUtensorMap* m, const void* base, int64_t tiles) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_cache(CUtensorMap* m, const CacheArgs& c, const void* rows, int block, int elem) {
+bool encode_cache(CUtensorMap* m, const CacheArgs& c, const void* rows, int tokens, int block, int elem) {
     const EncodeTiled f = encoder();
     if (!f) return false;
     const cuuint64_t width = (cuuint64_t)c.D * elem, apart = (width + 15) / 16 * 16;     // an axis of one has no stride of its own
     const cuuint64_t dims[4] = {width, c.page.d, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
     const cuuint64_t strides[3] = {c.ts ? (cuuint64_t)c.ts : apart, c.hs ? (cuuint64_t)c.hs : apart, c.ps ? (cuuint64_t)c.ps : apart};
-    const cuuint32_t box[4] = {(cuuint32_t)block, 16, 1, 1}, step[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {(cuuint32_t)block, (cuuint32_t)tokens, 1, 1}, step[4] = {1, 1, 1, 1};
     return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(rows), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
              block == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
