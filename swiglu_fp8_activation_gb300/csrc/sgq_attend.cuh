@@ -382,8 +382,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     W cu = ld;
     int left = count;                                            // to copy
 
-    // Copying, by the first warp of each group, in one of two ways. a.boxes, where pages are whole multiples of 16 tokens: boxes of 16 tokens by 128
-    // bytes, which the copy engine brings while the warp computes. Else 16 bytes a lane and instruction, each lane with the rows of
+    // Copying, by the first warp of each group, in one of two ways. a.boxes, where pages are whole multiples of 16 tokens: boxes of 16
+    // tokens, or of all that the warp takes, by 128 bytes, and their scales, which the copy engine brings while the warp computes (their issue by
+    // one lane takes 300 to 700 cycles a tile; scales by the lanes 100 more: 8 sequences of 65536, D 64, E4M3: 100 us, so 95). Else 16 bytes a lane and instruction, each lane with the rows of
     // its own token's page: their issue keeps the warp from computing, 700 cycles a tile and more the more of them are under way, but
     // boxes as small as odd pages allow take longer. (8 sequences of 65536, bf16: 271 us by boxes, 288 by lanes; 32 of 8192,
     // pages of one token: 248 by boxes of one, 136 by lanes.)
