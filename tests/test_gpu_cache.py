@@ -380,6 +380,24 @@ def test_attention_of_a_part_of_each_row(fmt, dtype, P):
     ref.check(sgq.paged_attention(dq.expand(3, -1, -1), dk, dv, dt, dn, fmt=fmt, k_scale=dks, v_scale=dvs).cpu(), want, tol)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("P", [16, 64])
+def test_attention_scales_on_any_4_bytes(dtype, P):
+    """Scales that no 16-byte copy can bring, of k, of v or of both."""
+    lengths = [200, 0, 77, 64]
+    table, pages = ref.table_of(lengths, P)
+    k, v, ks, vs = ref.pool("per_token", pages, 2, P, 80, dtype, 0)
+    q = torch.randn(4, 6, 80, generator=ref.gen(0)).to(dtype)
+    n = torch.tensor(lengths, dtype=torch.int32)
+    want, tol, _, _ = ref.attention(q, k, v, ks, vs, table, n)
+    dq, dk, dv, dt, dn = cuda(q, k, v, table, n)
+    for at_k, at_v in ((1, 0), (0, 3), (2, 2)):
+        sk, sv = (torch.full((s.numel() + 4,), math.nan, device=DEV) for s in (ks, vs))
+        sk, sv = sk[at_k:at_k + ks.numel()].view(ks.shape), sv[at_v:at_v + vs.numel()].view(vs.shape)
+        sk.copy_(ks), sv.copy_(vs)
+        ref.check(sgq.paged_attention(dq, dk, dv, dt, dn, fmt="per_token", k_scale=sk, v_scale=sv).cpu(), want, tol)
+
+
 @pytest.mark.parametrize("fmt,dtype", KINDS)
 @pytest.mark.parametrize("heads", [1, 3])
 @pytest.mark.parametrize("sinks", [False, True])
