@@ -75,6 +75,7 @@ struct WriteArgs {
     int wide;            // 64-bit slots
     int64_t T;
     int per;             // threads a token
+    int ahead;           // whether q's rows are asked for before the angles
     int D;
 };
 

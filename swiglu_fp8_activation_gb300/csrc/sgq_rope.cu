@@ -28,11 +28,11 @@ __device__ __forceinline__ uint4 ld16(const void* p) {
 }
 
 // LPR lanes a row, 16 values a lane; a.per threads (a multiple of a warp) work on one token, its heads one after the other.
-// Registers bound it: nine CTAs of 128 threads a multiprocessor (56 registers, a few spilled) against eight and ten: 8192 tokens, 32 heads
-// of 128 and 8 of k and v, bf16: 33.2 us (201 MB, 6065 GB/s), 34.0 and 34.3; E4M3: 33.5, 34.3 and 33.5; 40 heads of 16384 tokens turned:
-// 54.5 (336 MB, 6156 GB/s), 55.5 and 55.2. Reads of the next row held in registers cost more warps than they gain: 65.
+// Eight CTAs of 128 threads a multiprocessor: nine (56 registers, a few spilled) are better at large sizes without rows asked for ahead (33.3 us for
+// 34.0: 8192 tokens, 32 heads of 128 and 8 of k and v, E4M3) but not with them (31.2 for 30.0, 168 MB, 6170 GB/s), nor at small ones (2048 tokens: 8.9
+// for 7.7). Reads of the next row held in registers cost more warps than they gain (40 heads of 16384 tokens turned: 65 us for 55).
 template <int FMT, int DT, bool INTERLEAVED, int LPR>
-__global__ void __launch_bounds__(kThreads, 9) cache_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) cache_write_kernel(const WriteArgs a) {
     extern __shared__ float2 turn[];     // [tokens][8][pairs / 8]: factor * (cos, sin), a lane's 8 pairs a row apart (no bank twice)
     pdl_wait();
     pdl_trigger();
@@ -54,6 +54,12 @@ __global__ void __launch_bounds__(kThreads, 9) cache_write_kernel(const WriteArg
         if (second_on) w = ld16(p + apart);
     };
     const int apart = (c1 - c0) * 8;
+
+    // Rows that L2 does not hold: q's are on their way to it while the angles are computed.
+    if (a.ahead && live && (lane & 3) == 0 && lane * 16 < a.D) {
+        const uint16_t* x = a.q.p + t * a.q.ts + first * a.q.hs + lane * 16;
+        for (int h = first; h < a.q.n; h += heads, x += heads * a.q.hs) asm volatile("prefetch.global.L2 [%0];" ::"l"(x) : "memory");
+    }
 
     for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
         const int at = i / half;
@@ -177,6 +183,9 @@ cudaError_t launch_cache_write(int fmt, int dt, bool interleaved, const Device& 
         if (a.T < 2 * (int64_t)sms) split = (most + a.per / lpr - 1) / (a.per / lpr);
     }
     const int tokens = kThreads / a.per;
+    // Rows are asked for ahead where what is read and written passes L2 by (128 MB). 8192 tokens, 32 heads of 128 and 8 of k and v: bf16 31.5 us, else
+    // 33.8, E4M3 30.0 and 34.0; 40 heads of 16384 tokens turned: 50.2 and 54.6; but in L2, 2048 tokens, E4M3: 8.0 and 7.7; k and v too: 30.3 and 50.3.
+    a.ahead = a.T * (a.q.n + 2 * (int64_t)a.k.n) * a.D * 4 > (int64_t)128 << 20;
     const int64_t ctas = (a.T + tokens - 1) / tokens;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const int smem = tokens * a.rope.half * (int)sizeof(float2);

@@ -526,6 +526,35 @@ def test_attention_beyond_32_bit_offsets(fmt):
 
 # ------------------------------------------------------------------ calls
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rows_that_pass_l2_by(layout):
+    """Large calls ask for rows ahead: the same rows as in pieces."""
+    T, Hq, H, D = 7001, 32, 4, 128
+    r = torch.Generator(device=DEV).manual_seed(0)
+    qkv = torch.randn(T, Hq + 2 * H, D, generator=r, device=DEV).to(BF16)
+    assert 2 * qkv.numel() * 2 > 128 << 20
+    slots = torch.randperm(T, generator=r, device=DEV)
+    positions = torch.randint(0, 1 << 30, (T,), generator=r, device=DEV)
+    freqs = ref.turns(64).to(DEV)
+    pieces = [slice(0, 1), slice(1, 2048), slice(2048, 5000), slice(5000, T)]
+    whole = sgq.rope(qkv, positions, freqs, layout=layout)
+    assert torch.equal(whole, torch.cat([sgq.rope(qkv[p], positions[p], freqs, layout=layout) for p in pieces]))
+    for fmt in ("none", "per_token"):
+        def cache():
+            k, v = (torch.zeros(T // 16 + 1, H, 16, D, dtype=BF16 if fmt == "none" else torch.uint8, device=DEV) for _ in range(2))
+            ks, vs = (None, None) if fmt == "none" else torch.zeros(2, *k.shape[:3], device=DEV)
+            return k, v, ks, vs
+
+        def put(c, p):
+            d = qkv[p]
+            return sgq.cache_write(d[:, Hq:Hq + H], d[:, Hq + H:], c[0], c[1], slots[p], fmt=fmt, k_scale=c[2], v_scale=c[3], q=d[:, :Hq],
+                                   positions=positions[p], freqs=freqs, layout=layout)
+        one, many = cache(), cache()
+        q = put(one, slice(0, T))
+        assert torch.equal(q, torch.cat([put(many, p) for p in pieces])) and torch.equal(q, whole[:, :Hq])
+        assert all(a is None or torch.equal(a, b) for a, b in zip(one, many))
+
+
 def test_calls_of_no_rows():
     k, v, _, _ = ref.pool("none", 2, 2, 16, 64, BF16, 0)
     dk, dv = cuda(k, v)
