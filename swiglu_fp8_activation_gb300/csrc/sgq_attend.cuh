@@ -37,6 +37,12 @@
 #include "sgq_cache.cuh"
 #include "sgq_tc.cuh"
 
+// A test that makes a wait run out says here which copies come late or not at all, and how long waits are.
+#ifndef SGQ_ATTEND_COPIES
+#define SGQ_ATTEND_COPIES(item, part, tile) true
+#define SGQ_ATTEND_WAIT sgq::tc::kWaitCycles
+#endif
+
 namespace sgq {
 namespace attend {
 
@@ -406,6 +412,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     };
     // Copies w's tile into a slot; pid: page_of(w), asked for a tile before. Masked rows of a box come with it.
     auto copy = [&](const W& w, int slot, int pid) {
+        if (!SGQ_ATTEND_COPIES(w.b * a.items + w.j, part, w.tile)) return;
         const uint32_t at = base + slot * S::step, bar = bar_at(slot);
         const int t = token_of(w);
         const bool there = pid >= 0 && pid < a.c.pages;
@@ -814,7 +821,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     bool fresh = true, begun_here = cu.tile == 0;                // the item's first tile here; whether it is the item's first
     for (int turn = 0; todo > 0; ++turn) {
         if (turn >= a.stages) {
-            tc::bar_wait(bar_at(slot), parity, stop);
+            tc::bar_wait(bar_at(slot), parity, stop, SGQ_ATTEND_WAIT);
             __syncwarp();
             if (fresh) {
                 ready_q();
@@ -866,12 +873,14 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             parity ^= 1;
         }
     }
-    if (*stop) {
+    // All warps have made their last wait here, and take one way: a CTA in which one of them ran out of time, and another was done
+    // before, would else part at the barriers behind.
+    if (__syncthreads_or((int)*stop)) {
         // Out of time: what was computed since is no result. The last copies get as long again, so that none lands behind this CTA's end.
         uint32_t none = 0;
         if (copies)
             for (int s = 0; s < a.stages; ++s)
-                for (uint32_t p = 0; p < 2; ++p) tc::bar_wait(bar_at(s), p, &none);
+                for (uint32_t p = 0; p < 2; ++p) tc::bar_wait(bar_at(s), p, &none, SGQ_ATTEND_WAIT);
         __syncthreads();
         if (threadIdx.x == 0) atomicAdd(&gave_up, 1);
     }

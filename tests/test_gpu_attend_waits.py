@@ -1,0 +1,100 @@
+"""paged_attention where a wait runs out of time: the launch ends, is counted, and leaves what it has no part in as it
+should be. A build of the same kernels whose waits are limited to milliseconds and in which one copy is never issued
+(tests/cuda/attend_wait_check.cu), so that a barrier's phase stays open; nothing faults and nothing waits without a limit."""
+import ctypes as C
+import os
+import subprocess
+
+import pytest
+import torch
+
+import cache_ref as ref
+import swiglu_fp8_activation_gb300 as sgq
+from swiglu_fp8_activation_gb300 import cache
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+DEV = torch.device("cuda:0")
+BF16 = torch.bfloat16
+HEADS, D = 2, 64
+NEVER, LATE = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib(sgq_lib):
+    import __graft_entry__ as g
+    out = os.path.join(ROOT, "_build", "libattend_wait_check.so")
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    src = [os.path.join(ROOT, "tests", "cuda", "attend_wait_check.cu"), os.path.join(g.CSRC, "sgq_cache_api.cu")]
+    cmd = [g._nvcc(), *g.ARCH, "-O3", "-std=c++17", "-shared", "-cudart", "shared", "-Xcompiler", "-fPIC", "-I", g.CSRC, "-I", os.path.join(ROOT, "include"),
+           "-Xlinker", "-Bsymbolic", "-Xlinker", f"-rpath={g._cuda_lib_dir(g._nvcc())}", "-o", out, *src, os.path.join(g.PKG, "libsgq.so")]
+    subprocess.run(cmd, check=True)
+    L = C.CDLL(out)
+    L.paged_attention.restype, L.paged_attention.argtypes = C.c_int, cache._lib().paged_attention.argtypes
+    L.check_limit.restype = C.c_longlong
+    L.check_choose.argtypes = [C.c_int] * 4 + [C.c_longlong]
+    return L
+
+
+def gave_up(lib):
+    n = C.c_uint32(0)
+    assert lib.check_gave_up(C.byref(n)) == 0
+    return n.value
+
+
+class Case:
+    """Sequences of these lengths and a call of the build with short waits over them."""
+
+    def __init__(self, lib, fmt, lengths, group, P, shares):
+        self.lib, self.lengths, self.group = lib, lengths, group
+        table, pages = ref.table_of(lengths, P)
+        k, v, ks, vs = ref.pool(fmt, pages, HEADS, P, D, BF16, 0)
+        q = torch.randn(len(lengths), HEADS * group, D, generator=ref.gen(1)).to(BF16)
+        if shares:
+            table = torch.nn.functional.pad(table, (0, -(-60000 // P)), value=-1)
+        n = torch.tensor(lengths, dtype=torch.int32)
+        self.q, self.k, self.v, self.ks, self.vs, self.table, self.n = (None if t is None else t.to(DEV) for t in (q, k, v, ks, vs, table, n))
+        self.room = sgq.attention_workspace_bytes(fmt, len(lengths), HEADS * group, HEADS, D, table.shape[1], P)
+        assert (self.room > 0) == shares
+        self.code = cache.CACHE_FORMATS[fmt]
+        self.cache = cache._cache(self.k, self.v, fmt, self.ks, self.vs, BF16)[0]
+        self.plain = sgq.paged_attention(self.q, self.k, self.v, self.table, self.n, fmt=fmt, k_scale=self.ks, v_scale=self.vs)
+
+    def run(self, mode=0, item=0, part=0, tile=0, cycles=0):
+        assert self.lib.check_choose(mode, item, part, tile, cycles) == 0
+        out = torch.zeros_like(self.q)
+        ws = torch.empty(max(self.room, 16), dtype=torch.uint8, device=DEV)
+        at = torch.cuda.current_stream().cuda_stream
+        torch.cuda.synchronize()
+        st = self.lib.paged_attention(self.code, 0, len(self.lengths), self.cache, cache._heads(self.q, BF16, "q", self.q.shape), self.table.data_ptr(), self.table.shape[1],
+                                      self.n.data_ptr(), D ** -0.5, 0, None, out.data_ptr(), None, ws.data_ptr() if self.room else None, at)
+        assert st == 0
+        torch.cuda.synchronize()
+        return out
+
+
+FORMS = [([60, 0, 64], False), ([500, 130, 64], False), ([2000, 0, 900, 1], False), ([3000, 129, 0, 700], True)]
+
+
+@pytest.mark.parametrize("fmt,P", [("none", 16), ("none", 5), ("per_token", 16), ("per_token", 5)])
+@pytest.mark.parametrize("lengths,shares", FORMS)
+def test_a_copy_that_is_never_issued(lib, fmt, P, lengths, shares):
+    """One part of a CTA's warps waits in vain, in its first tile, a later or the last, while the others are done: the launch ends, the CTA is
+    counted once, items of other CTAs are right, and so is the next launch."""
+    case = Case(lib, fmt, lengths, 4, P, shares)
+    tokens = 128 if fmt == "per_token" else 64
+    before = gave_up(lib)
+    assert torch.equal(case.run(), case.plain) and gave_up(lib) == before
+    for seq, head in ((0, 1), (2 if lengths[2] else 3, 0)):
+        tiles = -(-lengths[seq] // tokens)
+        for tile in sorted({0, tiles // 2, tiles - 1}):
+            for part in range(4):
+                count = gave_up(lib)
+                out = case.run(NEVER, seq * HEADS + head, part, tile)
+                assert gave_up(lib) == count + 1, (seq, tile, part)
+                if not shares:
+                    others = torch.ones(out.shape[:2], dtype=torch.bool)
+                    others[seq, head * 4:head * 4 + 4] = False
+                    assert torch.equal(out[others], case.plain[others]), (seq, tile, part)
+    count = gave_up(lib)
+    assert torch.equal(case.run(), case.plain) and gave_up(lib) == count
