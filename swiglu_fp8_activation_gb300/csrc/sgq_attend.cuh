@@ -542,15 +542,16 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         constexpr int H = S::halves;
         const uint32_t at = base + slot * S::step, vt = at + S::half, sc = kF8 ? scales_at(slot) : 0;
         const uint32_t mask = s_mask[part][slot];
-        if (mask != S::full) {                       // what masked rows of v hold, and their scales, is multiplied by 0: it has to be a number
-            if (kF8 && cg == 0 && lane < S::rows && !((mask >> lane) & 1)) sts_f32(sc + (S::rows + lane) * 4, 0.0f);
-            if (cg == 0)
-                for (int i = lane; i < S::half / 16; i += 32) {
-                    const int r = i * 16 / S::block % S::rows;
-                    if (!((mask >> r) & 1)) sts16(vt + i * 16, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-                }
+        // What masked rows of v hold, and their scales, is multiplied by 0: it has to be a number. Each warp of the part writes the zeros that it
+        // reads, so that no barrier hangs on the mask: where a wait ran out, the part's warps may have seen unlike ones.
+        if (mask != S::full) {
+            if (kF8 && lane < S::rows && !((mask >> lane) & 1)) sts_f32(sc + (S::rows + lane) * 4, 0.0f);
+            for (int i = lane; i < S::half / 16; i += 32) {
+                const int r = i * 16 / S::block % S::rows;
+                if (!((mask >> r) & 1)) sts16(vt + i * 16, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            }
             tc::fence_async_smem();                  // before the copies that come here next
-            group_sync();
+            __syncwarp();
         }
         // S, in two chains of products a tile of 16 by 8
         float x[H][NT][4];

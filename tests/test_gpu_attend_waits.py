@@ -98,3 +98,23 @@ def test_a_copy_that_is_never_issued(lib, fmt, P, lengths, shares):
                     assert torch.equal(out[others], case.plain[others]), (seq, tile, part)
     count = gave_up(lib)
     assert torch.equal(case.run(), case.plain) and gave_up(lib) == count
+
+
+@pytest.mark.parametrize("P", [16, 5])
+@pytest.mark.parametrize("lengths,shares", FORMS)
+@pytest.mark.parametrize("mode", [NEVER, LATE])
+def test_warps_that_share_a_part_of_the_tokens(lib, P, lengths, shares, mode):
+    """Groups of 32 heads: two warps take a part's tokens, and one of them may have waited in vain for rows that the other
+    sees landed, whether the tile has masked rows or not. (A late copy of one of a CTA's first tiles, that is: later ones keep both from going on.)"""
+    case = Case(lib, "none", lengths, 32, P, shares)
+    before = gave_up(lib)
+    assert torch.equal(case.run(), case.plain) and gave_up(lib) == before
+    tiles = -(-lengths[0] // 64)
+    for tile in sorted({0, tiles // 2, tiles - 1}):
+        for part in range(4):
+            count = gave_up(lib)
+            out = case.run(mode, 1, part, tile, lib.check_limit() * 3 // 2)
+            more = gave_up(lib) - count
+            assert more == 1 or (mode == LATE and tile > 0 and more == 0 and torch.equal(out, case.plain)), (tile, part)
+    count = gave_up(lib)
+    assert torch.equal(case.run(), case.plain) and gave_up(lib) == count
