@@ -818,11 +818,12 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     const bool copies = cg == 0;
     uint32_t parity = 1;                                         // of the slots' barriers: 0 the first time round
     // a tile's pages are asked for a tile before its copy; where all tiles are one item's, two
-    int pid = copies && left > 0 ? page_of(ld) : -1, pid2 = DIRECT && copies && left > 1 ? page_of(ld, 1) : -1, todo = count, slot = 0;
+    int pid = copies && left > 0 ? page_of(ld) : -1, pid2 = DIRECT && copies && left > 1 ? page_of(ld, 1) : -1, todo = count, slot = 0, issued = 0;
     bool fresh = true, begun_here = cu.tile == 0;                // the item's first tile here; whether it is the item's first
     for (int turn = 0; todo > 0; ++turn) {
         if (turn >= a.stages) {
-            tc::bar_wait(bar_at(slot), parity, stop, SGQ_ATTEND_WAIT);
+            // (once one has run out the others do not begin)
+            if (!tc::bar_test(bar_at(slot), parity) && !*stop) tc::bar_wait(bar_at(slot), parity, stop, SGQ_ATTEND_WAIT);
             __syncwarp();
             if (fresh) {
                 ready_q();
@@ -857,8 +858,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             }
             group_sync();
         }
-        if (copies && left > 0 && !*stop) {
+        if (copies && left > 0 && !__any_sync(0xFFFFFFFFu, *stop)) {
             copy(ld, slot, pid);
+            ++issued;
             left -= !DIRECT && ld.tile + 1 == ld.tiles ? 1 + kEnd : 1;
             if (left > 0) {
                 advance(ld, true);
@@ -877,11 +879,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
     // All warps have made their last wait here, and take one way: a CTA in which one of them ran out of time, and another was done
     // before, would else part at the barriers behind.
     if (__syncthreads_or((int)*stop)) {
-        // Out of time: what was computed since is no result. The last copies get as long again, so that none lands behind this CTA's end.
+        // Out of time: what was computed since is no result. The last copies get as long again, so that none lands behind this CTA's
+        // end: the i-th went to slot i % stages, in that slot's phase i / stages. (Other phases may never end.)
         uint32_t none = 0;
         if (copies)
-            for (int s = 0; s < a.stages; ++s)
-                for (uint32_t p = 0; p < 2; ++p) tc::bar_wait(bar_at(s), p, &none, SGQ_ATTEND_WAIT);
+            for (int i = max(0, issued - a.stages); i < issued; ++i) tc::bar_wait(bar_at(i % a.stages), (i / a.stages) & 1, &none, SGQ_ATTEND_WAIT);
         __syncthreads();
         if (threadIdx.x == 0) atomicAdd(&gave_up, 1);
     }

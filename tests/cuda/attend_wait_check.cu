@@ -23,6 +23,12 @@ __device__ bool issued(int item, int part, int tile) {
     return true;
 }
 
+__global__ void spin(long long cycles) {
+    const long long start = clock64();
+    while (clock64() - start < cycles) {
+    }
+}
+
 }  // namespace
 
 #define SGQ_ATTEND_COPIES(item, part, tile) issued(item, part, tile)
@@ -46,6 +52,12 @@ extern "C" long long check_limit() { return SGQ_ATTEND_WAIT; }
 extern "C" int check_choose(int mode, int item, int part, int tile, long long cycles) {
     const Copy c = {mode, item, part, tile, cycles};
     return (int)cudaMemcpyToSymbol(chosen, &c, sizeof c);
+}
+
+// A kernel that takes so many cycles.
+extern "C" int check_spin(long long cycles, cudaStream_t stream) {
+    spin<<<1, 1, 0, stream>>>(cycles);
+    return (int)cudaGetLastError();
 }
 
 extern "C" int check_gave_up(uint32_t* n) { return (int)sgq::attend::read_gave_up(n); }

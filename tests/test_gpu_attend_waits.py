@@ -10,7 +10,7 @@ import torch
 
 import cache_ref as ref
 import swiglu_fp8_activation_gb300 as sgq
-from swiglu_fp8_activation_gb300 import cache
+from swiglu_fp8_activation_gb300 import binding, cache
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -33,6 +33,7 @@ def lib(sgq_lib):
     L.paged_attention.restype, L.paged_attention.argtypes = C.c_int, cache._lib().paged_attention.argtypes
     L.check_limit.restype = C.c_longlong
     L.check_choose.argtypes = [C.c_int] * 4 + [C.c_longlong]
+    L.check_spin.argtypes = [C.c_longlong, C.c_void_p]
     return L
 
 
@@ -66,11 +67,25 @@ class Case:
         ws = torch.empty(max(self.room, 16), dtype=torch.uint8, device=DEV)
         at = torch.cuda.current_stream().cuda_stream
         torch.cuda.synchronize()
+        begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        begin.record()
         st = self.lib.paged_attention(self.code, 0, len(self.lengths), self.cache, cache._heads(self.q, BF16, "q", self.q.shape), self.table.data_ptr(), self.table.shape[1],
                                       self.n.data_ptr(), D ** -0.5, 0, None, out.data_ptr(), None, ws.data_ptr() if self.room else None, at)
         assert st == 0
+        end.record()
         torch.cuda.synchronize()
+        self.ms = begin.elapsed_time(end)
         return out
+
+
+def limits(lib, n):
+    """Milliseconds that n limits of a wait take now."""
+    begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    begin.record()
+    assert lib.check_spin(int(n * lib.check_limit()), torch.cuda.current_stream().cuda_stream) == 0
+    end.record()
+    torch.cuda.synchronize()
+    return begin.elapsed_time(end)
 
 
 FORMS = [([60, 0, 64], False), ([500, 130, 64], False), ([2000, 0, 900, 1], False), ([3000, 129, 0, 700], True)]
@@ -118,3 +133,30 @@ def test_warps_that_share_a_part_of_the_tokens(lib, P, lengths, shares, mode):
             assert more == 1 or (mode == LATE and tile > 0 and more == 0 and torch.equal(out, case.plain)), (tile, part)
     count = gave_up(lib)
     assert torch.equal(case.run(), case.plain) and gave_up(lib) == count
+
+
+def test_the_last_copies_are_waited_for_and_no_others(lib):
+    """A copy that lands half a limit after a wait for it has run out: the launch ends then, and waits for no phase that no copy ends."""
+    for P in (16, 5):
+        case = Case(lib, "none", [500, 130], 32, P, False)
+        case.run()
+        count = gave_up(lib)
+        case.run(LATE, 1, 2, 0, lib.check_limit() * 3 // 2)
+        assert gave_up(lib) == count + 1
+        assert limits(lib, 1.4) < case.ms < limits(lib, 2.0)
+
+
+@pytest.mark.parametrize("fmt", ["none", "per_token"])
+def test_waits_end_soon_once_one_has_run_out(lib, fmt):
+    """One CTA has hundreds of tiles ahead of it when its first one does not come: two limits, for the tile and for its copy, and no more."""
+    binding.set_sm_budget(1)
+    try:
+        case = Case(lib, fmt, [60000], 8, 64, True)
+        case.run()
+        count = gave_up(lib)
+        case.run(NEVER, 0, 1, 0)
+        assert gave_up(lib) == count + 1
+        assert limits(lib, 1.9) < case.ms < limits(lib, 2.5)
+        assert torch.equal(case.run(), case.plain)
+    finally:
+        binding.set_sm_budget(0)
