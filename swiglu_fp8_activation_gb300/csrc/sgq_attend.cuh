@@ -53,6 +53,9 @@ constexpr int kEnd = kAttendEnd;
 constexpr int kStages = 8;                       // tiles copied ahead, at most (and 2 at least)
 constexpr float kNone = -3.0e38f;                // below every logit
 constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
+// Of a tile's p in a lane, which w does not bound where a row's scale is small or 0: a move leaves 2^102 of them at most, of which an
+// item's longest sum, 2^24 tiles of a lane, stays finite.
+constexpr float kMostSum = 0x1p103f;
 
 // Kinds of rows and queries.
 enum Kind : int { BF16 = 0, F16 = 1, FP8_BF16 = 2, FP8_F16 = 3 };
@@ -634,6 +637,10 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) over |= !(w[h][nt][i] <= kMost);
+        if (kF8) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) over |= !(fmaxf(s0[nt], s1[nt]) <= kMostSum);
+        }
         if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
