@@ -182,7 +182,8 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  * probabilities enter their product with v in two 16-bit parts, or in 11 bits (FP8
  * cache beside bf16); q beside an FP8 cache as 11 bits and an exponent a head, so that
  * a bf16 value under 2^-17 of the head's largest loses its last bits. A row's scale
- * in v_scale has to be 0 or between 2^-100 and 2^100.
+ * in v_scale has to be 0 or positive and at most 2^100; the sum counts rows alike,
+ * however far apart their scales are.
  *
  * Arguments:
  *   fmt, cache    as in cache_write; read

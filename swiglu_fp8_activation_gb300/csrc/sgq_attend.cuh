@@ -53,9 +53,10 @@ constexpr int kEnd = kAttendEnd;
 constexpr int kStages = 8;                       // tiles copied ahead, at most (and 2 at least)
 constexpr float kNone = -3.0e38f;                // below every logit
 constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
-// Of a tile's p in a lane, which w does not bound where a row's scale is small or 0: a move leaves 2^102 of them at most, of which an
-// item's longest sum, 2^24 tiles of a lane, stays finite.
-constexpr float kMostSum = 0x1p103f;
+// Of a tile's p in a lane, with E4M3 rows: w does not bound it where a row's scale is small or 0. An item's longest sum, 2^24 tiles of a lane, stays finite.
+constexpr float kMostSum = 0x1p40f;
+// The powers of two that w is divided by: of normal numbers, up and down; rows of zeros alone, which have no size, come to the least.
+constexpr float kLeastExp = -124.0f, kMostExp = 126.0f;
 
 // Kinds of rows and queries.
 enum Kind : int { BF16 = 0, F16 = 1, FP8_BF16 = 2, FP8_F16 = 3 };
@@ -178,11 +179,11 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
 }
 
-// floor(log2 s) of a scale, held inside +-100; zero and what is not finite included.
-__device__ __forceinline__ float scale_log(float s) {
-    const int e = (int)((__float_as_uint(s) >> 23) & 0xFF) - 127;
-    return (float)max(-100, min(100, e));
-}
+// floor(log2 s) of a scale; -127 for zero and what is subnormal, at most 127.
+__device__ __forceinline__ float exponent(float s) { return (float)min(127, (int)((__float_as_uint(s) >> 23) & 0xFF) - 127); }
+
+// 2^e of a whole e in [-126, 127].
+__device__ __forceinline__ float power(float e) { return __uint_as_float((uint32_t)(127 + (int)e) << 23); }
 
 // Walks over the tiles of a CTA's share, tiles of TOKENS each.
 template <int TOKENS>
@@ -530,12 +531,14 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
         }
     };
 
-    float o[kSteps][NT][4], ref[NT][2], sum[NT][2];
+    // sums of w v, and of p. down (E4M3 rows): w = p times the row's scale times down, so the sums of w v are 1 / down of what they stand for
+    float o[kSteps][NT][4], ref[NT][2], sum[NT][2], down[NT][2];
     auto clear = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             ref[nt][0] = ref[nt][1] = kNone;
             sum[nt][0] = sum[nt][1] = 0.0f;
+            down[nt][0] = down[nt][1] = 1.0f;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
         }
@@ -605,7 +608,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                     for (int i = 0; i < 4; ++i)
                         if (!((mask >> (h * 16 + g + 8 * (i >> 1))) & 1)) x[h][nt][i] = -INFINITY;
         }
-        // p, and w = p times the row's v scale. Where one is out of bounds (or no number) the reference moves.
+        // p, and w = p times the row's v scale, times the column's power of two. Where one is out of bounds (or no number) the reference moves to
+        // the largest logit, so that p is 1 at most, and the power to where the largest w is 1 to 2: they are two, since the scales may be
+        // as far apart as 32 bits allow, and the total counts every row the same whatever its scale.
         float vs[H][2], w[H][NT][4], s0[NT], s1[NT];
         bool over = false;
 #pragma unroll
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                     s1[nt] += w[h][nt][1] + w[h][nt][3];
                     if (kF8) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[h][nt][i] *= vs[h][i >> 1];
+                        for (int i = 0; i < 4; ++i) w[h][nt][i] = w[h][nt][i] * vs[h][i >> 1] * down[nt][i & 1];
                     }
                 }
             }
@@ -650,12 +655,28 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
 #pragma unroll
                     for (int h = 0; h < H; ++h)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) top = fmaxf(top, kF8 ? x[h][nt][2 * r + col] + scale_log(vs[h][r]) : x[h][nt][2 * r + col]);
+                        for (int r = 0; r < 2; ++r) top = fmaxf(top, x[h][nt][2 * r + col]);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    const float f = ex2_approx(ref[nt][col] - top);
+                    const float moved = ref[nt][col] - top;
                     ref[nt][col] = top;
-                    sum[nt][col] *= f;
+                    sum[nt][col] *= ex2_approx(moved);
+                    float f = moved;                             // of the sums of w v, log2
+                    if (kF8) {
+                        const float old = -exponent(down[nt][col]);              // log2 of what w is divided by
+                        float most = old + moved;
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (vs[h][r] != 0.0f) most = fmaxf(most, x[h][nt][2 * r + col] - top + exponent(vs[h][r]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+                        most = fminf(fmaxf(ceilf(most), kLeastExp), kMostExp);
+                        down[nt][col] = power(-most);
+                        f += old - most;
+                    }
+                    f = ex2_approx(f);
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
                         o[i][nt][col] *= f;
@@ -747,8 +768,21 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                 float l = sum[nt][col];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+                float m = ref[nt][col];
+                if (kF8) {
+                    // One reference again, the one at which the total is between 1 and 2 (0 where there is no token): the values' means
+                    // stay as far inside 32 bits as the rows are, and sums of some thousands of warps too.
+                    const float e = l > 0.0f ? exponent(l) : 0.0f, less = power(-e), up = power(-exponent(down[nt][col]));
+                    m += e;
+                    l *= less;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        o[i][nt][col] = o[i][nt][col] * less * up;
+                        o[i][nt][2 + col] = o[i][nt][2 + col] * less * up;
+                    }
+                }
                 if (g == 0) {
-                    s_m[part][(cg * NT + nt) * 8 + 2 * c + col] = ref[nt][col];
+                    s_m[part][(cg * NT + nt) * 8 + 2 * c + col] = m;
                     s_l[part][(cg * NT + nt) * 8 + 2 * c + col] = l;
                 }
             }

@@ -68,3 +68,70 @@ def test_rows_of_zeros_at_logits_far_above_the_others(dtype):
         ref.check(lse, want, 2.0 ** -20 * want, form)
         assert (out.double().abs() <= 448 * math.exp(-84.0)).all(), form
 
+
+CUTS = [(2.0 ** -60, 2.0 ** 68), (0.0, 2.0 ** 40), (0.0, 2.0 ** 98), (2.0 ** -99, 2.0 ** 99), (2.0 ** 99, 2.0 ** -99), (2.0 ** 60, 0.0)]
+
+
+@pytest.mark.parametrize("first,then", CUTS)
+@pytest.mark.parametrize("order", ["cut", "tiles"])
+def test_totals_where_scales_lie_far_apart(first, then, order):
+    """Half of the rows, or every second tile of them, scaled by one and the others by the other, at logits that are alike: out and
+    lse count both."""
+    lengths = [700, 130, 300]
+    which = (lambda t: t < 300) if order == "cut" else (lambda t: t // 128 % 2 == 0)
+    table, k, v, ks, vs = rows(lengths, BF16, 2, lambda t: 1.0, lambda t: first if which(t) else then)
+    q = (torch.randn(3, HEADS * GROUP, D, generator=ref.gen(3)) * 0.2).to(BF16)
+    n = torch.tensor(lengths, dtype=torch.int32)
+    want, tol, wl, tl = ref.attention(q, k, v, ks, vs, table, n)
+    for form, out, lse in calls(q, k, v, ks, vs, table, n):
+        ref.check(lse, wl, tl, f"{form} lse")
+        ref.check(out, want, tol, form)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("small", [2.0 ** -120, 2.0 ** -100, 0.0])
+def test_totals_beside_rows_of_next_to_nothing(dtype, small):
+    """Rows whose scale is near the end of 32 bits, as cache_write leaves them, before ordinary ones."""
+    lengths = [700, 130, 300]
+    table, k, v, ks, vs = rows(lengths, dtype, 4, lambda t: 1.0, lambda t: small if t % 300 < 150 else 0.01)
+    q = torch.randn(3, HEADS * GROUP, D, generator=ref.gen(5)).to(dtype)
+    n = torch.tensor(lengths, dtype=torch.int32)
+    want, tol, wl, tl = ref.attention(q, k, v, ks, vs, table, n)
+    for form, out, lse in calls(q, k, v, ks, vs, table, n):
+        ref.check(lse, wl, tl, f"{form} lse")
+        ref.check(out, want, tol, form)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -120, 2.0 ** -130, 2.0 ** -140])
+def test_rows_of_next_to_nothing_alone(scale):
+    """Down to subnormal scales: the answer is the rows' mean, to bf16's last step."""
+    lengths = [700, 130, 300]
+    table, k, v, ks, vs = rows(lengths, BF16, 6, lambda t: 1.0, lambda t: scale)
+    q = torch.randn(3, HEADS * GROUP, D, generator=ref.gen(7)).to(BF16)
+    n = torch.tensor(lengths, dtype=torch.int32)
+    want, tol, wl, tl = ref.attention(q, k, v, ks, vs, table, n)
+    for form, out, lse in calls(q, k, v, ks, vs, table, n):
+        ref.check(lse, wl, tl, f"{form} lse")
+        ref.check(out, want, tol, form)
+
+
+def test_small_rows_that_cache_write_leaves():
+    """Rows of v of every size down to bf16's subnormals, written and attended: scales as small as a subnormal number's."""
+    T = 400
+    r = ref.gen(8)
+    k = torch.randn(T, HEADS, D, generator=r).to(BF16)
+    v = (torch.randn(T, HEADS, D, generator=r) * torch.exp2(torch.linspace(-133, -90, T)).view(T, 1, 1)).to(BF16)
+    v[7] = 0
+    pages = -(-T // P)
+    kc, vc = torch.zeros(2, pages, HEADS, P, D, dtype=torch.uint8, device=DEV)
+    ks, vs = torch.zeros(2, pages, HEADS, P, device=DEV)
+    sgq.cache_write(k.to(DEV), v.to(DEV), kc, vc, torch.arange(T, device=DEV), fmt="per_token", k_scale=ks, v_scale=vs)
+    assert 0 < vs[vs > 0].min() < 2.0 ** -130
+    table, n = torch.arange(pages, dtype=torch.int32).view(1, -1), torch.tensor([T], dtype=torch.int32)
+    q = torch.randn(1, HEADS * GROUP, D, generator=r).to(BF16)
+    for some in (T, 40):                                                                 # with larger rows among them, and without
+        n[0] = some
+        want, tol, wl, tl = ref.attention(q, kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu(), table, n)
+        for form, out, lse in calls(q, kc, vc, ks, vs, table, n):
+            ref.check(lse, wl, tl, f"{form} lse")
+            ref.check(out, want, tol, form)
