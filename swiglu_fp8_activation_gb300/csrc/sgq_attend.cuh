@@ -30,7 +30,7 @@
 // summed, and in which the rows of V^T stand in their tiles, is free: both
 // follow what a lane's 16-byte reads bring, so no byte is moved twice.
 //
-// The running maximum is a reference that is moved only when a weight exceeds it 512
+// The running maximum is a reference that is moved only when a weight exceeds it some 512
 // times, so most tiles need no reduction over lanes and no rescaling.
 #pragma once
 
@@ -52,7 +52,6 @@ enum Joined : int { kByCta = 1, kByItem = 2 };
 constexpr int kEnd = kAttendEnd;
 constexpr int kStages = 8;                       // tiles copied ahead, at most (and 2 at least)
 constexpr float kNone = -3.0e38f;                // below every logit
-constexpr float kMost = 512.0f;                  // of w; moved to 1, a row's scale counted by its power of two
 // Of a tile's p in a lane, with E4M3 rows: w does not bound it where a row's scale is small or 0. An item's longest sum, 2^24 tiles of a lane, stays finite.
 constexpr float kMostSum = 0x1p40f;
 // The powers of two that w is divided by: of normal numbers, up and down; rows of zeros alone, which have no size, come to the least.
@@ -263,6 +262,11 @@ template <int KIND, int DP, int CG, int NT, bool DIRECT>
 __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shape<KIND, DP, CG, NT, DIRECT>::ctas) attend_kernel(const __grid_constant__ AttendArgs a) {
     using S = Shape<KIND, DP, CG, NT, DIRECT>;
     constexpr bool kF8 = S::fp8, kBf = KIND == BF16;
+    // A move of the reference leaves the largest w near 2^kRoom (rows' scales counted by their powers of two), and one above kMost is what moves
+    // it. fp16 ends at 2^-24, in both parts of p, and at 65504: with 6 weights down to 2^-30 of the largest are in the product (with 0
+    // those below 2^-25 were lost: 32768 tokens 17.5 nats under one that the same warps took came to 0), and moves are as rare as
+    // with 0 and 512; with 10 and 32768 they cost 61.9 us for 54.1 (32 sequences of 8192, groups of 16, E4M3). bf16 ends where 32 bits do.
+    constexpr float kRoom = kBf ? 0.0f : 6.0f, kMost = kBf ? 512.0f : 65504.0f;
     constexpr int kDt = KIND == BF16 || KIND == FP8_BF16 ? DT_BF16 : DT_F16;
     constexpr int kSteps = DP / 16, kCols = CG * NT * 8, kThreads = S::threads;
     extern __shared__ uint8_t raw[];
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                         if (!((mask >> (h * 16 + g + 8 * (i >> 1))) & 1)) x[h][nt][i] = -INFINITY;
         }
         // p, and w = p times the row's v scale, times the column's power of two. Where one is out of bounds (or no number) the reference moves to
-        // the largest logit, so that p is 1 at most, and the power to where the largest w is 1 to 2: they are two, since the scales may be
+        // the largest logit, so that p is 1 at most (16-bit rows: 2^room), and the power to where the largest w is 2^room: they are two, since the scales may be
         // as far apart as 32 bits allow, and the total counts every row the same whatever its scale.
         float vs[H][2], w[H][NT][4], s0[NT], s1[NT];
         bool over = false;
@@ -651,20 +655,21 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int col = 0; col < 2; ++col) {
-                    float top = ref[nt][col];
+                    float top = kF8 ? ref[nt][col] : ref[nt][col] + kRoom;
 #pragma unroll
                     for (int h = 0; h < H; ++h)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) top = fmaxf(top, x[h][nt][2 * r + col]);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    if (!kF8) top -= kRoom;
                     const float moved = ref[nt][col] - top;
                     ref[nt][col] = top;
                     sum[nt][col] *= ex2_approx(moved);
                     float f = moved;                             // of the sums of w v, log2
                     if (kF8) {
                         const float old = -exponent(down[nt][col]);              // log2 of what w is divided by
-                        float most = old + moved;
+                        float most = old + moved + kRoom;
 #pragma unroll
                         for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -672,7 +677,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP, CG, NT, DIRECT>::threads, Shap
                                 if (vs[h][r] != 0.0f) most = fmaxf(most, x[h][nt][2 * r + col] - top + exponent(vs[h][r]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-                        most = fminf(fmaxf(ceilf(most), kLeastExp), kMostExp);
+                        most = fminf(fmaxf(ceilf(most) - kRoom, kLeastExp), kMostExp);
                         down[nt][col] = power(-most);
                         f += old - most;
                     }
