@@ -202,17 +202,19 @@ struct Walk {
     }
 };
 
-// An item's result: sums of columns rel. to the reference m (log2), and their total.
+// An item's result: sums of columns rel. to the reference m (log2), and their total. A sink beside which the tokens weigh nothing is lse as it
+// is, at the ends of 32 bits too, where its base-2 logarithm would be infinite.
 __device__ __forceinline__ void finish(const AttendArgs& a, int b, int head, float m, float l, float& inv, float& lse) {
     constexpr float kLog2e = 1.44269504088896340736f;
     if (a.sinks) {
-        const float s = a.sinks[head] * kLog2e, M = fmaxf(m, s), f = ex2_approx(m - M);
-        l = l * f + ex2_approx(s - M);
-        inv = l > 0.0f ? f / l : 0.0f;
-        m = M;
-    } else {
-        inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float sink = a.sinks[head], log = sink * kLog2e, s = log > -kNone ? -kNone : log < kNone ? kNone : log;
+        const float M = fmaxf(m, s), f = ex2_approx(m - M), tokens = l * f;
+        l = tokens + ex2_approx(s - M);
+        inv = tokens == 0.0f ? 0.0f : f / l;
+        lse = tokens == 0.0f ? sink : (M + log2f(l)) * kLn2;
+        return;
     }
+    inv = l == 0.0f ? 0.0f : 1.0f / l;
     lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
