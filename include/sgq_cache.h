@@ -100,7 +100,8 @@ typedef struct sgq_rope {
 } sgq_rope_t;
 
 /*
- * Rotary positions on heads. Computed in fp32 (the angles in 64-bit integers), rounded once.
+ * Rotary positions on heads. Computed in fp32 (the angles in 64-bit integers, each
+ * rounded once to fp32), rounded once.
  *
  * Arguments:
  *   flags         SGQ_F_FP16, SGQ_F_ROPE_INTERLEAVED, SGQ_F_ROPE_INVERSE

@@ -11,8 +11,9 @@
 // The angles are a token's own, shared by all its heads: the CTA computes the
 // R/2 cosines and sines of each of its tokens once, into shared memory. A
 // frequency is a 64-bit fraction of a turn, so position * frequency wraps where
-// the angle does and keeps 2^-64 of a turn for every 1 in position; its upper 32 bits
-// are the angle.
+// the angle does and keeps 2^-64 of a turn for every 1 in position. The angle is that, rounded to
+// fp32: its upper 32 bits alone would leave a slow pair near the beginning, 2^-30 of a turn and less a position
+// in contexts stretched far, a sine of a few bits.
 #include "sgq_cache.cuh"
 
 namespace sgq {
@@ -66,9 +67,9 @@ __global__ void __launch_bounds__(kThreads, 8) cache_write_kernel(const WriteArg
         if (t0 + at >= a.T) break;
         const int pair = i - at * half;
         const uint64_t phase = (uint64_t)load_index(a.rope.positions, a.rope.wide, t0 + at) * a.rope.freqs[pair];
-        // half a turn is 1: sincospi's argument in [-1, 1)
+        // half a turn is 1: sincospi's argument in [-1, 1]
         float s, c;
-        sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+        sincospif((float)(int64_t)phase * 0x1p-63f, &s, &c);
         turn[at * half + (pair & 7) * (half >> 3) + (pair >> 3)] = make_float2(a.rope.factor * c, a.rope.factor * (a.rope.inverse ? -s : s));
     }
     __syncthreads();
