@@ -199,7 +199,7 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  *                 (width * page_size / 64 + 3) < 2^31
  *   lengths       [B] int32, read
  *   scale         finite
- *   window        >= 0; 0 for none
+ *   window        >= 0; 0 for none, as is any beyond the longest sequence
  *   sinks         [Hq] fp32, read, or NULL; -infinity is no sink
  *   out           [B, Hq, D], written, contiguous
  *   lse           [B, Hq] fp32, written, or NULL

@@ -33,6 +33,7 @@ MAX_HEAD = 256
 MAX_HEADS = 1024
 MAX_PAGE = 65536
 MAX_SEQUENCES = 65536
+MAX_WINDOW = (1 << 31) - 1      # no sequence is longer
 #: The cache's formats.
 CACHE_FORMATS = {"none": 3, "per_token": 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": F_ROPE_INTERLEAVED}
@@ -330,7 +331,7 @@ def attention_workspace_bytes(fmt: str, B: int, Hq: int, heads: int, D: int, wid
     """Bytes of paged_attention's workspace (0 where it needs none, or out of range)."""
     if fmt not in CACHE_FORMATS:
         raise SgqError(f"unknown cache format {fmt!r}")
-    return _workspace(_lib(), CACHE_FORMATS[fmt], B, Hq, heads, D, width, page_size, window)
+    return _workspace(_lib(), CACHE_FORMATS[fmt], B, Hq, heads, D, width, page_size, max(-1, min(window, MAX_WINDOW)))
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor, *,
@@ -370,6 +371,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _need(sinks, (Hq,), torch.float32, "sinks")
     if out is not None:
         _need(out, shape, dt, "out")
+    if not 0 <= window <= MAX_WINDOW:        # an argument of 64 bits would cut what they do not hold
+        if window < 0:
+            raise SgqError(f"window: expected 0 (none) or more, got {window}", 1)
+        window = MAX_WINDOW
     L = _lib()
     room = _workspace(L, code, B, Hq, heads, D, width, page_size, window)
     if workspace is not None:
