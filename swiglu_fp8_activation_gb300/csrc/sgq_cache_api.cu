@@ -156,8 +156,8 @@ struct AttendPlan {
 };
 
 bool plan_attend(int fmt, int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t width, int64_t page_size, int64_t window, AttendPlan* p) {
-    if (B < 1 || B > SGQ_MAX_SEQUENCES || heads < 1 || heads > SGQ_MAX_HEADS || Hq < heads || Hq > SGQ_MAX_HEADS || Hq % heads != 0 || D < 1 ||
-        D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size || window < 0)
+    if ((fmt != SGQ_FMT_16BIT && fmt != SGQ_FMT_FP8_PER_TOKEN) || B < 1 || B > SGQ_MAX_SEQUENCES || heads < 1 || heads > SGQ_MAX_HEADS || Hq < heads ||
+        Hq > SGQ_MAX_HEADS || Hq % heads != 0 || D < 1 || D % (fmt == SGQ_FMT_FP8_PER_TOKEN ? 16 : 8) != 0 || D > SGQ_MAX_HEAD || width < 0 || page_size < 1 || page_size > SGQ_MAX_PAGE || width > 0x7FFFFFFF / page_size || window < 0)
         return false;
     const int64_t group = Hq / heads;
     const bool fp8 = fmt == SGQ_FMT_FP8_PER_TOKEN;

@@ -1,4 +1,5 @@
-"""Windows of any size, without a GPU: one beyond every sequence is none, up to the largest number that the call takes and beyond it."""
+"""Windows of any size, without a GPU: one beyond every sequence is none, up to the largest number that the call takes and beyond it; and
+the workspace of calls that are refused."""
 import pytest
 import torch
 
@@ -26,3 +27,14 @@ def test_windows_no_64_bits_hold(sgq_lib):
         assert sgq.attention_workspace_bytes("none", 2, 8, 4, 64, 6250, 16, window) == 0
         with pytest.raises(sgq.SgqError, match="window"):
             sgq.paged_attention(q, c, c.clone(), table, n, window=window)
+
+
+def test_calls_that_are_refused_have_no_workspace(sgq_lib):
+    """Formats that a cache does not have, heads whose rows are no whole pieces."""
+    ws = cache._lib().sgq_attention_workspace_bytes
+    sizes = (2, 8, 4)
+    assert ws(3, *sizes, 72, 6250, 16, 0) > 0 and ws(2, *sizes, 80, 6250, 16, 0) > 0
+    for fmt in (-1, 0, 1, 4, 7):
+        assert ws(fmt, *sizes, 64, 6250, 16, 0) == 0
+    for fmt, D in ((3, 60), (3, 4), (3, 0), (2, 72), (2, 8), (3, 264), (2, 272)):
+        assert ws(fmt, *sizes, D, 6250, 16, 0) == 0
