@@ -116,6 +116,9 @@ struct AttendArgs {
     int boxes;           // tokens of the copy engine's boxes; 0 where lanes copy
 };
 
+// Pairs of times in the comments on paged_attention's rules, here and in sgq_attend.cuh, are of the two sides of a rule when it was made, the rest
+// alike; either side may have become faster since.
+
 // Most CTAs that take shares of one paged_attention, for which its workspace has room.
 constexpr int kAttendCtas = 512;
 
@@ -138,14 +141,16 @@ constexpr int kAttendEnd = 2;
 __host__ __device__ constexpr int attend_resident(bool fp8, int DP, int cols, bool direct) {
     return DP == 256 ? (fp8 && cols == 8 ? 2 : 1) : cols == 32 ? 1 : cols == 16 ? 2 : direct || DP == 64 ? 3 : 2;
 }
-// CTAs in clusters of `split` that surely run at once, n a multiprocessor: clusters do not fill the device's processor groups. (In clusters of
-// 8: 120, 288 and 408 with n of 1, 2 and 3; of 4: 144, 296 and 440.)
+// CTAs in clusters of `split` that surely run at once, n a multiprocessor: clusters do not fill the device's processor groups. (At most 120, 288
+// and 408 in clusters of 8 with n of 1, 2 and 3, and 144, 296 and 440 in clusters of 4, by the occupancy calculator; this gives 120, 272, 408 and 136, 288, 432.)
 constexpr int64_t attend_room(int64_t sms, int n, int split) { return n * sms - (split == 1 ? 0 : (n > 2 ? 6 : 4) * split); }
 // CTAs of a cluster, where each cluster takes one item; 0 where CTAs take shares of all items' tiles. A cluster needs no workspace
 // and no second launch; but it is 8 CTAs at most, and where long items are to be taken, or many sequences are empty, some multiprocessors
 // end long before others. The host knows the table's width alone: up to 8 tiles a CTA, or 1024 tokens where all CTAs run
 // at once. (Times in a graph, clusters and shares: 32 of 1024, 8 heads, bf16: 24.6 and 28.2 us; 24 of 2000, E4M3: 20.6 and 24.9; 1 of 4000, bf16: 11.1
 // and 9.4, but 5 us of the host's time less; 33 up to 5001, 3 heads, E4M3, 10 tiles a CTA: 24.1 and 19.7; 128 up to 8000, bf16, 16 tiles in 9 rounds: 318 and 283.)
+// The plan is for the 152 multiprocessors of the device, whatever sgq_set_sm_budget says: the workspace's size goes by it, and has to hold for
+// a call with another budget. The budget sets the CTAs that take shares.
 constexpr int attend_split(bool fp8, int DP, int64_t items, int64_t tiles, int cols) {
     const int n = attend_resident(fp8, DP, cols, true);
     int split = 1;

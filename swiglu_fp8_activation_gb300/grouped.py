@@ -233,10 +233,11 @@ def combine_rows(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | N
 
 
 def wait_timeouts() -> int:
-    """Launches of grouped_gemm, lora_add and paged_attention on the current device in
-    which a wait inside the kernel ran out of time (some seconds without progress). Such
-    a launch ends, its call having returned, and leaves its outputs unspecified:
-    this count is where it shows. Waits for the device; not during graph capture."""
+    """Launches of grouped_gemm and lora_add, and CTAs of paged_attention's launches, on the
+    current device in which a wait inside the kernel ran out of time (some seconds without
+    progress): a sign, 0 or not. Such a launch ends, its call having returned, and leaves its
+    outputs unspecified: this count is where it shows. Waits for the device; not during graph
+    capture."""
     n = C.c_uint32(0)
     _check(_lib().sgq_wait_timeouts(C.byref(n)), "sgq_wait_timeouts")
     return n.value
