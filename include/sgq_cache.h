@@ -179,7 +179,8 @@ int cache_read(int fmt, uint32_t flags, int64_t S, const sgq_kv_cache_t* cache, 
  * rows hold has no influence, and no page outside is read. Where nothing is left out[b] is zeros and lse the sink, or -infinity.
  *
  * Products in 16 bits by 16 bits, exact; sums, the softmax and its statistics in
- * fp32, exp2 to 2^-22 of its value (0 below 2^-126); FP8 codes enter as they are
+ * fp32, exp2 to 2^-22 of its value and 0 below 2^-126: a token 87 nats under the largest,
+ * or under the sink, counts as nothing, whatever its row's scale. FP8 codes enter as they are
  * and the rows' scales in fp32. The probabilities enter their product with v in two
  * 16-bit parts, or in 11 bits (FP8 cache beside bf16). Beside an FP8 or fp16 cache these
  * are fp16: a probability (with FP8, times its row's scale) is kept to 2^-30 of the largest

@@ -3,7 +3,8 @@ in the total.
 
 Tolerance. A weight enters its product as fp16 (bf16 beside a bf16 cache) in one or two parts. Where it is subnormal it is
 off by half of fp16's last step, 2^-25, and the largest weight that a warp has met is at 2^5 or above: so by 2^-30
-of the largest, here 1, for each token. The rest is the 2^-12 (or less) of each weight that its parts keep, 2^-18 of everything for logits of at most
+of the largest, here 1, for each token. The rest is what the parts lose of each weight, 2^-11 (one fp16 part: half of eps, 2^-10), 2^-21
+(two, of 2^-22) or 2^-17 (two of bf16, of 2^-18), 2^-18 of everything for logits of at most
 2^5 in 32 bits, exp2 and the sums of equal numbers, and the rounding of the result."""
 import math
 
@@ -45,7 +46,7 @@ def test_many_small_weights_behind_a_large_one(fmt, dtype, D, nats, n):
     many, few = float(n - len(high)), float(len(high))
     total = many * math.exp(-nats) + few
     want = torch.full((1, 1, D), many * math.exp(-nats) / total, dtype=torch.float64)
-    parts = {("none", BF16): 2.0 ** -17, ("none", F16): 2.0 ** -21, ("per_token", BF16): 2.0 ** -12, ("per_token", F16): 2.0 ** -21}[fmt, dtype]
+    parts = {("none", BF16): 2.0 ** -17, ("none", F16): 2.0 ** -21, ("per_token", BF16): 2.0 ** -11, ("per_token", F16): 2.0 ** -21}[fmt, dtype]
     floor = 0.0 if (fmt, dtype) == ("none", BF16) else 2.0 ** -30
     tol = want * (parts + 2.0 ** -18) + floor * many / total
     tol = tol + ref.rounding(want + tol, dtype)
